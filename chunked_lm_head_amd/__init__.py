@@ -642,3 +642,13 @@ def support_kl(H, W, ids, ref_logq, temperature: float = 0.0, row_temperature=No
                padded: bool = False):
     """KL(q || p_hat) per row over the candidates (KL-only entry)."""
     return ChunkedLMHeadSupportKL.apply(H, W, ids, ref_logq, temperature, row_temperature, padded)
+
+
+# ------------------------------------- around the projection (lmhead_decode.h)
+
+from .decode import (  # noqa: E402
+    DEVERR_LOGIT, DEVERR_SAMPLING, DTYPE_BF16, DTYPE_F32, FP8_BLOCK, NormOutputs, RMSNorm, lmhead_fp8_problem,
+    lmhead_logits_fp8, lmhead_logits_fp8_workspace_size, lmhead_norm, lmhead_quantize_fp8, lmhead_rms_norm_bwd,
+    lmhead_rms_norm_bwd_workspace_size, lmhead_rms_norm_fwd, lmhead_sample, lmhead_sample_problem,
+    lmhead_sample_workspace_size, logits_fp8, next_token, quantize_fp8, rms_norm, rms_norm_backward,
+    rms_norm_forward, rms_norm_quant, sample)

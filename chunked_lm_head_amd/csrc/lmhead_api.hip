@@ -14,8 +14,32 @@
 
 #include <hip/hip_runtime.h>
 
+#include "host_util.h"
 #include "lmhead.h"
 #include "lmhead_kernels.h"
+
+namespace lmhead {
+
+int check_device() {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return LMHEAD_ERR_DEVICE;
+    // 0 unknown, 1 gfx950, 2 other; atomic so that threads calling at once on
+    // different devices (or the same one) neither race nor tear
+    static std::atomic<int> cache[256];
+    if (dev < 256) {
+        const int known = cache[dev].load(std::memory_order_relaxed);
+        if (known != 0) return known == 1 ? LMHEAD_OK : LMHEAD_ERR_DEVICE;
+    }
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return LMHEAD_ERR_DEVICE;
+    const bool ok = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+    if (dev < 256) cache[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
+    return ok ? LMHEAD_OK : LMHEAD_ERR_DEVICE;
+}
+
+int launched() { return hipGetLastError() == hipSuccess ? LMHEAD_OK : LMHEAD_ERR_HIP; }
+
+}  // namespace lmhead
 
 namespace {
 
@@ -31,9 +55,6 @@ constexpr int64_t kMaxChunkPad = (int64_t(1) << 22) - 256;
 constexpr int64_t kMaxWorkItems = 0xffffffffLL;   // work-items in one launch
 // Most K slices of a chunk's dH contraction (bounds the fp32 partials)
 constexpr int kMaxDhSlices = 16;
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
 // Per-tile candidate buckets of the dense support entry (hit_count_kernel):
 // one set in the forward's regions and one in the backward's.
@@ -254,33 +275,12 @@ Layout plan(const lmhead_problem& p, int entry) {
     return L;
 }
 
-bool aligned(const void* ptr, uintptr_t a) { return ((uintptr_t)ptr % a) == 0; }
-
 Temperature temperature_of(const lmhead_problem& p) {
     Temperature T;
     T.t = p.temperature == 0.0f ? 1.0f : p.temperature;
     T.row = p.row_temperature;
     return T;
 }
-
-int check_device() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return LMHEAD_ERR_DEVICE;
-    // 0 unknown, 1 gfx950, 2 other; atomic so that threads calling at once on
-    // different devices (or the same one) neither race nor tear
-    static std::atomic<int> cache[256];
-    if (dev < 256) {
-        const int known = cache[dev].load(std::memory_order_relaxed);
-        if (known != 0) return known == 1 ? LMHEAD_OK : LMHEAD_ERR_DEVICE;
-    }
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return LMHEAD_ERR_DEVICE;
-    const bool ok = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    if (dev < 256) cache[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
-    return ok ? LMHEAD_OK : LMHEAD_ERR_DEVICE;
-}
-
-int launched() { return hipGetLastError() == hipSuccess ? LMHEAD_OK : LMHEAD_ERR_HIP; }
 
 // The dW and dH contractions of a chunk run as two launches, or as one when
 // that finishes sooner: a launch whose last round of 256 x 256 tiles leaves
@@ -382,12 +382,6 @@ int dh_slices(int64_t n, int64_t n_pad, int64_t hidden, int64_t w_pad) {
         }
     }
     return best;
-}
-
-int grid_1d(int64_t items, int per_block, int cap) {
-    int64_t g = cdiv(items, per_block);
-    if (g < 1) g = 1;
-    return (int)(g < cap ? g : cap);
 }
 
 void fill_u32(void* p, int64_t count, uint32_t value, hipStream_t s) {

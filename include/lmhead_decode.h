@@ -1,0 +1,233 @@
+/*
+ * lmhead_decode.h — the operators around the vocabulary projection when a
+ * model answers (and, for the norm, when it trains), in the same library as
+ * lmhead.h (liblmhead.so, gfx950):
+ *
+ *   lmhead_rms_norm_fwd / _bwd   the norm in front of the head, with the
+ *                                residual's addition; bf16 output and / or an
+ *                                8-bit output with scales;
+ *   lmhead_quantize_fp8          bf16 rows or a weight matrix to 8 bits with
+ *                                block scales;
+ *   lmhead_logits_fp8            logits from 8-bit rows and an 8-bit W;
+ *   lmhead_sample                one token per row from given random numbers,
+ *                                with the log-probability that lmhead_logprob
+ *                                gives for it.
+ *
+ * The conventions of lmhead.h hold for every entry: device pointers on the
+ * current HIP device, caller-owned buffers and workspace, no allocation, no
+ * synchronisation, all work on `stream`, host-checkable errors as a status
+ * before anything is enqueued, reductions in a fixed order (two calls with
+ * the same arguments give the same bits). n = 0 is a valid, empty call. An
+ * output may be the same buffer as an input only where an entry says so.
+ *
+ * 8-bit values are OCP e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest
+ * 448, no infinity), rounded to nearest even. A block scale is fp32: the value
+ * is q * scale. The scale of a block is its largest magnitude / 448, at least
+ * 2^-126 (1 for a block of zeros).
+ */
+#ifndef LMHEAD_DECODE_H
+#define LMHEAD_DECODE_H
+
+#include "lmhead.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+enum lmhead_dtype {
+    LMHEAD_DTYPE_BF16 = 0,
+    LMHEAD_DTYPE_F32 = 1
+};
+
+/* Further device error codes (bits, beside enum lmhead_device_error). */
+enum lmhead_decode_device_error {
+    LMHEAD_DEVERR_LOGIT = 8,    /* a logit that is NaN or +infinity */
+    LMHEAD_DEVERR_SAMPLING = 16 /* a u outside [0, 1), a top_p outside (0, 1] or a min_p outside [0, 1] */
+};
+
+/* ------------------------------------------------------------- RMS norm */
+
+/*
+ *   n              rows, 0 <= n <= 2^30.
+ *   hidden         a multiple of 64, 64 <= hidden <= 65536; with the 8-bit
+ *                  output a multiple of 128.
+ *   eps            finite, >= 0.
+ *   weight_offset  finite; the weight applied is weight_offset + weight (0, or
+ *                  1 for zero-centred weights).
+ *   weight_dtype   enum lmhead_dtype of weight and dweight.
+ *   reserved       must be 0.
+ */
+typedef struct lmhead_norm {
+    int64_t n;
+    int64_t hidden;
+    float eps;
+    float weight_offset;
+    int32_t weight_dtype;
+    int32_t reserved;
+} lmhead_norm;
+
+/*
+ * r = x + residual (fp32 sum, rounded to bf16: the residual stream), or x
+ * without a residual; rstd = 1 / sqrt(mean_j r_j^2 + eps);
+ * y_j = r_j rstd (weight_offset + weight_j), in fp32.
+ *   x, residual   device, bf16 [n, hidden]; residual may be NULL.
+ *   weight        device, [hidden], weight_dtype.
+ *   residual_out  device, bf16 [n, hidden] r, or NULL; needs residual. May be
+ *                 the buffer of x or of residual.
+ *   y             device, bf16 [n, hidden] or NULL. May be the buffer of x
+ *                 when residual_out is not.
+ *   q, scale      device, e4m3 [n, hidden] and fp32 [n, hidden / 128], or
+ *                 both NULL: y (before any rounding to bf16) in 8 bits with
+ *                 one scale per row and 128 columns.
+ *   rstd          device, fp32 [n] or NULL: what the backward needs.
+ * All pointers 16-byte aligned. At least one of y, q, rstd, residual_out.
+ */
+int lmhead_rms_norm_fwd(const lmhead_norm* p, const void* x, const void* residual, const void* weight,
+                        void* residual_out, void* y, void* q, float* scale, float* rstd, void* stream);
+
+/* Bytes of workspace lmhead_rms_norm_bwd needs for dweight (0 for an invalid
+ * problem): fp32 partial sums of dweight, at most 512 rows of them. */
+size_t lmhead_rms_norm_bwd_workspace_size(const lmhead_norm* p);
+
+/*
+ * Backward of y (bf16 output). With g_j = dy_j (weight_offset + weight_j) and
+ * x_j = r_j rstd:  dx_j = rstd (g_j - x_j mean_i(g_i x_i)) + dresidual_j,
+ * the gradient of x and of residual alike; dweight_j = sum_n dy_nj x_nj (fp32
+ * sums in a fixed order).
+ *   dy         device, bf16 [n, hidden].
+ *   r          device, bf16 [n, hidden]: the forward's residual_out (x where
+ *              it had no residual).
+ *   rstd       device, fp32 [n]: the forward's.
+ *   dresidual  device, bf16 [n, hidden] or NULL: the gradient that reaches
+ *              residual_out from its other uses.
+ *   dx         device, bf16 [n, hidden] or NULL. May be the buffer of dy or of
+ *              dresidual.
+ *   dweight    device, [hidden], weight_dtype, or NULL. n = 0 writes zeros.
+ *   workspace  256-byte aligned; may be NULL without dweight.
+ */
+int lmhead_rms_norm_bwd(const lmhead_norm* p, const void* dy, const void* r, const void* weight,
+                        const float* rstd, const void* dresidual, void* dx, void* dweight,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------ quantiser */
+
+/*
+ * x bf16 [rows, cols] to e4m3 with one scale per block.
+ *   rows        0 <= rows <= 2^30, cols a multiple of 128, <= 65536.
+ *   block_rows  1 (a scale per row and 128 columns: hidden states) or 128 (a
+ *               scale per 128 x 128 block: a weight matrix; the last block of
+ *               rows may hold fewer).
+ *   q           device, e4m3 [rows, cols].
+ *   scale       device, fp32 [ceil(rows / block_rows), cols / 128].
+ */
+int lmhead_quantize_fp8(int64_t rows, int64_t cols, int32_t block_rows, const void* x, void* q,
+                        float* scale, void* stream);
+
+/* --------------------------------------------------------------- logits */
+
+/*
+ *   n          rows, 0 <= n <= 2^24.
+ *   vocab      1 <= vocab <= 2^30.
+ *   hidden     a multiple of 128, 128 <= hidden <= 65536.
+ *   ld         elements between two rows of out, >= vocab.
+ *   out_dtype  enum lmhead_dtype of out.
+ *   reserved   must be 0.
+ *   ceil(n / 16) * ceil(vocab / 64) <= 16,777,215 (one launch).
+ */
+typedef struct lmhead_fp8_problem {
+    int64_t n;
+    int64_t vocab;
+    int64_t hidden;
+    int64_t ld;
+    int32_t out_dtype;
+    int32_t reserved;
+} lmhead_fp8_problem;
+
+/* Bytes of workspace lmhead_logits_fp8 needs (>= 256; 0 for an invalid problem). */
+size_t lmhead_logits_fp8_workspace_size(const lmhead_fp8_problem* p);
+
+/*
+ * out[i, v] = sum_b a_scale[i, b] w_scale[v / 128, b] sum_{j in block b}
+ * a[i, j] w[v, j], blocks of 128 columns, all sums in fp32 over ascending b.
+ *   a, a_scale  device, e4m3 [n, hidden], fp32 [n, hidden / 128]
+ *               (lmhead_rms_norm_fwd's q and scale, or lmhead_quantize_fp8's
+ *               with block_rows 1).
+ *   w, w_scale  device, e4m3 [vocab, hidden], fp32 [ceil(vocab / 128),
+ *               hidden / 128] (lmhead_quantize_fp8 with block_rows 128).
+ *   out         device, out_dtype [n, ld]; columns vocab .. ld - 1 are left
+ *               as they are.
+ */
+int lmhead_logits_fp8(const lmhead_fp8_problem* p, const void* a, const float* a_scale, const void* w,
+                      const float* w_scale, void* out, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* ------------------------------------------------------------- sampling */
+
+/*
+ *   n             rows, 0 <= n <= 2^30.
+ *   vocab         1 <= vocab <= 2^30.
+ *   ld            elements between two rows of logits, >= vocab.
+ *   logits_dtype  enum lmhead_dtype.
+ *   top_k         scalar; 0 = off.
+ *   temperature   scalar t; 0 = off (1). Finite, >= 0.
+ *   top_p         scalar in [0, 1]; 0 and 1 = off.
+ *   min_p         scalar in [0, 1]; 0 = off.
+ *   row_temperature, row_top_k, row_top_p, row_min_p   device [n] arrays or
+ *                 NULL. row_temperature multiplies the scalar, as in
+ *                 lmhead_problem (tau = t r, positive and finite); the others
+ *                 take the scalar's place: row_top_k <= 0 is off, row_top_p in
+ *                 (0, 1], row_min_p in [0, 1].
+ */
+typedef struct lmhead_sample_problem {
+    int64_t n;
+    int64_t vocab;
+    int64_t ld;
+    int32_t logits_dtype;
+    int32_t top_k;
+    float temperature;
+    float top_p;
+    float min_p;
+    int32_t reserved;
+    const float* row_temperature;
+    const int32_t* row_top_k;
+    const float* row_top_p;
+    const float* row_min_p;
+} lmhead_sample_problem;
+
+/* Bytes of workspace lmhead_sample needs (0 for an invalid problem). */
+size_t lmhead_sample_workspace_size(const lmhead_sample_problem* p);
+
+/*
+ * One token per row. With w_v = exp((x_v - max x) / tau) and the tokens in
+ * the order of descending logit, equal logits by ascending index:
+ *   1. top-k keeps the first k tokens;
+ *   2. top-p keeps, of those, the shortest prefix whose weight reaches
+ *      top_p times theirs (a token is kept when the weight before it is
+ *      below that; the first always is);
+ *   3. min-p keeps, of those, the tokens with w_v >= min_p;
+ *   4. the token is the lowest index v at which the kept weight of indices
+ *      0 .. v passes u times all kept weight.
+ * A logit of -infinity masks a token (never kept). Weights are held as
+ * integers of 2^-s, s = min(44, 62 - ceil(log2(vocab))), so every sum is
+ * exact and independent of its order; a token below half of that step
+ * beside the most likely one is never drawn.
+ *   logits    device, logits_dtype [n, ld], aligned to its elements (any ld).
+ *   u         device, fp32 [n], in [0, 1).
+ *   token     device, int32 [n].
+ *   logprob   device, fp32 [n] or NULL: (x_token - max x) / tau - log sum_v
+ *             w_v, over all unmasked tokens (lmhead_logprob's definition with
+ *             the same temperature, for any filter).
+ *   workspace 256-byte aligned; its error word as everywhere
+ *             (lmhead_read_device_error).
+ * A row whose tokens are all masked gives token -1 and logprob 0 (-1 is an
+ * ignored label everywhere in lmhead.h). A row with a data error gives
+ * token -1 and logprob NaN.
+ */
+int lmhead_sample(const lmhead_sample_problem* p, const void* logits, const float* u, int32_t* token,
+                  float* logprob, void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LMHEAD_DECODE_H */

@@ -1,0 +1,95 @@
+"""Logits from 8-bit operands against the 64-bit product of the values they
+stand for. Tolerance: products of e4m3 values are exact in fp32; a block's 128
+products and the blocks' sums are fp32 additions, each off by at most one step
+(2^-23, truncation allowed) of a partial sum that the sum of magnitudes bounds:
+(128 + blocks) 2^-23 sum |a w|. A bf16 output adds half a step, 2^-8."""
+import numpy as np
+import pytest
+import torch
+
+import chunked_lm_head_amd as lm
+import decode_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def operand(rows, cols, block_rows, rng):
+    q = torch.from_numpy(rng.standard_normal((rows, cols)).astype(np.float32) * 100).clamp(-448, 448)
+    q = q.to(torch.float8_e4m3fn).cuda()
+    s = torch.from_numpy(np.exp(rng.uniform(-3, 3, (-(-rows // block_rows), cols // 128))).astype(np.float32)).cuda()
+    return q, s
+
+
+def check(out, a, sa, w, sw):
+    A = f64(a) * ref.spread_scales(f64(sa), 1, a.shape[0])
+    B = f64(w) * ref.spread_scales(f64(sw), 128, w.shape[0])
+    z, size = A @ B.T, np.abs(A) @ np.abs(B).T
+    tol = (128 + a.shape[1] // 128) * 2.0 ** -23 * size
+    if out.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * 1.01 * np.abs(z)
+    bad = np.abs(f64(out) - z) > tol
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:5], np.abs(f64(out) - z).max())
+
+
+SHAPES = [(1, 1, 128), (1, 1000, 256), (3, 130, 384), (5, 16, 128), (15, 257, 512), (16, 128, 640), (17, 1000, 256),
+          (32, 63, 1152), (33, 2050, 128), (64, 512, 4096), (65, 300, 256), (100, 129, 1280), (128, 1000, 512),
+          (200, 700, 256), (257, 513, 384), (300, 1100, 2048), (513, 260, 128), (1030, 1030, 256)]
+
+
+@pytest.mark.parametrize("n,vocab,hidden", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_against_definition(n, vocab, hidden, dtype):
+    print(f"[logits] n={n} vocab={vocab} hidden={hidden} {dtype}", flush=True)
+    rng = np.random.default_rng(n * 7 + vocab + hidden)
+    a, sa = operand(n, hidden, 1, rng)
+    w, sw = operand(vocab, hidden, 128, rng)
+    out = lm.logits_fp8(a, sa, w, sw, out_dtype=dtype)
+    check(out, a, sa, w, sw)
+    assert torch.equal(out, lm.logits_fp8(a, sa, w, sw, out_dtype=dtype))
+
+
+@pytest.mark.parametrize("n", [2, 40, 150, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ld", [333, 335, 512])
+def test_row_stride_leaves_the_rest(n, dtype, ld):
+    rng = np.random.default_rng(5)
+    a, sa = operand(n, 256, 1, rng)
+    w, sw = operand(333, 256, 128, rng)
+    buf = torch.full((n + 1, ld), 7.0, dtype=dtype, device="cuda")
+    out = lm.logits_fp8(a, sa, w, sw, out=buf[:n, :333])
+    check(out, a, sa, w, sw)
+    assert (buf[:n, 333:] == 7.0).all() and (buf[n] == 7.0).all()
+
+
+def test_rows_do_not_touch_each_other():
+    """A row with NaN, and a W block with an infinite scale, stay where they are."""
+    rng = np.random.default_rng(6)
+    a, sa = operand(20, 256, 1, rng)
+    w, sw = operand(300, 256, 128, rng)
+    want = lm.logits_fp8(a, sa, w, sw, out_dtype=torch.float32)
+    sa2, sw2 = sa.clone(), sw.clone()
+    sa2[3, 1] = float("nan")
+    sw2[2, 0] = float("inf")
+    got = lm.logits_fp8(a, sa2, w, sw2, out_dtype=torch.float32)
+    assert got[3].isnan().all()
+    keep = torch.ones(20, dtype=torch.bool, device="cuda")
+    keep[3] = False
+    assert torch.equal(got[keep][:, :256], want[keep][:, :256])
+    assert not torch.isfinite(got[keep][:, 256:]).any()
+
+
+def test_empty_and_python_checks():
+    rng = np.random.default_rng(7)
+    a, sa = operand(4, 256, 1, rng)
+    w, sw = operand(300, 256, 128, rng)
+    assert lm.logits_fp8(a[:0], sa[:0], w, sw).shape == (0, 300)
+    for bad in (lambda: lm.logits_fp8(a, sa.double(), w, sw), lambda: lm.logits_fp8(a, sa[:, :1], w, sw),
+                lambda: lm.logits_fp8(a, sa, w, sw[:2]), lambda: lm.logits_fp8(a, sa, w, sw, out_dtype=torch.float16),
+                lambda: lm.logits_fp8(a.float(), sa, w, sw), lambda: lm.logits_fp8(a[:, :128], sa, w, sw),
+                lambda: lm.logits_fp8(a, sa, w, sw, out=torch.empty(300, 4, device="cuda").t())):
+        with pytest.raises(ValueError):
+            bad()

@@ -55,18 +55,12 @@ struct Frag {
 };
 struct Wide {
     bf16x8 p[4];
-    __device__ __forceinline__ Wide(const Frag& f) {
+    __device__ __forceinline__ void set(const Frag& f) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) p[s] = f.part(s);
     }
 };
 
-__device__ __forceinline__ floatx4 block_sum(const Wide& a, const Wide& b) {
-    floatx4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[s], b.p[s], z, 0, 0, 0);
-    return z;
-}
 __device__ __forceinline__ floatx4 block_sum(const i32x8& a, const i32x8& b) {
     const floatx4 z = {0.0f, 0.0f, 0.0f, 0.0f};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
@@ -74,102 +68,32 @@ __device__ __forceinline__ floatx4 block_sum(const i32x8& a, const i32x8& b) {
 
 // ------------------------------------------------------------- few rows
 
-constexpr int kStreamRows = 128;
-constexpr int kStreamWaves = 4;
+constexpr int kStreamRows = 64;
 
-__device__ __forceinline__ void store_out(const LogitsArgs& a, int64_t at, float v) {
-    if (a.out_f32)
-        reinterpret_cast<float*>(a.out)[at] = v;
-    else
-        reinterpret_cast<__bf16*>(a.out)[at] = (__bf16)v;
-}
-
-// One workgroup: VT * 16 vocabulary rows x all (NT * 16) input rows.
-template <int VT, int NT>
-__global__ __launch_bounds__(64 * kStreamWaves) void logits_stream_kernel(LogitsArgs a) {
-    constexpr int kV = 16 * VT, kN = 16 * NT, kPitch = kV + 4;
-    __shared__ __attribute__((aligned(16))) float part[kStreamWaves][kN][kPitch];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = lane & 15, g = lane >> 4;
-    const int64_t v0 = (int64_t)blockIdx.x * kV;
-    const int nb = a.hidden / kQBlock;
-    const int b0 = nb * wave / kStreamWaves, b1 = nb * (wave + 1) / kStreamWaves;
-    const uint8_t* w[VT];
-    const uint8_t* x[NT];
-    const float* sa[NT];
-#pragma unroll
-    for (int i = 0; i < VT; ++i) {
-        const int64_t r = v0 + 16 * i + c;
-        w[i] = a.w + (r < a.vocab ? r : a.vocab - 1) * a.hidden + 16 * g;
+// Four consecutive logits of a row per lane, `count` of them (<= 0: none)
+// inside the vocabulary: one store where the row pitch keeps them aligned.
+__device__ __forceinline__ void store4(const LogitsArgs& a, int64_t row, int64_t v, int count, const floatx4& x) {
+    if (row >= a.n || count <= 0) return;
+    const int64_t at = row * a.ld + v;
+    if (count >= 4 && (a.ld & 3) == 0) {
+        if (a.out_f32)
+            *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(a.out) + at) = x;
+        else
+            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_bits*>(a.out) + at) =
+                make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        return;
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int64_t r = 16 * j + c;
-        const int64_t rc = r < a.n ? r : a.n - 1;
-        x[j] = a.a + rc * a.hidden + 16 * g;
-        sa[j] = a.a_scale + rc * nb;
-    }
-    const float* sw = a.w_scale + (v0 / kQBlock) * nb;   // kV divides 128: one block of rows
-    floatx4 acc[VT][NT];
-#pragma unroll
-    for (int i = 0; i < VT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    Frag fw[VT];
-    auto load_w = [&](Frag (&f)[VT], int b) {
-#pragma unroll
-        for (int i = 0; i < VT; ++i) {
-            f[i].lo = *reinterpret_cast<const u32x4*>(w[i] + b * kQBlock);
-            f[i].hi = *reinterpret_cast<const u32x4*>(w[i] + b * kQBlock + 64);
+    for (int e = 0; e < 4; ++e)
+        if (e < count) {
+            if (a.out_f32)
+                reinterpret_cast<float*>(a.out)[at + e] = x[e];
+            else
+                reinterpret_cast<__bf16*>(a.out)[at + e] = (__bf16)x[e];
         }
-    };
-    if (b0 < b1) load_w(fw, b0);
-    for (int b = b0; b < b1; ++b) {
-        Frag nw[VT];
-        load_w(nw, b + 1 < b1 ? b + 1 : b);
-        const float s0 = sw[b];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            Frag fx;
-            fx.lo = *reinterpret_cast<const u32x4*>(x[j] + b * kQBlock);
-            fx.hi = *reinterpret_cast<const u32x4*>(x[j] + b * kQBlock + 64);
-            const float s = sa[j][b] * s0;
-            const Wide wx(fx);
-#pragma unroll
-            for (int i = 0; i < VT; ++i) {
-                const floatx4 z = block_sum(Wide(fw[i]), wx);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(z[e], s, acc[i][j][e]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < VT; ++i) fw[i] = nw[i];
-    }
-    // lane: vocabulary rows 16 i + 4 g .. + 4 of input row 16 j + c
-#pragma unroll
-    for (int i = 0; i < VT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<floatx4*>(&part[wave][16 * j + c][16 * i + 4 * g]) = acc[i][j];
-    __syncthreads();
-    const int rows = a.n < kN ? (int)a.n : kN;
-    for (int q = threadIdx.x; q < rows * kV; q += 64 * kStreamWaves) {
-        const int r = q / kV, v = q % kV;
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kStreamWaves; ++k) s += part[k][r][v];
-        if (v0 + v < a.vocab) store_out(a, r * a.ld + v0 + v, s);
-    }
 }
 
-template <int VT, int NT>
-void stream(const LogitsArgs& a, hipStream_t s) {
-    logits_stream_kernel<VT, NT><<<(unsigned)cdiv(a.vocab, 16 * VT), 64 * kStreamWaves, 0, s>>>(a);
-}
-
-// ------------------------------------------------------------- many rows
-
-// The rows packed for the tile kernel: 16-row x 128-column blocks of 2 KB in
+// The rows packed: 16-row x 128-column blocks of 2 KB in
 // fragment order (the lanes' low 16 bytes, then their high ones), block (i /
 // 16, b) at ((i / 16) nb + b) * 2 KB, rows up to n_pad zero; and the scales
 // transposed, [nb][n_pad].
@@ -192,6 +116,171 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const uint8_t* a, const 
         scale_t[q] = row < n ? a_scale[row * nb + b] : 0.0f;
     }
 }
+
+// Every wave takes its share of the vocabulary's 16-row groups, kStreamWaves of
+// them over the whole chip at once (eight per compute unit, all resident), VT
+// groups at a time over all columns and all (NT * 16) input rows: the shares
+// differ by one group at most, there is no last round that leaves units idle,
+// nothing to join, and the waves of a unit read the same rows' fragments at
+// about the same time. A wave's part of W goes through two steps of LDS of its
+// own: LDS-direct loads of whole 128-byte lines (a fragment loaded straight
+// from row-major W takes 16 bytes of 16 lines per 16 lanes), 16-byte chunk q of
+// row r at q ^ ((r >> 1) & 7) for conflict-free fragment reads. Only the wave's
+// own counters order it: no barrier. The input rows' fragments come from
+// the packed copy (PACKED), or from the rows themselves while they are at
+// most 16.
+constexpr int kStreamWaves = 2048;   // 256 compute units x 8
+constexpr int kStreamGroup = 8;      // waves per workgroup
+
+template <int VT, int NT, bool PACKED>
+__global__ __launch_bounds__(64 * kStreamGroup) void logits_stream_kernel(LogitsArgs a, const uint8_t* packed,
+                                                                         const float* scale_t, int n_pad) {
+    constexpr int kStage = 16 * VT * 128;
+    __shared__ __attribute__((aligned(16))) char smem[kStreamGroup * 2 * kStage];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int nb = a.hidden / kQBlock;
+    // Step k of a workgroup is column block (k + rot) mod nb. All waves read
+    // 128 bytes of many rows at a time; were they all at the same columns, the
+    // addresses would agree in their low bits and meet in a few memory
+    // channels (one row: 127 us so, 107 us rotated).
+    const int rot = (int)blockIdx.x % nb;
+    auto block_of = [&](int k) { return k + rot < nb ? k + rot : k + rot - nb; };
+    const int64_t groups = (a.vocab + 15) / 16;
+    const int id = (int)blockIdx.x * kStreamGroup + wave;
+    const int64_t first = groups * id / kStreamWaves, last = groups * (id + 1) / kStreamWaves;
+    char* const ring = smem + wave * 2 * kStage;
+    // load u: rows 8 u .. + 8 in lane order; row r + 8 has swizzle(r) ^ 4
+    const int lr = lane >> 3, lq = (lane & 7) ^ swizzle(lr);
+    const uint32_t vw[2] = {(uint32_t)(lr * a.hidden + lq * 16), (uint32_t)(lr * a.hidden + (lq ^ 4) * 16)};
+    const uint8_t* x[NT];
+    const float* sa[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        if (PACKED) {
+            x[j] = packed + (int64_t)j * nb * 2048 + lane * 16;
+            sa[j] = scale_t + 16 * j + c;
+        } else {
+            const int64_t r = 16 * j + c < a.n ? 16 * j + c : a.n - 1;
+            x[j] = a.a + r * a.hidden + 16 * g;
+            sa[j] = a.a_scale + r * nb;
+        }
+    }
+    for (int64_t g0 = first; g0 < last; g0 += VT) {
+        const int64_t v0 = 16 * g0;
+        const int64_t left = (last * 16 < a.vocab ? last * 16 : a.vocab) - v0;
+        const int vrows = left < 16 * VT ? (int)left : 16 * VT;
+        // rows past the wave's share read as zero (buffer range)
+        auto load_w = [&](int i, int b) {   // group i of step b; past the last step an empty range: nothing is read
+            const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(a.w + v0 * a.hidden), 0, b < nb ? vrows * a.hidden : 0, 0x00020000);
+            char* stage = ring + (b & 1) * kStage;
+#pragma unroll
+            for (int u = 2 * i; u < 2 * i + 2; ++u)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(stage + u * 1024), 16, vw[u & 1],
+                                                         (uint32_t)(u * 8 * a.hidden + block_of(b) * kQBlock), 0, 0);
+        };
+        // a group of 16 rows lies in one scale block; a group past the share has rows of zeros
+        const float* sw[VT];
+#pragma unroll
+        for (int i = 0; i < VT; ++i) sw[i] = a.w_scale + (16 * i < vrows ? v0 + 16 * i : v0) / kQBlock * nb;
+        Frag fx[NT];
+        float sx[NT], sv[VT];
+        auto load_x = [&](int k) {
+            const int b = block_of(k);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint8_t* p = x[j] + (int64_t)b * (PACKED ? 2048 : kQBlock);
+                fx[j].lo = *reinterpret_cast<const u32x4*>(p);
+                fx[j].hi = *reinterpret_cast<const u32x4*>(p + (PACKED ? 1024 : 64));
+                sx[j] = sa[j][PACKED ? b * n_pad : b];
+            }
+#pragma unroll
+            for (int i = 0; i < VT; ++i) sv[i] = sw[i][b];
+        };
+        floatx4 acc[VT][NT];
+#pragma unroll
+        for (int i = 0; i < VT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < VT; ++i) load_w(i, 0);
+        load_x(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < VT; ++i) load_w(i, 1);
+        for (int b = 0; b < nb; ++b) {
+            // all but the next step's W, issued last, has landed
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * VT) : "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            Wide wx[NT];
+            float s[NT], t[VT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) wx[j].set(fx[j]), s[j] = sx[j];
+#pragma unroll
+            for (int i = 0; i < VT; ++i) t[i] = sv[i];
+            __builtin_amdgcn_sched_barrier(0);
+            load_x(b + 1 < nb ? b + 1 : b);
+            __builtin_amdgcn_sched_barrier(0);
+            const char* stage = ring + (b & 1) * kStage;
+#pragma unroll
+            for (int i = 0; i < VT; ++i) {
+                const int r = 16 * i + c;
+                Frag f;
+                f.lo = *reinterpret_cast<const u32x4*>(stage + r * 128 + ((g ^ swizzle(r)) << 4));
+                f.hi = *reinterpret_cast<const u32x4*>(stage + r * 128 + (((4 + g) ^ swizzle(r)) << 4));
+                // the fragment is in registers: its slot takes the step after next
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                load_w(i, b + 2);
+                __builtin_amdgcn_sched_barrier(0);
+                Wide ww;
+                ww.set(f);
+                floatx4 z[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) z[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        z[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww.p[q], wx[j].p[q], z[j], 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const float m = s[j] * t[i];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(z[j][e], m, acc[i][j][e]);
+                }
+            }
+        }
+        // the empty loads too have landed before the slots are used again
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < VT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                store4(a, 16 * j + c, v0 + 16 * i + 4 * g, 16 * i + 4 * g < vrows ? vrows - 16 * i - 4 * g : 0, acc[i][j]);
+    }
+}
+
+template <int VT, int NT, bool PACKED>
+void stream(const LogitsArgs& a, const uint8_t* packed, const float* scale_t, int n_pad, hipStream_t s) {
+    logits_stream_kernel<VT, NT, PACKED>
+        <<<kStreamWaves / kStreamGroup, 64 * kStreamGroup, 0, s>>>(a, packed, scale_t, n_pad);
+}
+
+// Groups of 16 rows at a time: the wave's whole share where it is at most five
+// (more would not fit the LDS or the registers), else a divisor-like part of it.
+template <int NT, bool PACKED>
+void stream_by_share(const LogitsArgs& a, const uint8_t* packed, const float* scale_t, int n_pad, hipStream_t s) {
+    const int64_t share = cdiv(cdiv(a.vocab, 16), kStreamWaves);
+    const int64_t vt = cdiv(share, cdiv(share, 5));
+    if (vt <= 1) return stream<1, NT, PACKED>(a, packed, scale_t, n_pad, s);
+    if (vt == 2) return stream<2, NT, PACKED>(a, packed, scale_t, n_pad, s);
+    if (vt == 3) return stream<3, NT, PACKED>(a, packed, scale_t, n_pad, s);
+    if (vt == 4) return stream<4, NT, PACKED>(a, packed, scale_t, n_pad, s);
+    return stream<5, NT, PACKED>(a, packed, scale_t, n_pad, s);
+}
+
+// ------------------------------------------------------------- many rows
 
 constexpr int kTileRows = 256;       // input rows of a tile
 constexpr int kTileThreads = 512;    // eight waves: 2 along the vocabulary, 4 along the rows
@@ -234,8 +323,15 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
     const int lr = wave * 8 * kLoads + (lane >> 3);
     const int lq = (lane & 7) ^ swizzle(lr);
     const uint32_t vw[2] = {(uint32_t)(lr * a.hidden + lq * 16), (uint32_t)(lr * a.hidden + (lq ^ 4) * 16)};
+    // step k is column block (k + rot) mod nb, an eighth of the way on from one XCD to the
+    // next (fewer waves at the same columns of memory; 256 rows: 233 us without, 215 us with)
+    const int rot = (int)(blockIdx.x % 8) * nb / 8;
+    auto block_of = [&](int k) {
+        const int kc = (k < nb ? k : nb - 1) + rot;
+        return kc < nb ? kc : kc - nb;
+    };
     auto load_w = [&](int b) {
-        const int bc = b < nb ? b : nb - 1;
+        const int bc = block_of(b);
         char* stage = smem + (b & (kStages - 1)) * kStage;
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
@@ -254,7 +350,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
         float s[4], s0;
     };
     auto load_rows = [&](int b, Step& n) {
-        const int bc = b < nb ? b : nb - 1;
+        const int bc = block_of(b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint8_t* p = rows + ((int64_t)j * nb + bc) * 2048;
@@ -293,10 +389,13 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
         };
         Frag fw = w_frag(0);
         if constexpr (EXACT) {
-            const Wide wx[4] = {Wide(cur.f[0]), Wide(cur.f[1]), Wide(cur.f[2]), Wide(cur.f[3])};
+            Wide wx[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) wx[j].set(cur.f[j]);
 #pragma unroll
             for (int i = 0; i < VI; ++i) {
-                const Wide ww(fw);
+                Wide ww;
+                ww.set(fw);
                 if (i + 1 < VI) fw = w_frag(i + 1);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -345,59 +444,41 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
     if (b < nb) step(b, s0, s1);
     // every LDS-direct load (the clamped ones past the last step included) lands before the end
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    // four consecutive logits of a row per lane: one store where rows keep that aligned
-    const bool whole = (a.ld & 3) == 0;
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
         const int64_t v = v0 + wv * 16 * VI + 16 * i + 4 * g;
+        const int64_t left = a.vocab - v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t row = i0 + 16 * j + c;
-            if (row >= a.n) continue;
-            const int64_t at = row * a.ld + v;
-            if (whole && v + 4 <= a.vocab) {
-                if (EXACT)
-                    *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(a.out) + at) = acc[i][j];
-                else
-                    *reinterpret_cast<uint2*>(reinterpret_cast<bf16_bits*>(a.out) + at) =
-                        make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (v + e < a.vocab) {
-                        if (EXACT)
-                            reinterpret_cast<float*>(a.out)[at + e] = acc[i][j][e];
-                        else
-                            reinterpret_cast<__bf16*>(a.out)[at + e] = (__bf16)acc[i][j][e];
-                    }
-            }
-        }
+        for (int j = 0; j < 4; ++j) store4(a, i0 + 16 * j + c, v, left < 4 ? (int)left : 4, acc[i][j]);
     }
 }
 
 }  // namespace
 
+// rows padded for the packed copy: none up to 16
+int64_t packed_rows(int64_t n) { return n <= 16 ? 0 : round_up(n, n <= kStreamRows ? 16 : kTileRows); }
+
 size_t logits_workspace(int64_t n, int hidden) {
-    if (n <= kStreamRows) return 256;
-    const int64_t n_pad = round_up(n, kTileRows);
-    return (size_t)(n_pad * hidden + round_up(4 * n_pad * (hidden / kQBlock), 256));
+    const int64_t n_pad = packed_rows(n);
+    return (size_t)(n_pad * hidden + round_up(4 * n_pad * (hidden / kQBlock) + 1, 256));
 }
 
 void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s) {
-    if (a.n <= 16) return stream<2, 1>(a, s);
-    if (a.n <= 32) return stream<4, 2>(a, s);
-    if (a.n <= 64) return stream<4, 4>(a, s);
-    if (a.n <= kStreamRows) return stream<2, 8>(a, s);
+    if (a.n <= 16) return stream_by_share<1, false>(a, nullptr, nullptr, 0, s);
+    const int64_t n_pad = packed_rows(a.n);
+    uint8_t* rows = (uint8_t*)workspace;
+    float* scale_t = (float*)(rows + n_pad * a.hidden);
+    pack_rows_kernel<<<grid_1d(n_pad * a.hidden / 16, 256, 8192), 256, 0, s>>>(a.a, a.a_scale, a.n, n_pad, a.hidden,
+                                                                              rows, scale_t);
+    if (a.n <= 32) return stream_by_share<2, true>(a, rows, scale_t, (int)n_pad, s);
+    if (a.n <= 48) return stream_by_share<3, true>(a, rows, scale_t, (int)n_pad, s);
+    if (a.n <= kStreamRows) return stream_by_share<4, true>(a, rows, scale_t, (int)n_pad, s);
     TileArgs t;
     t.p = a;
-    t.n_pad = round_up(a.n, kTileRows);
-    uint8_t* rows = (uint8_t*)workspace;
-    float* scale_t = (float*)(rows + t.n_pad * a.hidden);
     t.rows = rows;
     t.scale_t = scale_t;
-    pack_rows_kernel<<<grid_1d(t.n_pad * a.hidden / 16, 256, 8192), 256, 0, s>>>(a.a, a.a_scale, a.n, t.n_pad, a.hidden,
-                                                                                rows, scale_t);
-    t.tiles_n = t.n_pad / kTileRows;
+    t.n_pad = n_pad;
+    t.tiles_n = n_pad / kTileRows;
     if (a.out_f32) {
         t.tiles_v = cdiv(a.vocab, 128);
         logits_tile_kernel<true, 4><<<(unsigned)(t.tiles_n * t.tiles_v), kTileThreads, 0, s>>>(t);

@@ -93,10 +93,11 @@ __device__ __forceinline__ void store4(const LogitsArgs& a, int64_t row, int64_t
         }
 }
 
-// The rows packed: 16-row x 128-column blocks of 2 KB in
-// fragment order (the lanes' low 16 bytes, then their high ones), block (i /
-// 16, b) at ((i / 16) nb + b) * 2 KB, rows up to n_pad zero; and the scales
-// transposed, [nb][n_pad].
+// The rows packed: 16-row x 128-column blocks of 2 KB in fragment order (the
+// lanes' low 16 bytes, then their high ones), block (i / 16, b) at ((i / 16) nb
+// + b) * 2 KB, rows up to n_pad zero; and the scales transposed, [nb][n_pad],
+// row 64 t + 16 j + c at 64 t + 4 c + j when n_pad is a multiple of 64 (a
+// lane's four rows side by side), else in order.
 __global__ __launch_bounds__(256) void pack_rows_kernel(const uint8_t* a, const float* a_scale, int64_t n,
                                                         int64_t n_pad, int hidden, uint8_t* out, float* scale_t) {
     const int nb = hidden / kQBlock;
@@ -112,7 +113,8 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const uint8_t* a, const 
         reinterpret_cast<uint4*>(out)[q] = v;
     }
     for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < scales; q += step) {
-        const int64_t b = q / n_pad, row = q - b * n_pad;
+        const int64_t b = q / n_pad, at = q - b * n_pad;
+        const int64_t row = n_pad % 64 == 0 ? at / 64 * 64 + (at & 3) * 16 + (at >> 2 & 15) : at;
         scale_t[q] = row < n ? a_scale[row * nb + b] : 0.0f;
     }
 }
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(64 * kStreamGroup) void logits_stream_kernel(Logits
     for (int j = 0; j < NT; ++j) {
         if (PACKED) {
             x[j] = packed + (int64_t)j * nb * 2048 + lane * 16;
-            sa[j] = scale_t + 16 * j + c;
+            sa[j] = scale_t + (n_pad == 64 ? 4 * c + j : 16 * j + c);
         } else {
             const int64_t r = 16 * j + c < a.n ? 16 * j + c : a.n - 1;
             x[j] = a.a + r * a.hidden + 16 * g;
@@ -298,8 +300,8 @@ struct TileArgs {
 // 16-byte chunk q of row r at q ^ ((r >> 1) & 7) (conflict-free fragment
 // reads), written by LDS-direct buffer loads, four steps in a ring. The rows'
 // fragments come straight from the packed copy into registers, a step ahead.
-// In a step a wave issues the next step's row fragments first and then the W
-// loads of step b + 3: waiting for the former at the next step's start leaves
+// In a step a wave issues the next step's row fragments and scales first and
+// then the W loads of step b + 3: waiting for the former at the next step's start leaves
 // only the latter in flight, so W of step b + 1 has landed for every wave that
 // has begun step b, and one barrier per step is enough.
 template <bool EXACT, int VI>
@@ -330,34 +332,34 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
         const int kc = (k < nb ? k : nb - 1) + rot;
         return kc < nb ? kc : kc - nb;
     };
-    auto load_w = [&](int b) {
+    auto load_w = [&](int b, int half) {
         const int bc = block_of(b);
         char* stage = smem + (b & (kStages - 1)) * kStage;
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u)
+        for (int u = half * (kLoads / 2); u < (half + 1) * (kLoads / 2); ++u)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(stage + (wave * kLoads + u) * 1024), 16, vw[u & 1],
                                                      (uint32_t)(u * 8 * a.hidden + bc * kQBlock), 0, 0);
     };
     const int64_t i0 = tn * kTileRows + wn * 64;
     const uint8_t* rows = t.rows + (i0 / 16) * nb * 2048 + lane * 16;
-    const float* sat = t.scale_t + i0 + c;
+    const float* sat = t.scale_t + i0 + 4 * c;
     // a wave's rows of W share a scale block; where they lie past the vocabulary they are
     // zero, and the tile's first block stands in
     const int64_t vw0 = v0 + wv * 16 * VI;
     const float* sw = a.w_scale + (vw0 < a.vocab ? vw0 : v0) / kQBlock * nb;
     struct Step {
         Frag f[4];
-        float s[4], s0;
+        floatx4 s;
+        float s0;
     };
-    auto load_rows = [&](int b, Step& n) {
+    auto load_row = [&](int b, Step& n, int j) {
+        const uint8_t* p = rows + ((int64_t)j * nb + block_of(b)) * 2048;
+        n.f[j].lo = *reinterpret_cast<const u32x4*>(p);
+        n.f[j].hi = *reinterpret_cast<const u32x4*>(p + 1024);
+    };
+    auto load_scales = [&](int b, Step& n) {
         const int bc = block_of(b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint8_t* p = rows + ((int64_t)j * nb + bc) * 2048;
-            n.f[j].lo = *reinterpret_cast<const u32x4*>(p);
-            n.f[j].hi = *reinterpret_cast<const u32x4*>(p + 1024);
-            n.s[j] = sat[(int64_t)bc * t.n_pad + 16 * j];
-        }
+        n.s = *reinterpret_cast<const floatx4*>(sat + (int64_t)bc * t.n_pad);
         n.s0 = sw[bc];
     };
     floatx4 acc[VI][4];
@@ -366,11 +368,17 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     // One step: the W fragment of group i + 1 is read, and group i - 1's sums
-    // are scaled and added, between the matrix instructions of group i.
+    // are scaled and added, between the matrix instructions of group i. The
+    // step's loads are spread over its groups too, the row fragments in the
+    // first half, the scales, then W: issued together at the start they filled
+    // the load queue and every wave stood before its first matrix instruction.
     auto step = [&](int b, Step& cur, Step& nxt) {
-        load_rows(b + 1, nxt);
-        load_w(b + 3);
-        __builtin_amdgcn_sched_barrier(0);
+        auto issue = [&](int i) {   // after group i of 8 (VI = 8) or half group of 4
+            if (i < 4) load_row(b + 1, nxt, i);
+            if (i == 4) load_scales(b + 1, nxt);
+            if (i == 5) load_w(b + 3, 0);
+            if (i == 6) load_w(b + 3, 1);
+        };
         const char* stage = smem + (b & (kStages - 1)) * kStage + wv * 16 * VI * 128;
         auto w_frag = [&](int i) {
             const int r = 16 * i + c;
@@ -382,6 +390,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
         float s[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[j] = cur.s[j] * cur.s0;
+        __builtin_amdgcn_sched_barrier(0);
         floatx4 z[2][4];
         auto add = [&](int i, int j) {
 #pragma unroll
@@ -405,6 +414,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
                         z[i & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww.p[q], wx[j].p[q], z[i & 1][j], 0, 0, 0);
                     }
                     if (i > 0) add(i - 1, q);
+                    if (q & 1) issue(2 * i + (q >> 1));
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -418,6 +428,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
                     z[i & 1][j] = block_sum(ww, wx[j]);
                     if (j == 0 && i + 1 < VI) fw = w_frag(i + 1);
                     if (i > 0) add(i - 1, j);
+                    if (j == 2) issue(i);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -430,10 +441,13 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
         __builtin_amdgcn_sched_barrier(0);
     };
     Step s0, s1;
-    load_w(0);
-    load_w(1);
-    load_rows(0, s0);
-    load_w(2);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) load_w(k, 0), load_w(k, 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_row(0, s0, j);
+    load_scales(0, s0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_w(2, 0), load_w(2, 1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     int b = 0;

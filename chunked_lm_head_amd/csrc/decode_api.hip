@@ -184,7 +184,7 @@ int lmhead_logits_fp8(const lmhead_fp8_problem* p, const void* a, const float* a
 }
 
 size_t lmhead_sample_workspace_size(const lmhead_sample_problem* p) {
-    return validate(p) == LMHEAD_OK ? 256 : 0;
+    return validate(p) == LMHEAD_OK ? sample_workspace(p->n) : 0;
 }
 
 int lmhead_sample(const lmhead_sample_problem* p, const void* logits, const float* u, int32_t* token,
@@ -201,9 +201,12 @@ int lmhead_sample(const lmhead_sample_problem* p, const void* logits, const floa
     st = check_device();
     if (st != LMHEAD_OK) return st;
     hipStream_t s = (hipStream_t)stream;
-    init_header_kernel<<<1, 64, 0, s>>>((int32_t*)workspace);
-    if (p->n == 0) return launched();
-    SampleArgs a;
+    if (p->n == 0) {
+        init_header_kernel<<<1, 64, 0, s>>>((int32_t*)workspace);
+        return launched();
+    }
+    SampleArgs a;   // the first launch clears the header
+
     a.logits = logits;
     a.logits_f32 = p->logits_dtype == LMHEAD_DTYPE_F32;
     a.n = p->n;
@@ -225,7 +228,7 @@ int lmhead_sample(const lmhead_sample_problem* p, const void* logits, const floa
     int bits = 0;
     while ((int64_t(1) << bits) < p->vocab) ++bits;
     a.shift = 62 - bits < 44 ? 62 - bits : 44;
-    launch_sample(a, s);
+    launch_sample(a, workspace, s);
     return launched();
 }
 

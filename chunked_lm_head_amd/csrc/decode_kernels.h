@@ -78,6 +78,7 @@ struct SampleArgs {
     int32_t* hdr;
     int shift;   // weights are integers of 2^-shift
 };
-void launch_sample(const SampleArgs& a, hipStream_t s);
+size_t sample_workspace(int64_t n);
+void launch_sample(const SampleArgs& a, void* workspace, hipStream_t s);
 
 }  // namespace lmhead

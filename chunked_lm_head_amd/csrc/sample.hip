@@ -3,11 +3,28 @@
 // weight in index order (include/lmhead_decode.h states the rule).
 //
 // Exactness. Which token a row gets is decided by comparisons of sums of
-// weights w = exp((x - max) / tau), so the weights are made once, in 64 bits
-// (2^d by a degree-10 polynomial on |r| <= 1/2, relative error 6e-16), and
-// rounded to integers of 2^-shift (shift = 44 up to 262,144 tokens). Their sums
-// are exact in 64-bit integers whatever the order, so histograms may be
-// filled with integer atomics and the result still repeats bit for bit.
+// weights w = exp((x - max) / tau), so the weights are made in 64 bits (2^d by
+// a degree-9 polynomial on |r| <= 1/2, relative error 4e-14) and rounded to
+// integers of 2^-shift (shift = 44 up to 262,144 tokens). Their sums are exact
+// in 64-bit integers whatever the order, so histograms may be filled with
+// integer atomics and the result still repeats bit for bit.
+//
+// Plan. In the order of descending logit (equal logits by index) each filter
+// keeps a prefix, so all of them together keep the shortest of the prefixes.
+// Rows are cut into slices, a workgroup each, and go through five launches
+// (three without filters):
+//   scan    largest and smallest logit of the slice, bad values;
+//   hist    weight (and count, for top-k) of the slice's tokens in 2048 bins
+//           of equal width below the row's largest logit;
+//   border  (a workgroup per row) the bins in which the prefixes end;
+//   gather  the row's tokens in those bins (some hundred) are listed;
+//   pick    the list sorted, the end of the prefix found exactly; the kept
+//           weight of each slice from its histogram; the slice in which u
+//           falls, and the token in it.
+// So each logit is read three times (from memory once, the rest from the
+// caches: rows are taken 256 at a time) and its weight is computed once. What
+// the list cannot hold (thousands of equal logits at the border) is resolved
+// by a radix descent over the row, in the pick kernel.
 #include "decode_kernels.h"
 #include "host_util.h"
 
@@ -21,6 +38,9 @@ constexpr int kRowThreads = 1024;
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kBins = 2048;
 constexpr int kSegs = 2048;
+constexpr int kList = 4096;        // listed border tokens per row
+constexpr int kMaxSlices = 16;
+constexpr int kChunkRows = 256;    // rows per set of launches
 constexpr uint32_t kMaskedKey = 0x007fffffu;   // key of -infinity
 
 // Order-preserving map of floats to integers; -0 and +0 share a key.
@@ -32,37 +52,36 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// 2^(d + shift), d <= 0: 2^n (1 + r q(r)), r = d - n, |r| <= 1/2. q
-// interpolates (2^r - 1) / r at the ten Chebyshev nodes of the interval.
-__device__ __forceinline__ double exp2_scaled(double d, int shift) {
-    const double n = __builtin_rint(d);
-    const double r = d - n;
-    double q = 0x1.e5e9f548e5725p-28;
-    q = __builtin_fma(q, r, 0x1.b6571de2f2351p-24);
-    q = __builtin_fma(q, r, 0x1.62bfe46117445p-20);
-    q = __builtin_fma(q, r, 0x1.ffcb76789860fp-17);
-    q = __builtin_fma(q, r, 0x1.4309130378460p-13);
-    q = __builtin_fma(q, r, 0x1.5d87fe908f88ap-10);
-    q = __builtin_fma(q, r, 0x1.3b2ab6fba385fp-7);
-    q = __builtin_fma(q, r, 0x1.c6b08d7044119p-5);
-    q = __builtin_fma(q, r, 0x1.ebfbdff82c590p-3);
-    q = __builtin_fma(q, r, 0x1.62e42fefa39f7p-1);
-    q = __builtin_fma(q, r, 1.0);
-    return __builtin_amdgcn_ldexp(q, (int)n + shift);
-}
-
-// The row's weights: scaled(x) = 2^shift exp((x - top) / tau), and its integer.
+// The row's weights: scaled(x) = 2^shift exp((x - top) / tau) as a double.
+// 2^d = 2^n (1 + r q(r)), r = d - n, |r| <= 1/2; q interpolates (2^r - 1) / r
+// at the nine Chebyshev nodes of the interval. The nearest integer n comes from
+// adding 1.5 * 2^52, whose low word then holds it; 2^n goes into the exponent
+// field. d is kept at -64 or above (-infinity included): a weight of 0.
 struct Weights {
     double top, scale;   // scale = log2(e) / tau
     int shift;
     __device__ __forceinline__ double scaled(float x) const {
-        const double d = ((double)x - top) * scale;
-        return d > -64.0 ? exp2_scaled(d, shift) : 0.0;   // -infinity included
+        const double d = __builtin_fmax(((double)x - top) * scale, -64.0);
+        const double t = d + 0x1.8p52;
+        const double r = d - (t - 0x1.8p52);
+        double q = 0x1.b63880a30e9ffp-24;
+        q = __builtin_fma(q, r, 0x1.63d136366db24p-20);
+        q = __builtin_fma(q, r, 0x1.ffcb9515a8016p-17);
+        q = __builtin_fma(q, r, 0x1.4308ac85aa947p-13);
+        q = __builtin_fma(q, r, 0x1.5d87fe86fe88ep-10);
+        q = __builtin_fma(q, r, 0x1.3b2ab7181b755p-7);
+        q = __builtin_fma(q, r, 0x1.c6b08d7047e52p-5);
+        q = __builtin_fma(q, r, 0x1.ebfbdff823cedp-3);
+        q = __builtin_fma(q, r, 0x1.62e42fefa39efp-1);
+        q = __builtin_fma(q, r, 1.0);
+        const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t) + shift;
+        return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, q) + ((uint64_t)(uint32_t)n << 52));
     }
     // nearest integer of a value below 2^51: the low bits of 2^52 + it
     static __device__ __forceinline__ uint64_t whole(double s) {
         return __builtin_bit_cast(uint64_t, s + 0x1.0p52) & 0xfffffffffffffull;
     }
+    __device__ __forceinline__ uint64_t of(float x) const { return whole(scaled(x)); }
 };
 
 // A row of logits as 16-byte vectors: the first and last may reach past it
@@ -80,6 +99,72 @@ struct Row {
         end = off + vocab;
     }
     __device__ __forceinline__ int64_t vectors() const { return (end + kPer - 1) / kPer; }
+    // vectors k, k + STEP, k + 2 STEP, k + 3 STEP, those from k1 on as -infinity
+    template <int STEP>
+    __device__ __forceinline__ void load4(int64_t k, int64_t k1, float (&x)[4][kPer]) const {
+        if (k * kPer >= off && (k + 3 * STEP + 1) * kPer <= end && k + 3 * STEP < k1) {
+            uint4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(base + (k + q * STEP) * 16);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (F32) {
+                        x[q][i] = __builtin_bit_cast(float, w[i]);
+                    } else {
+                        x[q][2 * i] = __builtin_bit_cast(float, w[i] << 16);
+                        x[q][2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
+                    }
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (k + q * STEP < k1) {
+                load(k + q * STEP, x[q]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) x[q][i] = -__builtin_huge_valf();
+            }
+        }
+    }
+    // f(x, position) for this thread's share of vectors k0 .. k1 - 1, four loads in flight
+    template <class F>
+    __device__ __forceinline__ void each(int64_t k0, int64_t k1, F f) const {
+        const int64_t a0 = k0 == 0 && off > 0 ? 1 : k0;               // the vectors inside the row
+        const int64_t a1 = k1 * kPer > end ? end / kPer : k1;
+        for (int64_t b = a0 + threadIdx.x; b < a1; b += 4 * kRowThreads) {
+            uint32_t w[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t k = b + q * kRowThreads;
+                const uint4 v = *reinterpret_cast<const uint4*>(base + (k < a1 ? k : b) * 16);
+                w[q][0] = v.x, w[q][1] = v.y, w[q][2] = v.z, w[q][3] = v.w;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t k = b + q * kRowThreads;
+                if (k >= a1) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (F32) {
+                        f(__builtin_bit_cast(float, w[q][i]), k * kPer + i);
+                    } else {
+                        f(__builtin_bit_cast(float, w[q][i] << 16), k * kPer + 2 * i);
+                        f(__builtin_bit_cast(float, w[q][i] & 0xffff0000u), k * kPer + 2 * i + 1);
+                    }
+                }
+            }
+        }
+        // the row's first and last positions outside whole vectors, one a thread
+        const int64_t h1 = end < kPer ? end : kPer;
+        if (k0 == 0 && k1 > 0 && off > 0 && threadIdx.x < h1 - off) f(at(off + threadIdx.x), off + threadIdx.x);
+        const int64_t t0 = end / kPer * kPer;
+        if (k1 * kPer > end && (t0 > 0 || off == 0) && threadIdx.x < end - t0) f(at(t0 + threadIdx.x), t0 + threadIdx.x);
+    }
     __device__ __forceinline__ float at(int64_t pos) const {
         if (F32) return reinterpret_cast<const float*>(base)[pos];
         return __builtin_bit_cast(float, (uint32_t) reinterpret_cast<const uint16_t*>(base)[pos] << 16);
@@ -106,19 +191,29 @@ struct Row {
     }
 };
 
-__device__ __forceinline__ uint64_t wave_scan(uint64_t v, int lane) {   // inclusive
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint64_t o = __shfl_up(v, m);
-        if (lane >= m) v += o;
-    }
-    return v;
+// v plus the value that the DPP move CTRL brings from another lane (0 where it brings none)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t add_dpp(uint64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+    return v + ((uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ uint64_t wave_total(uint64_t v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-    return v;
+// Inclusive prefix over the wave: within rows of 16 lanes (row_shr 1, 2, 4, 8),
+// then lane 15 of a row to the next (row_bcast 15), lane 31 to the upper half.
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
+    v = add_dpp<0x111, 0xf>(v);
+    v = add_dpp<0x112, 0xf>(v);
+    v = add_dpp<0x114, 0xf>(v);
+    v = add_dpp<0x118, 0xf>(v);
+    v = add_dpp<0x142, 0xa>(v);
+    return add_dpp<0x143, 0xc>(v);
 }
+__device__ __forceinline__ uint64_t last_lane(uint64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63);
+    return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t wave_total(uint64_t v) { return last_lane(wave_scan(v)); }
 
 struct Shared {
     uint64_t hist[kBins];
@@ -132,7 +227,7 @@ struct Shared {
 // Exclusive prefix of v over the workgroup's threads; total to all.
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, Shared& S, uint64_t& total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint64_t inc = wave_scan(v, lane);
+    const uint64_t inc = wave_scan(v);
     __syncthreads();
     if (lane == 63) S.part[wave] = inc;
     __syncthreads();
@@ -182,7 +277,7 @@ __device__ Threshold descend(const Row<F32>& row, const Weights& W, Shared& S, u
     const int64_t nvec = row.vectors();
     uint32_t prefix = 0, mask = 0;
     uint64_t above = 0;
-    const uint64_t w_in = WEIGHTED ? Weights::whole(W.scaled(value_of(in.key))) : 0;
+    const uint64_t w_in = WEIGHTED && in.ties > 0 ? W.of(value_of(in.key)) : 0;
     for (int level = 0; level < 3; ++level) {
         const int sh = level == 0 ? 21 : level == 1 ? 10 : 0;
         const uint32_t field = level == 2 ? 1023u : 2047u;
@@ -196,7 +291,7 @@ __device__ Threshold descend(const Row<F32>& row, const Weights& W, Shared& S, u
                 const uint32_t key = key_of(x[i]);
                 if (key > in.key && (key & mask) == prefix)
                     atomicAdd((unsigned long long*)&S.hist[(key >> sh) & field],
-                              (unsigned long long)(WEIGHTED ? Weights::whole(W.scaled(x[i])) : 1));
+                              (unsigned long long)(WEIGHTED ? W.of(x[i]) : 1));
             }
         }
         __syncthreads();
@@ -208,201 +303,729 @@ __device__ Threshold descend(const Row<F32>& row, const Weights& W, Shared& S, u
         prefix |= bin << sh;
         mask |= field << sh;
     }
-    const uint64_t w = WEIGHTED ? Weights::whole(W.scaled(value_of(prefix))) : 1;
+    const uint64_t w = WEIGHTED ? W.of(value_of(prefix)) : 1;
     return {prefix, (target - above + w - 1) / w};
 }
 
+struct Params {
+    float tau, u, top_p, min_p;
+    int64_t top_k;
+    int code;   // data errors of the row's own numbers
+};
+
+__device__ __forceinline__ Params row_params(const SampleArgs& a, int64_t r) {
+    Params P;
+    P.tau = row_tau(a.T, r);
+    P.u = a.u[r];
+    P.top_p = a.row_top_p != nullptr ? a.row_top_p[r] : (a.top_p == 0.0f ? 1.0f : a.top_p);
+    P.min_p = a.row_min_p != nullptr ? a.row_min_p[r] : a.min_p;
+    P.top_k = a.row_top_k != nullptr ? a.row_top_k[r] : a.top_k;
+    P.code = (tau_ok(P.tau) ? 0 : kDevErrTemperature) |
+             (P.u >= 0.0f && P.u < 1.0f && P.top_p > 0.0f && P.top_p <= 1.0f && P.min_p >= 0.0f && P.min_p <= 1.0f
+                  ? 0 : kDevErrSampling);
+    return P;
+}
+
+// smallest integer weight that min-p keeps
+__device__ __forceinline__ uint64_t weight_floor(float min_p, int shift) {
+    return (uint64_t)__builtin_ceil((double)min_p * (double)(1ull << shift));
+}
+// integer weight that top-p has to reach, of `kept`
+__device__ __forceinline__ uint64_t nucleus(float top_p, uint64_t kept) {
+    const uint64_t t = (uint64_t)__builtin_ceil((double)top_p * (double)kept);
+    return t < 1 ? 1 : (t > kept ? kept : t);
+}
+
 template <bool F32>
-__global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) {
+__device__ __forceinline__ void write_token(const SampleArgs& a, int64_t r, const Row<F32>& row, int64_t pos,
+                                            const Weights& W, float tau, uint64_t all) {
+    a.token[r] = (int32_t)(pos - row.off);
+    if (a.logprob != nullptr)
+        a.logprob[r] = (float)(((double)row.at(pos) - W.top) / (double)tau -
+                               log((double)all * __builtin_amdgcn_ldexp(1.0, -W.shift)));
+}
+
+// A whole row by radix descent: what the listed border tokens cannot resolve.
+template <bool F32>
+__device__ __attribute__((noinline)) void whole_row(const SampleArgs& a, int64_t r, const Row<F32>& row, const Params& P, const Weights& W,
+                          Shared& S) {
     constexpr int kPer = Row<F32>::kPer;
-    __shared__ Shared S;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
-        const Row<F32> row(a.logits, r, a.ld, a.vocab);
-        const int64_t nvec = row.vectors();
-        const float tau = row_tau(a.T, r);
-        const float u = a.u[r];
-        const float top_p = a.row_top_p != nullptr ? a.row_top_p[r] : (a.top_p == 0.0f ? 1.0f : a.top_p);
-        const float min_p = a.row_min_p != nullptr ? a.row_min_p[r] : a.min_p;
-        const int64_t top_k = a.row_top_k != nullptr ? a.row_top_k[r] : a.top_k;
-        // largest logit, unmasked tokens, bad logits
-        __syncthreads();
-        if (tid == 0) S.flags = S.top = 0;
-        __syncthreads();
-        uint32_t top = 0, bad = 0;
-        uint64_t valid = 0;
+    const int64_t nvec = row.vectors();
+    // filters: the threshold of top-k, then that of top-p within it
+    Threshold T{kMaskedKey, 0};
+    if (P.top_k > 0) T = descend<F32, false>(row, W, S, (uint64_t)P.top_k, T);
+    // the weight of everything (for the log-probability) and of what top-k kept
+    uint64_t all, kept;
+    {
+        uint64_t s_all = 0, s_kept = 0;
         for (int64_t k = tid; k < nvec; k += kRowThreads) {
             float x[kPer];
             row.load(k, x);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                bad |= !(x[i] < __builtin_huge_valf());   // NaN, +infinity
+                const uint64_t w = W.of(x[i]);
+                s_all += w;
+                s_kept += key_of(x[i]) > T.key ? w : 0;
+            }
+        }
+        block_scan(s_all, S, all);
+        block_scan(s_kept, S, kept);
+        if (T.ties > 0) kept += T.ties * W.of(value_of(T.key));
+    }
+    if (P.top_p < 1.0f) T = descend<F32, true>(row, W, S, nucleus(P.top_p, kept), T);
+    const uint64_t floor_w = weight_floor(P.min_p, W.shift);
+    const uint64_t edge = T.ties > 0 ? W.of(value_of(T.key)) : 0;
+    const uint64_t w_tie = T.ties > 0 && edge >= floor_w ? edge : 0;
+    // kept weight and ties per segment of 64 m vectors, a wave each
+    const int64_t m = (nvec + 64 * kSegs - 1) / (64 * kSegs);
+    const int nseg = (int)((nvec + 64 * m - 1) / (64 * m));
+    __syncthreads();
+    for (int sg = tid; sg < kSegs; sg += kRowThreads) S.hist[sg] = 0, S.ties[sg] = 0;
+    __syncthreads();
+    for (int sg = wave; sg < nseg; sg += kRowWaves) {
+        uint64_t w = 0, t = 0;
+        for (int64_t j = 0; j < m; ++j) {
+            const int64_t k = ((int64_t)sg * m + j) * 64 + lane;
+            if (k >= nvec) break;
+            float x[kPer];
+            row.load(k, x);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
                 const uint32_t key = key_of(x[i]);
-                top = key > top ? key : top;
-                valid += key > kMaskedKey;
+                const uint64_t wx = W.of(x[i]);
+                w += key > T.key && wx >= floor_w ? wx : 0;
+                t += key == T.key;
             }
         }
-        atomicMax(&S.top, top);
-        if (bad) atomicOr(&S.flags, 1u);
-        uint64_t n_valid;
-        block_scan(valid, S, n_valid);
-        const int code = (S.flags ? kDevErrLogit : 0) | (tau_ok(tau) ? 0 : kDevErrTemperature) |
-                         (u >= 0.0f && u < 1.0f && top_p > 0.0f && top_p <= 1.0f && min_p >= 0.0f && min_p <= 1.0f
-                              ? 0 : kDevErrSampling);
-        if (code != 0 || n_valid == 0) {
-            if (tid == 0) {
-                a.token[r] = -1;
-                if (a.logprob != nullptr) a.logprob[r] = code != 0 ? __builtin_nanf("") : 0.0f;
-                if (code != 0) {
-                    atomicOr(a.hdr + kHdrErrCode, code);
-                    atomicMin(a.hdr + kHdrErrRow, (int32_t)r);
-                }
-            }
-            continue;
-        }
-        Weights W;
-        W.top = (double)value_of(S.top);
-        W.scale = 1.4426950408889634 / (double)tau;
-        W.shift = a.shift;
-        // filters: the threshold of top-k, then that of top-p within it
-        Threshold T{kMaskedKey, 0};
-        if (top_k > 0 && (uint64_t)top_k < n_valid) T = descend<F32, false>(row, W, S, (uint64_t)top_k, T);
-        // the weight of everything (for the log-probability) and of what top-k kept
-        uint64_t all, kept;
-        {
-            uint64_t s_all = 0, s_kept = 0;
-            for (int64_t k = tid; k < nvec; k += kRowThreads) {
-                float x[kPer];
+        w = wave_total(w);
+        t = wave_total(t);
+        if (lane == 0) S.hist[sg] = w, S.ties[sg] = (uint32_t)t;
+    }
+    __syncthreads();
+    // prefix over the segments (two per thread): ties first, then weight
+    const uint64_t t0 = S.ties[2 * tid], t1 = S.ties[2 * tid + 1];
+    uint64_t n_ties, total;
+    const uint64_t tb = block_scan(t0 + t1, S, n_ties);
+    auto kept_ties = [&](uint64_t before, uint64_t here) {
+        const uint64_t left = before < T.ties ? T.ties - before : 0;
+        return left < here ? left : here;
+    };
+    const uint64_t w0 = S.hist[2 * tid] + kept_ties(tb, t0) * w_tie;
+    const uint64_t w1 = S.hist[2 * tid + 1] + kept_ties(tb + t0, t1) * w_tie;
+    const uint64_t wb = block_scan(w0 + w1, S, total);
+    uint64_t goal = (uint64_t)((double)P.u * (double)total);
+    goal = goal < total ? goal : total - 1;
+    // the segment where the running weight passes the goal: its index, the
+    // weight and the ties before it
+    __syncthreads();
+    if (wb <= goal && wb + w0 + w1 > goal) {
+        const bool first = wb + w0 > goal;
+        S.found_bin = 2 * tid + (first ? 0 : 1);
+        S.found_above = first ? wb : wb + w0;
+        S.part[kRowWaves] = first ? tb : tb + t0;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        uint64_t run = S.found_above, ties = S.part[kRowWaves];
+        const int64_t sg = S.found_bin;
+        bool done = false;
+        for (int64_t j = 0; j < m && !done; ++j) {
+            const int64_t k = (sg * m + j) * 64 + lane;
+            float x[kPer];
+            uint64_t w[kPer], lane_w = 0, lane_t = 0;
+            if (k < nvec) {
                 row.load(k, x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) x[i] = -__builtin_huge_valf();
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) lane_t += key_of(x[i]) == T.key;
+            const uint64_t t_inc = wave_scan(lane_t);
+            uint64_t rank = ties + t_inc - lane_t;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const uint32_t key = key_of(x[i]);
+                const uint64_t wx = W.of(x[i]);
+                const bool tie = key == T.key;
+                w[i] = tie ? (rank < T.ties ? w_tie : 0) : (key > T.key && wx >= floor_w ? wx : 0);
+                rank += tie;
+                lane_w += w[i];
+            }
+            const uint64_t w_inc = wave_scan(lane_w);
+            const uint64_t before = run + w_inc - lane_w;
+            const bool mine = before <= goal && before + lane_w > goal;
+            if (mine) {
+                uint64_t c = before;
+                int pick = 0;
+                bool got = false;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
-                    const uint64_t w = Weights::whole(W.scaled(x[i]));
-                    s_all += w;
-                    s_kept += key_of(x[i]) > T.key ? w : 0;
+                    c += w[i];
+                    if (!got && c > goal) pick = i, got = true;
                 }
+                const int64_t pos = k * kPer + pick;
+                write_token(a, r, row, pos, W, P.tau, all);
             }
-            block_scan(s_all, S, all);
-            block_scan(s_kept, S, kept);
-            kept += T.ties * Weights::whole(W.scaled(value_of(T.key)));
-        }
-        if (top_p < 1.0f) {
-            uint64_t target = (uint64_t)__builtin_ceil((double)top_p * (double)kept);
-            target = target < 1 ? 1 : (target > kept ? kept : target);
-            T = descend<F32, true>(row, W, S, target, T);
-        }
-        const double floor_p = (double)min_p * __builtin_amdgcn_ldexp(1.0, a.shift);
-        const double edge = W.scaled(value_of(T.key));
-        const uint64_t w_tie = T.ties > 0 && edge >= floor_p ? Weights::whole(edge) : 0;
-        // kept weight and ties per segment of 64 m vectors, a wave each
-        const int64_t m = (nvec + 64 * kSegs - 1) / (64 * kSegs);
-        const int nseg = (int)((nvec + 64 * m - 1) / (64 * m));
-        __syncthreads();
-        for (int sg = tid; sg < kSegs; sg += kRowThreads) S.hist[sg] = 0, S.ties[sg] = 0;
-        __syncthreads();
-        for (int sg = wave; sg < nseg; sg += kRowWaves) {
-            uint64_t w = 0, t = 0;
-            for (int64_t j = 0; j < m; ++j) {
-                const int64_t k = ((int64_t)sg * m + j) * 64 + lane;
-                if (k >= nvec) break;
-                float x[kPer];
-                row.load(k, x);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const uint32_t key = key_of(x[i]);
-                    const double s = W.scaled(x[i]);
-                    w += key > T.key && s >= floor_p ? Weights::whole(s) : 0;
-                    t += key == T.key;
-                }
-            }
-            w = wave_total(w);
-            t = wave_total(t);
-            if (lane == 0) S.hist[sg] = w, S.ties[sg] = (uint32_t)t;
-        }
-        __syncthreads();
-        // prefix over the segments (two per thread): ties first, then weight
-        const uint64_t t0 = S.ties[2 * tid], t1 = S.ties[2 * tid + 1];
-        uint64_t n_ties, total;
-        const uint64_t tb = block_scan(t0 + t1, S, n_ties);
-        auto kept_ties = [&](uint64_t before, uint64_t here) {
-            const uint64_t left = before < T.ties ? T.ties - before : 0;
-            return left < here ? left : here;
-        };
-        const uint64_t w0 = S.hist[2 * tid] + kept_ties(tb, t0) * w_tie;
-        const uint64_t w1 = S.hist[2 * tid + 1] + kept_ties(tb + t0, t1) * w_tie;
-        const uint64_t wb = block_scan(w0 + w1, S, total);
-        uint64_t goal = (uint64_t)((double)u * (double)total);
-        goal = goal < total ? goal : total - 1;
-        // the segment where the running weight passes the goal: its index, the
-        // weight and the ties before it
-        __syncthreads();
-        if (wb <= goal && wb + w0 + w1 > goal) {
-            const bool first = wb + w0 > goal;
-            S.found_bin = 2 * tid + (first ? 0 : 1);
-            S.found_above = first ? wb : wb + w0;
-            S.part[kRowWaves] = first ? tb : tb + t0;
-        }
-        __syncthreads();
-        if (wave == 0) {
-            uint64_t run = S.found_above, ties = S.part[kRowWaves];
-            const int64_t sg = S.found_bin;
-            bool done = false;
-            for (int64_t j = 0; j < m && !done; ++j) {
-                const int64_t k = (sg * m + j) * 64 + lane;
-                float x[kPer];
-                uint64_t w[kPer], lane_w = 0, lane_t = 0;
-                if (k < nvec) {
-                    row.load(k, x);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) x[i] = -__builtin_huge_valf();
-                }
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) lane_t += key_of(x[i]) == T.key;
-                const uint64_t t_inc = wave_scan(lane_t, lane);
-                uint64_t rank = ties + t_inc - lane_t;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const uint32_t key = key_of(x[i]);
-                    const double s = W.scaled(x[i]);
-                    const bool tie = key == T.key;
-                    w[i] = tie ? (rank < T.ties ? w_tie : 0) : (key > T.key && s >= floor_p ? Weights::whole(s) : 0);
-                    rank += tie;
-                    lane_w += w[i];
-                }
-                const uint64_t w_inc = wave_scan(lane_w, lane);
-                const uint64_t before = run + w_inc - lane_w;
-                const bool mine = before <= goal && before + lane_w > goal;
-                if (mine) {
-                    uint64_t c = before;
-                    int pick = 0;
-                    bool got = false;
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) {
-                        c += w[i];
-                        if (!got && c > goal) pick = i, got = true;
-                    }
-                    const int64_t pos = k * kPer + pick;
-                    a.token[r] = (int32_t)(pos - row.off);
-                    if (a.logprob != nullptr)
-                        a.logprob[r] = (float)(((double)row.at(pos) - W.top) / (double)tau -
-                                               log((double)all * __builtin_amdgcn_ldexp(1.0, -a.shift)));
-                }
-                done = __any(mine);
-                run += __shfl(w_inc, 63);
-                ties += __shfl(t_inc, 63);
-            }
+            done = __any(mine);
+            run += last_lane(w_inc);
+            ties += last_lane(t_inc);
         }
     }
 }
 
+// ------------------------------------------------------------ the four launches
+
+struct SliceStat {
+    uint32_t top, low, bad, valid;   // keys of the unmasked logits
+};
+
+// Workspace of one set of launches: [rows][slices] throughout.
+struct SampleSpace {
+    SliceStat* stat;
+    uint64_t* weight;    // [kBins] a slice
+    uint64_t* total;     // one a slice
+    uint32_t* count;     // [kBins] a slice
+    uint32_t* listed;    // one a row
+    uint64_t* list;      // [kList] a row: ~key << 32 | token
+    uint64_t* run_weight;   // [kBins] a row: weight before the bin
+    uint32_t* run_count;    // [kBins] a row: tokens before the bin (with top-k)
+    struct Borders* borders;   // one a row
+};
+
+// What every kernel after the scan derives from the row's scan.
+struct RowPlan {
+    Weights W;
+    Params P;
+    float c;           // bins per unit of logit below the top
+    uint64_t valid;
+    bool bad, filtered;
+    bool capped;       // the last bin holds tokens of weight 0 only
+    __device__ __forceinline__ int bin(float x) const {
+        const float d = ((float)W.top - x) * c;
+        return d < (float)(kBins - 1) ? (int)d : kBins - 1;
+    }
+};
+
+__device__ __forceinline__ RowPlan row_plan(const SampleArgs& a, const SampleSpace& w, int64_t r, int local, int slices) {
+    RowPlan R;
+    R.P = row_params(a, r);
+    uint32_t top = 0, low = 0xffffffffu, bad = 0;
+    R.valid = 0;
+    for (int s = 0; s < slices; ++s) {
+        const SliceStat t = w.stat[local * slices + s];
+        top = t.top > top ? t.top : top;
+        low = t.low < low ? t.low : low;
+        bad |= t.bad;
+        R.valid += t.valid;
+    }
+    R.bad = bad != 0 || R.P.code != 0 || R.valid == 0;
+    if (bad) R.P.code |= kDevErrLogit;
+    R.W.top = (double)value_of(top);
+    R.W.scale = 1.4426950408889634 / (double)R.P.tau;
+    R.W.shift = a.shift;
+    if (R.P.top_k <= 0 || (uint64_t)R.P.top_k >= R.valid) R.P.top_k = 0;
+    R.filtered = R.P.top_k > 0 || R.P.top_p < 1.0f || R.P.min_p > 0.0f;
+    // bins over the row's range, or over the 47 binary orders below the top that weights can tell apart
+    const double whole = R.W.top - (double)value_of(low), most = 47.0 / R.W.scale;
+    R.capped = whole > most;
+    const double range = R.capped ? most : whole;
+    R.c = range > 0.0 ? (float)__builtin_fmin((kBins - 1) / range, 1e38) : 0.0f;
+    return R;
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kRowThreads) void sample_scan_kernel(SampleArgs a, SampleSpace w, int64_t r0) {
+    __shared__ uint32_t s_top, s_low, s_bad, s_valid;
+    const int s = blockIdx.x, slices = gridDim.x, local = blockIdx.y;
+    if (threadIdx.x == 0) {
+        s_top = s_bad = s_valid = 0;
+        s_low = 0xffffffffu;
+        if (s == 0) w.listed[local] = 0;
+        if (s == 0 && local == 0 && r0 == 0) {
+            a.hdr[kHdrErrCode] = 0;
+            a.hdr[kHdrErrRow] = INT_MAX;
+            a.hdr[kHdrCount] = 0;
+        }
+    }
+    __syncthreads();
+    const Row<F32> row(a.logits, r0 + local, a.ld, a.vocab);
+    const int64_t nvec = row.vectors();
+    uint32_t top = 0, low = 0xffffffffu, bad = 0, valid = 0;
+    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](float x, int64_t) {
+        bad |= !(x < __builtin_huge_valf());   // NaN, +infinity
+        const uint32_t key = key_of(x);
+        const bool in = key > kMaskedKey;
+        top = in && key > top ? key : top;
+        low = in && key < low ? key : low;
+        valid += in;
+    });
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const uint32_t t = __shfl_xor(top, m), l = __shfl_xor(low, m);
+        top = t > top ? t : top;
+        low = l < low ? l : low;
+        bad |= __shfl_xor(bad, m);
+        valid += __shfl_xor(valid, m);
+    }
+    if ((threadIdx.x & 63) == 0) {
+        atomicMax(&s_top, top);
+        atomicMin(&s_low, low);
+        atomicOr(&s_bad, bad);
+        atomicAdd(&s_valid, valid);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) w.stat[local * slices + s] = SliceStat{s_top, s_low, s_bad, s_valid};
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kRowThreads) void sample_hist_kernel(SampleArgs a, SampleSpace w, int64_t r0) {
+    __shared__ uint64_t hist[kBins];
+    __shared__ uint32_t count[kBins];
+    __shared__ uint64_t part[kRowWaves];
+    const int s = blockIdx.x, slices = gridDim.x, local = blockIdx.y;
+    const RowPlan R = row_plan(a, w, r0 + local, local, slices);
+    if (R.bad) return;
+    const bool counted = R.P.top_k > 0;
+    for (int i = threadIdx.x; i < kBins; i += kRowThreads) hist[i] = 0, count[i] = 0;
+    __syncthreads();
+    const Row<F32> row(a.logits, r0 + local, a.ld, a.vocab);
+    const int64_t nvec = row.vectors();
+    uint64_t total = 0;
+    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](float x, int64_t) {
+        if (!(x > -__builtin_huge_valf())) return;
+        const uint64_t v = R.W.of(x);
+        total += v;
+        if (R.filtered) {
+            const int b = R.bin(x);
+            atomicAdd((unsigned long long*)&hist[b], (unsigned long long)v);
+            if (counted) atomicAdd(&count[b], 1u);
+        }
+    });
+    total = wave_total(total);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = total;
+    __syncthreads();
+    const int64_t at = (int64_t)local * slices + s;
+    if (threadIdx.x == 0) {
+        uint64_t t = 0;
+        for (int i = 0; i < kRowWaves; ++i) t += part[i];
+        w.total[at] = t;
+    }
+    if (!R.filtered) return;
+    for (int i = threadIdx.x; i < kBins; i += kRowThreads) {
+        w.weight[at * kBins + i] = hist[i];
+        if (counted) w.count[at * kBins + i] = count[i];
+    }
+}
+
+// The bins in which the kept prefix may end: lo .. lim, and bk, top-k's own
+// (-1: none; needed beyond lim where top-p refers to what top-k keeps). Every
+// token in a bin below lo is kept, none above lim (lo > lim: none is undecided). Leaves the row's exclusive
+// running weight in S.hist and, with top-k, its running count in S.ties.
+struct Borders {
+    int lo, lim, bk;
+    uint64_t all;
+};
+
+__device__ Borders borders(const RowPlan& R, const SampleSpace& w, int local, int slices, Shared& S) {
+    const int b = 2 * threadIdx.x;
+    const bool counted = R.P.top_k > 0;
+    uint64_t h0 = 0, h1 = 0, c0 = 0, c1 = 0;
+    for (int s = 0; s < slices; ++s) {
+        const int64_t at = ((int64_t)local * slices + s) * kBins + b;
+        const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(w.weight + at);
+        h0 += h.x, h1 += h.y;
+        if (counted) {
+            const uint2 c = *reinterpret_cast<const uint2*>(w.count + at);
+            c0 += c.x, c1 += c.y;
+        }
+    }
+    Borders B;
+    uint64_t n;
+    const uint64_t ew = block_scan(h0 + h1, S, B.all);
+    __syncthreads();
+    S.hist[b] = ew, S.hist[b + 1] = ew + h0;
+    if (threadIdx.x == 0) S.found_bin = kBins;
+    __syncthreads();
+    B.bk = -1;
+    uint64_t w_lo = B.all, w_hi = B.all;
+    if (counted) {
+        const uint64_t k = (uint64_t)R.P.top_k;
+        const uint64_t ec = block_scan(c0 + c1, S, n);
+        S.ties[b] = (uint32_t)ec, S.ties[b + 1] = (uint32_t)(ec + c0);
+        if (ec < k && ec + c0 + c1 >= k) S.found_bin = ec + c0 >= k ? b : b + 1;
+        __syncthreads();
+        B.bk = (int)S.found_bin;
+        // a border among tokens of weight 0 decides nothing
+        if (R.capped && B.bk == kBins - 1) B.bk = -1;
+        if (B.bk >= 0) {
+            w_lo = S.hist[B.bk];
+            w_hi = B.bk + 1 < kBins ? S.hist[B.bk + 1] : B.all;
+        }
+    }
+    B.lo = B.lim = kBins - 1;
+    if (B.bk >= 0) B.lo = B.lim = B.bk;
+    if (R.P.top_p < 1.0f) {
+        // the target lies between those of top-k's weight without and with its border bin
+        const uint64_t t0 = nucleus(R.P.top_p, w_lo > 0 ? w_lo : 1), t1 = nucleus(R.P.top_p, w_hi);
+        __syncthreads();
+        if (ew < t0 && ew + h0 + h1 >= t0) S.part[0] = ew + h0 >= t0 ? b : b + 1;
+        if (ew < t1 && ew + h0 + h1 >= t1) S.part[1] = ew + h0 >= t1 ? b : b + 1;
+        __syncthreads();
+        const int p0 = (int)S.part[0], p1 = (int)S.part[1];
+        B.lo = p0 < B.lo ? p0 : B.lo;
+        B.lim = p1 < B.lim ? p1 : B.lim;
+    }
+    if (R.P.min_p > 0.0f) {
+        // within one bin of where the weight falls to min_p (float rounding of bin())
+        const double d = -log2((double)R.P.min_p) / R.W.scale * (double)R.c;
+        const int m = d < (double)kBins ? (int)d : kBins;
+        B.lo = m - 1 < B.lo ? (m > 0 ? m - 1 : 0) : B.lo;
+        B.lim = m + 1 < B.lim ? m + 1 : B.lim;
+    }
+    if (R.capped && B.lim == kBins - 1) B.lim = kBins - 2;
+    __syncthreads();
+    return B;
+}
+
+__global__ __launch_bounds__(kRowThreads) void sample_border_kernel(SampleArgs a, SampleSpace w, int64_t r0, int slices) {
+    __shared__ Shared S;
+    const int local = blockIdx.x;
+    const RowPlan R = row_plan(a, w, r0 + local, local, slices);
+    if (R.bad || !R.filtered) return;
+    const Borders B = borders(R, w, local, slices, S);
+    for (int i = threadIdx.x; i < kBins; i += kRowThreads) {
+        w.run_weight[(int64_t)local * kBins + i] = S.hist[i];
+        if (R.P.top_k > 0) w.run_count[(int64_t)local * kBins + i] = S.ties[i];
+    }
+    if (threadIdx.x == 0) w.borders[local] = B;
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kRowThreads) void sample_gather_kernel(SampleArgs a, SampleSpace w, int64_t r0) {
+    __shared__ uint64_t found[kList];
+    __shared__ uint32_t n_found, at0;
+    const int s = blockIdx.x, slices = gridDim.x, local = blockIdx.y;
+    const RowPlan R = row_plan(a, w, r0 + local, local, slices);
+    if (R.bad || !R.filtered) return;
+    if (threadIdx.x == 0) n_found = 0;
+    const Borders B = w.borders[local];
+    __syncthreads();
+    const int extra = R.P.top_p < 1.0f ? B.bk : -1;
+    const Row<F32> row(a.logits, r0 + local, a.ld, a.vocab);
+    const int64_t nvec = row.vectors();
+    // the bins' tokens go to LDS first: one global atomic a workgroup
+    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](float x, int64_t pos) {
+        if (!(x > -__builtin_huge_valf())) return;
+        const int b = R.bin(x);
+        if ((b >= B.lo && b <= B.lim) || b == extra) {
+            const uint32_t at = atomicAdd(&n_found, 1u);
+            if (at < kList) found[at] = (uint64_t)(~key_of(x)) << 32 | (uint32_t)(pos - row.off);
+        }
+    });
+    __syncthreads();
+    const uint32_t n = n_found;
+    if (n == 0) return;
+    if (threadIdx.x == 0) at0 = atomicAdd(&w.listed[local], n);
+    __syncthreads();
+    uint64_t* list = w.list + (int64_t)local * kList;
+    const uint32_t first = at0;
+    for (uint32_t i = threadIdx.x; i < n && i < kList && first + i < kList; i += kRowThreads) list[first + i] = found[i];
+}
+
+struct PickShared {
+    Shared S;
+    uint64_t list[kList];     // sorted: descending logit, ascending token
+    uint64_t before[kList];   // running weight of the list
+    int first[kBins];         // first list position of a bin
+    uint64_t slice[kMaxSlices + 1];
+    uint64_t zk;
+    int last, done;
+};
+
+// Ascending bitonic sort in LDS; size a power of two.
+__device__ __forceinline__ void sort_list(uint64_t* list, int size) {
+    for (int k = 2; k <= size; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            for (int i = threadIdx.x; i < size / 2; i += kRowThreads) {
+                const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+                const uint64_t x = list[lo], y = list[hi];
+                if ((x > y) == ((lo & k) == 0)) list[lo] = y, list[hi] = x;
+            }
+            __syncthreads();
+        }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, SampleSpace w, int64_t r0, int slices) {
+    constexpr int kPer = Row<F32>::kPer;
+    __shared__ PickShared L;
+    Shared& S = L.S;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, local = blockIdx.x;
+    const int64_t r = r0 + local;
+    const RowPlan R = row_plan(a, w, r, local, slices);
+    if (R.bad) {
+        if (tid == 0) {
+            a.token[r] = -1;
+            if (a.logprob != nullptr) a.logprob[r] = R.P.code != 0 ? __builtin_nanf("") : 0.0f;
+            if (R.P.code != 0) {
+                atomicOr(a.hdr + kHdrErrCode, R.P.code);
+                atomicMin(a.hdr + kHdrErrRow, (int32_t)r);
+            }
+        }
+        return;
+    }
+    const Row<F32> row(a.logits, r, a.ld, a.vocab);
+    const int64_t nvec = row.vectors();
+    const uint64_t floor_w = weight_floor(R.P.min_p, R.W.shift);
+    // a token is kept in bins below `lim`, and in `lim` up to `end` in the list's order
+    int lim = kBins;
+    uint64_t end = 0, all = 0;
+    if (!R.filtered) {
+        for (int s = 0; s < slices; ++s) all += w.total[(int64_t)local * slices + s];
+    } else {
+        const uint32_t listed = w.listed[local];
+        if (listed > kList) {
+            whole_row<F32>(a, r, row, R.P, R.W, S);
+            return;
+        }
+        const Borders B = w.borders[local];
+        all = B.all;
+        for (int i = tid; i < kBins; i += kRowThreads) {
+            S.hist[i] = w.run_weight[(int64_t)local * kBins + i];
+            if (R.P.top_k > 0) S.ties[i] = w.run_count[(int64_t)local * kBins + i];
+        }
+        int size = 64;
+        while (size < (int)listed) size <<= 1;
+        for (int i = tid; i < size; i += kRowThreads) L.before[i] = i < (int)listed ? w.list[(int64_t)local * kList + i] : ~0ull;
+        if (tid == 0) L.last = -1;
+        __syncthreads();
+        if (listed <= 512) {
+            // each thread counts what comes before its entry (all entries differ)
+            if (tid < (int)listed) {
+                int rank = 0;
+                const uint64_t mine = L.before[tid];
+#pragma unroll 8
+                for (int i = 0; i < (int)listed; ++i) rank += L.before[i] < mine;
+                L.list[rank] = mine;
+            }
+            __syncthreads();
+        } else {
+            for (int i = tid; i < size; i += kRowThreads) L.list[i] = L.before[i];
+            __syncthreads();
+            sort_list(L.list, size);
+        }
+        // running weight of the list: four consecutive entries a thread
+        const int p0 = 4 * tid;
+        uint64_t v[4], sum = 0;
+        int bin[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = p0 + i < (int)listed;
+            const float x = value_of(~(uint32_t)((in ? L.list[p0 + i] : 0) >> 32));
+            v[i] = in ? R.W.of(x) : 0;
+            bin[i] = in ? R.bin(x) : -1;
+            sum += v[i];
+        }
+        uint64_t total;
+        uint64_t run = block_scan(sum, S, total);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (bin[i] >= 0) {
+                const int p = p0 + i;
+                L.before[p] = run;
+                run += v[i];
+                const float px = p > 0 ? value_of(~(uint32_t)(L.list[p - 1] >> 32)) : 0.0f;
+                if (p == 0 || R.bin(px) != bin[i]) L.first[bin[i]] = p;
+            }
+        __syncthreads();
+        // what top-k keeps, then the three rules for each listed token
+        uint64_t in_bk = 0;
+        const uint64_t k = (uint64_t)R.P.top_k;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (bin[i] >= 0 && bin[i] == B.bk && S.ties[B.bk] + (uint64_t)(p0 + i - L.first[B.bk]) < k) in_bk += v[i];
+        block_scan(in_bk, S, total);
+        const uint64_t zk = B.bk >= 0 ? S.hist[B.bk] + total : all;
+        const uint64_t target = R.P.top_p < 1.0f ? nucleus(R.P.top_p, zk) : ~0ull;
+        int last = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (bin[i] >= 0) {
+                const int p = p0 + i, f = L.first[bin[i]];
+                const bool rank_ok = B.bk < 0 || S.ties[bin[i]] + (uint64_t)(p - f) < k;
+                const bool sum_ok = S.hist[bin[i]] + (L.before[p] - L.before[f]) < target;
+                if (rank_ok && sum_ok && v[i] >= floor_w) last = p;
+            }
+        if (last >= 0) atomicMax(&L.last, last);
+        __syncthreads();
+        last = L.last;
+        lim = B.lo;   // nothing listed is kept: the prefix ends before the listed bins
+        if (last >= 0) {
+            end = L.list[last];
+            lim = R.bin(value_of(~(uint32_t)(end >> 32)));
+        }
+        // kept weight of each slice: its bins below lim, and the listed tokens of lim
+        for (int s = wave; s < slices; s += kRowWaves) {
+            uint64_t t = 0;
+            for (int b = lane; b < lim; b += 64) t += w.weight[((int64_t)local * slices + s) * kBins + b];
+            t = wave_total(t);
+            if (lane == 0) L.slice[s] = t;
+        }
+        __syncthreads();
+        if (last >= 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (bin[i] == lim && p0 + i <= last) {
+                    const int64_t vec = ((int64_t)(uint32_t)L.list[p0 + i] + row.off) / kPer;
+                    int s = (int)(vec * slices / nvec);
+                    while (s + 1 < slices && vec >= nvec * (s + 1) / slices) ++s;
+                    while (s > 0 && vec < nvec * s / slices) --s;
+                    atomicAdd((unsigned long long*)&L.slice[s], (unsigned long long)v[i]);
+                }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        uint64_t total = 0;
+        for (int s = 0; s < slices; ++s) {
+            if (!R.filtered) L.slice[s] = w.total[(int64_t)local * slices + s];
+            total += L.slice[s];
+        }
+        uint64_t goal = (uint64_t)((double)R.P.u * (double)total);
+        goal = goal < total ? goal : total - 1;
+        uint64_t before = 0;
+        int s = 0;
+        while (before + L.slice[s] <= goal) before += L.slice[s++];
+        S.found_bin = s;
+        S.found_above = goal - before;   // the goal within the slice
+    }
+    __syncthreads();
+    const int s = (int)S.found_bin;
+    uint64_t goal = S.found_above;
+    const int64_t k0 = nvec * s / slices, k1 = nvec * (s + 1) / slices;
+    auto weigh = [&](float x, int64_t pos) -> uint64_t {
+        if (!(x > -__builtin_huge_valf())) return 0;
+        if (lim < kBins) {
+            const int b = R.bin(x);
+            if (b > lim) return 0;
+            if (b == lim && ((uint64_t)(~key_of(x)) << 32 | (uint32_t)(pos - row.off)) > end) return 0;
+        }
+        return R.W.of(x);
+    };
+    // Narrow the slice down: its vectors in 16 runs, a wave each, the run in
+    // which the goal lies, again until 64 vectors are left for one wave.
+    int64_t lo = k0, hi = k1;
+    while (hi - lo > 64) {
+        const int64_t run = (hi - lo + kRowWaves - 1) / kRowWaves;
+        const int64_t e0 = lo + run * wave, e1 = e0 + run < hi ? e0 + run : hi;
+        uint64_t t = 0;
+        for (int64_t k = e0 + lane; k < e1; k += 4 * 64) {
+            float x[4][kPer];
+            row.template load4<64>(k, e1, x);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) t += weigh(x[q][i], (k + 64 * q) * kPer + i);
+        }
+        t = wave_total(t);
+        if (lane == 0) S.part[wave] = t;
+        __syncthreads();
+        int g = 0;
+        while (S.part[g] <= goal) goal -= S.part[g++];
+        lo += run * g;
+        hi = lo + run < hi ? lo + run : hi;
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    const int64_t k = lo + lane;
+    float x[kPer];
+    uint64_t v[kPer], mine = 0;
+    if (k < hi) {
+        row.load(k, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x[i] = -__builtin_huge_valf();
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        v[i] = weigh(x[i], k * kPer + i);
+        mine += v[i];
+    }
+    uint64_t c = wave_scan(mine) - mine;
+    if (c <= goal && c + mine > goal) {
+        int pick = kPer;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            c += v[i];
+            if (pick == kPer && c > goal) pick = i;
+        }
+        write_token(a, r, row, k * kPer + pick, R.W, R.P.tau, all);
+    }
+}
+
+#ifndef SL
+#define SL 4
+#endif
+int slices_of(int64_t rows) {
+    const int64_t s = SL * 256 / rows;   // workgroups for four to a compute unit
+    return (int)(s < 1 ? 1 : (s < kMaxSlices ? s : kMaxSlices));
+}
+
+template <bool F32>
+void sample_rows(const SampleArgs& a, const SampleSpace& w, hipStream_t s) {
+    const bool filters = a.row_top_k != nullptr || a.row_top_p != nullptr || a.row_min_p != nullptr || a.top_k > 0 ||
+                         (a.top_p > 0.0f && a.top_p < 1.0f) || a.min_p > 0.0f;
+    for (int64_t r0 = 0; r0 < a.n; r0 += kChunkRows) {
+        const int rows = (int)(a.n - r0 < kChunkRows ? a.n - r0 : kChunkRows);
+        const int slices = slices_of(rows);
+        const dim3 grid(slices, rows);
+        sample_scan_kernel<F32><<<grid, kRowThreads, 0, s>>>(a, w, r0);
+        sample_hist_kernel<F32><<<grid, kRowThreads, 0, s>>>(a, w, r0);
+        if (filters) sample_border_kernel<<<rows, kRowThreads, 0, s>>>(a, w, r0, slices);
+        if (filters) sample_gather_kernel<F32><<<grid, kRowThreads, 0, s>>>(a, w, r0);
+        sample_pick_kernel<F32><<<rows, kRowThreads, 0, s>>>(a, w, r0, slices);
+    }
+}
+
+// Regions after the header; returns the size.
+size_t carve(int64_t n, char* base, SampleSpace& w) {
+    const int64_t rows = n < 1 ? 1 : (n < kChunkRows ? n : kChunkRows);
+    // the most slices any set of up to `rows` rows has
+    int64_t parts = 0;
+    for (int64_t r = 1; r <= rows; ++r) parts = r * slices_of(r) > parts ? r * slices_of(r) : parts;
+    size_t off = 256;
+    auto take = [&](int64_t bytes) {
+        char* p = base + off;
+        off += (size_t)round_up(bytes, 256);
+        return p;
+    };
+    w.stat = (SliceStat*)take(parts * (int64_t)sizeof(SliceStat));
+    w.weight = (uint64_t*)take(8 * parts * kBins);
+    w.total = (uint64_t*)take(8 * parts);
+    w.count = (uint32_t*)take(4 * parts * kBins);
+    w.listed = (uint32_t*)take(4 * rows);
+    w.list = (uint64_t*)take(8 * rows * kList);
+    w.run_weight = (uint64_t*)take(8 * rows * kBins);
+    w.run_count = (uint32_t*)take(4 * rows * kBins);
+    w.borders = (Borders*)take(rows * (int64_t)sizeof(Borders));
+    return off;
+}
+
 }  // namespace
 
-void launch_sample(const SampleArgs& a, hipStream_t s) {
-    const int grid = grid_1d(a.n, 1, 1 << 20);
+size_t sample_workspace(int64_t n) {
+    SampleSpace w;
+    return carve(n, nullptr, w);
+}
+
+void launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
+    SampleSpace w;
+    carve(a.n, (char*)workspace, w);
     if (a.logits_f32)
-        sample_rows_kernel<true><<<grid, kRowThreads, 0, s>>>(a);
+        sample_rows<true>(a, w, s);
     else
-        sample_rows_kernel<false><<<grid, kRowThreads, 0, s>>>(a);
+        sample_rows<false>(a, w, s);
 }
 
 }  // namespace lmhead

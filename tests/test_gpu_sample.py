@@ -118,7 +118,8 @@ def test_bad_rows_and_the_error_word():
     x[3, 0] = float("inf")
     u2 = u.clone()
     u2[4], u2[5], u2[6] = 1.0, float("nan"), -0.1
-    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(lm.lmhead_sample_workspace_size(lm.lmhead_sample_problem(n, vocab, vocab, 1)), dtype=torch.uint8,
+                     device="cuda")
     token, lp = lm.sample(x, u2, top_p=0.9, ws=ws)
     bad = torch.tensor([2, 3, 4, 5, 6], device="cuda")
     assert (token[bad] == -1).all() and lp[bad].isnan().all()

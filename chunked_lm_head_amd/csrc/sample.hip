@@ -52,6 +52,15 @@ __device__ __forceinline__ float value_of(uint32_t key) {
     return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
+// a * b + c with the constant c in scalar registers. Given as a builtin, the
+// compiler copies every constant into vector registers before each use, one
+// move per multiply-add.
+__device__ __forceinline__ double fma_s(double a, double b, double c) {
+    double d;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+    return d;
+}
+
 // The row's weights: scaled(x) = 2^shift exp((x - top) / tau) as a double.
 // 2^d = 2^n (1 + r q(r)), r = d - n, |r| <= 1/2; q interpolates (2^r - 1) / r
 // at the nine Chebyshev nodes of the interval. The nearest integer n comes from
@@ -65,14 +74,14 @@ struct Weights {
         const double t = d + 0x1.8p52;
         const double r = d - (t - 0x1.8p52);
         double q = 0x1.b63880a30e9ffp-24;
-        q = __builtin_fma(q, r, 0x1.63d136366db24p-20);
-        q = __builtin_fma(q, r, 0x1.ffcb9515a8016p-17);
-        q = __builtin_fma(q, r, 0x1.4308ac85aa947p-13);
-        q = __builtin_fma(q, r, 0x1.5d87fe86fe88ep-10);
-        q = __builtin_fma(q, r, 0x1.3b2ab7181b755p-7);
-        q = __builtin_fma(q, r, 0x1.c6b08d7047e52p-5);
-        q = __builtin_fma(q, r, 0x1.ebfbdff823cedp-3);
-        q = __builtin_fma(q, r, 0x1.62e42fefa39efp-1);
+        q = fma_s(q, r, 0x1.63d136366db24p-20);
+        q = fma_s(q, r, 0x1.ffcb9515a8016p-17);
+        q = fma_s(q, r, 0x1.4308ac85aa947p-13);
+        q = fma_s(q, r, 0x1.5d87fe86fe88ep-10);
+        q = fma_s(q, r, 0x1.3b2ab7181b755p-7);
+        q = fma_s(q, r, 0x1.c6b08d7047e52p-5);
+        q = fma_s(q, r, 0x1.ebfbdff823cedp-3);
+        q = fma_s(q, r, 0x1.62e42fefa39efp-1);
         q = __builtin_fma(q, r, 1.0);
         const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t) + shift;
         return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, q) + ((uint64_t)(uint32_t)n << 52));
@@ -102,10 +111,14 @@ struct Row {
     // vectors k, k + STEP, k + 2 STEP, k + 3 STEP, those from k1 on as -infinity
     template <int STEP>
     __device__ __forceinline__ void load4(int64_t k, int64_t k1, float (&x)[4][kPer]) const {
-        if (k * kPer >= off && (k + 3 * STEP + 1) * kPer <= end && k + 3 * STEP < k1) {
+        const int64_t a0 = off > 0 ? 1 : 0, a1 = end / kPer;   // the vectors inside the row
+        if (a0 < a1) {
             uint4 v[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(base + (k + q * STEP) * 16);
+            for (int q = 0; q < 4; ++q) {
+                const int64_t kq = k + q * STEP;
+                v[q] = *reinterpret_cast<const uint4*>(base + (kq < a0 ? a0 : kq < a1 ? kq : a1 - 1) * 16);
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
@@ -119,19 +132,21 @@ struct Row {
                     }
                 }
             }
-            return;
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (k + q * STEP < k1) {
-                load(k + q * STEP, x[q]);
+            const int64_t kq = k + q * STEP;
+            if (kq < k1 && kq >= a0 && kq < a1) continue;
+            if (kq < k1) {
+                load(kq, x[q]);   // a ragged end
             } else {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) x[q][i] = -__builtin_huge_valf();
             }
         }
     }
-    // f(x, position) for this thread's share of vectors k0 .. k1 - 1, four loads in flight
+    // f(values, first position) for this thread's share of vectors k0 .. k1 - 1 (arrays of kPer values;
+    // of one at the row's ragged ends), four loads in flight
     template <class F>
     __device__ __forceinline__ void each(int64_t k0, int64_t k1, F f) const {
         const int64_t a0 = k0 == 0 && off > 0 ? 1 : k0;               // the vectors inside the row
@@ -148,22 +163,29 @@ struct Row {
             for (int q = 0; q < 4; ++q) {
                 const int64_t k = b + q * kRowThreads;
                 if (k >= a1) break;
+                float x[kPer];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (F32) {
-                        f(__builtin_bit_cast(float, w[q][i]), k * kPer + i);
+                        x[i] = __builtin_bit_cast(float, w[q][i]);
                     } else {
-                        f(__builtin_bit_cast(float, w[q][i] << 16), k * kPer + 2 * i);
-                        f(__builtin_bit_cast(float, w[q][i] & 0xffff0000u), k * kPer + 2 * i + 1);
+                        x[2 * i] = __builtin_bit_cast(float, w[q][i] << 16);
+                        x[2 * i + 1] = __builtin_bit_cast(float, w[q][i] & 0xffff0000u);
                     }
                 }
+                f(x, k * kPer);
             }
         }
         // the row's first and last positions outside whole vectors, one a thread
         const int64_t h1 = end < kPer ? end : kPer;
-        if (k0 == 0 && k1 > 0 && off > 0 && threadIdx.x < h1 - off) f(at(off + threadIdx.x), off + threadIdx.x);
+        if (k0 == 0 && k1 > 0 && off > 0 && threadIdx.x < h1 - off) one(f, off + threadIdx.x);
         const int64_t t0 = end / kPer * kPer;
-        if (k1 * kPer > end && (t0 > 0 || off == 0) && threadIdx.x < end - t0) f(at(t0 + threadIdx.x), t0 + threadIdx.x);
+        if (k1 * kPer > end && (t0 > 0 || off == 0) && threadIdx.x < end - t0) one(f, t0 + threadIdx.x);
+    }
+    template <class F>
+    __device__ __forceinline__ void one(F f, int64_t pos) const {
+        const float x[1] = {at(pos)};
+        f(x, pos);
     }
     __device__ __forceinline__ float at(int64_t pos) const {
         if (F32) return reinterpret_cast<const float*>(base)[pos];
@@ -498,31 +520,38 @@ struct SampleSpace {
 struct RowPlan {
     Weights W;
     Params P;
-    float c;           // bins per unit of logit below the top
+    float top, c;      // largest logit; bins per unit of logit below it
     uint64_t valid;
     bool bad, filtered;
     bool capped;       // the last bin holds tokens of weight 0 only
     __device__ __forceinline__ int bin(float x) const {
-        const float d = ((float)W.top - x) * c;
-        return d < (float)(kBins - 1) ? (int)d : kBins - 1;
+        return (int)__builtin_fminf((top - x) * c, (float)(kBins - 1));   // a NaN (0 times infinity) gives the last
     }
 };
+
+// Maximum (0), or (1), sum (2) over the 16 lanes of a row, as a uniform value.
+template <int OP>
+__device__ __forceinline__ uint32_t row_join(uint32_t v) {
+    auto join = [](uint32_t x, uint32_t y) { return OP == 0 ? (x > y ? x : y) : OP == 1 ? x | y : x + y; };
+    v = join(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));   // row_ror 8, 4, 2, 1
+    v = join(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+    v = join(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+    v = join(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
 
 __device__ __forceinline__ RowPlan row_plan(const SampleArgs& a, const SampleSpace& w, int64_t r, int local, int slices) {
     RowPlan R;
     R.P = row_params(a, r);
-    uint32_t top = 0, low = 0xffffffffu, bad = 0;
-    R.valid = 0;
-    for (int s = 0; s < slices; ++s) {
-        const SliceStat t = w.stat[local * slices + s];
-        top = t.top > top ? t.top : top;
-        low = t.low < low ? t.low : low;
-        bad |= t.bad;
-        R.valid += t.valid;
-    }
+    // a lane a slice, joined over the 16 lanes of a DPP row
+    const int lane = threadIdx.x & 15;
+    const SliceStat t = w.stat[local * slices + (lane < slices ? lane : 0)];
+    const uint32_t top = row_join<0>(t.top), low = ~row_join<0>(~t.low), bad = row_join<1>(t.bad);
+    R.valid = row_join<2>(lane < slices ? t.valid : 0);
     R.bad = bad != 0 || R.P.code != 0 || R.valid == 0;
     if (bad) R.P.code |= kDevErrLogit;
-    R.W.top = (double)value_of(top);
+    R.top = value_of(top);
+    R.W.top = (double)R.top;
     R.W.scale = 1.4426950408889634 / (double)R.P.tau;
     R.W.shift = a.shift;
     if (R.P.top_k <= 0 || (uint64_t)R.P.top_k >= R.valid) R.P.top_k = 0;
@@ -553,13 +582,16 @@ __global__ __launch_bounds__(kRowThreads) void sample_scan_kernel(SampleArgs a, 
     const Row<F32> row(a.logits, r0 + local, a.ld, a.vocab);
     const int64_t nvec = row.vectors();
     uint32_t top = 0, low = 0xffffffffu, bad = 0, valid = 0;
-    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](float x, int64_t) {
-        bad |= !(x < __builtin_huge_valf());   // NaN, +infinity
-        const uint32_t key = key_of(x);
-        const bool in = key > kMaskedKey;
-        top = in && key > top ? key : top;
-        low = in && key < low ? key : low;
-        valid += in;
+    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](auto& x, int64_t) {
+#pragma unroll
+        for (float v : x) {
+            bad |= !(v < __builtin_huge_valf());   // NaN, +infinity
+            const uint32_t key = key_of(v);
+            const bool in = key > kMaskedKey;
+            top = in && key > top ? key : top;
+            low = in && key < low ? key : low;
+            valid += in;
+        }
     });
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
@@ -593,13 +625,20 @@ __global__ __launch_bounds__(kRowThreads) void sample_hist_kernel(SampleArgs a, 
     const Row<F32> row(a.logits, r0 + local, a.ld, a.vocab);
     const int64_t nvec = row.vectors();
     uint64_t total = 0;
-    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](float x, int64_t) {
-        if (!(x > -__builtin_huge_valf())) return;
-        const uint64_t v = R.W.of(x);
-        total += v;
-        if (R.filtered) {
-            const int b = R.bin(x);
-            atomicAdd((unsigned long long*)&hist[b], (unsigned long long)v);
+    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](auto& x, int64_t) {
+        constexpr int N = sizeof(x) / 4;
+        uint64_t v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = R.W.of(x[i]);   // 0 for a masked token
+            total += v[i];
+        }
+        if (!R.filtered) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int b = R.bin(x[i]);
+            if (v[i] == 0) continue;
+            atomicAdd((unsigned long long*)&hist[b], (unsigned long long)v[i]);
             if (counted) atomicAdd(&count[b], 1u);
         }
     });
@@ -632,6 +671,7 @@ __device__ Borders borders(const RowPlan& R, const SampleSpace& w, int local, in
     const int b = 2 * threadIdx.x;
     const bool counted = R.P.top_k > 0;
     uint64_t h0 = 0, h1 = 0, c0 = 0, c1 = 0;
+#pragma unroll 4
     for (int s = 0; s < slices; ++s) {
         const int64_t at = ((int64_t)local * slices + s) * kBins + b;
         const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(w.weight + at);
@@ -657,8 +697,8 @@ __device__ Borders borders(const RowPlan& R, const SampleSpace& w, int local, in
         if (ec < k && ec + c0 + c1 >= k) S.found_bin = ec + c0 >= k ? b : b + 1;
         __syncthreads();
         B.bk = (int)S.found_bin;
-        // a border among tokens of weight 0 decides nothing
-        if (R.capped && B.bk == kBins - 1) B.bk = -1;
+        // only tokens that weigh something are counted: with fewer of them than k, top-k decides nothing
+        if (B.bk == kBins) B.bk = -1;
         if (B.bk >= 0) {
             w_lo = S.hist[B.bk];
             w_hi = B.bk + 1 < kBins ? S.hist[B.bk + 1] : B.all;
@@ -704,24 +744,40 @@ __global__ __launch_bounds__(kRowThreads) void sample_border_kernel(SampleArgs a
 
 template <bool F32>
 __global__ __launch_bounds__(kRowThreads) void sample_gather_kernel(SampleArgs a, SampleSpace w, int64_t r0) {
-    __shared__ uint64_t found[kList];
+    __shared__ uint64_t found[kList], below[kRowWaves];
     __shared__ uint32_t n_found, at0;
     const int s = blockIdx.x, slices = gridDim.x, local = blockIdx.y;
     const RowPlan R = row_plan(a, w, r0 + local, local, slices);
     if (R.bad || !R.filtered) return;
     if (threadIdx.x == 0) n_found = 0;
     const Borders B = w.borders[local];
+    // the slice's weight in the bins below lo, for the pick kernel
+    const int64_t at = (int64_t)local * slices + s;
+    {
+        uint64_t t = 0;
+        for (int b = threadIdx.x; b < B.lo; b += kRowThreads) t += w.weight[at * kBins + b];
+        t = wave_total(t);
+        if ((threadIdx.x & 63) == 0) below[threadIdx.x >> 6] = t;
+    }
     __syncthreads();
+    if (threadIdx.x == 0) {
+        uint64_t t = 0;
+#pragma unroll
+        for (int i = 0; i < kRowWaves; ++i) t += below[i];
+        w.total[at] = t;   // in the place of the slice's whole weight, which the border kernel has summed
+    }
     const int extra = R.P.top_p < 1.0f ? B.bk : -1;
     const Row<F32> row(a.logits, r0 + local, a.ld, a.vocab);
     const int64_t nvec = row.vectors();
     // the bins' tokens go to LDS first: one global atomic a workgroup
-    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](float x, int64_t pos) {
-        if (!(x > -__builtin_huge_valf())) return;
-        const int b = R.bin(x);
-        if ((b >= B.lo && b <= B.lim) || b == extra) {
+    row.each(nvec * s / slices, nvec * (s + 1) / slices, [&](auto& x, int64_t pos) {
+        constexpr int N = sizeof(x) / 4;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int b = R.bin(x[i]);
+            if (!((b >= B.lo && b <= B.lim) || b == extra) || !(x[i] > -__builtin_huge_valf())) continue;
             const uint32_t at = atomicAdd(&n_found, 1u);
-            if (at < kList) found[at] = (uint64_t)(~key_of(x)) << 32 | (uint32_t)(pos - row.off);
+            if (at < kList) found[at] = (uint64_t)(~key_of(x[i])) << 32 | (uint32_t)(pos + i - row.off);
         }
     });
     __syncthreads();
@@ -866,12 +922,14 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
             end = L.list[last];
             lim = R.bin(value_of(~(uint32_t)(end >> 32)));
         }
-        // kept weight of each slice: its bins below lim, and the listed tokens of lim
+        // kept weight of each slice: its bins below lo (from the gather kernel) and on to lim, and the
+        // listed tokens of lim
         for (int s = wave; s < slices; s += kRowWaves) {
+            const int64_t at = (int64_t)local * slices + s;
             uint64_t t = 0;
-            for (int b = lane; b < lim; b += 64) t += w.weight[((int64_t)local * slices + s) * kBins + b];
+            for (int b = B.lo + lane; b < lim; b += 64) t += w.weight[at * kBins + b];
             t = wave_total(t);
-            if (lane == 0) L.slice[s] = t;
+            if (lane == 0) L.slice[s] = w.total[at] + t;
         }
         __syncthreads();
         if (last >= 0)
@@ -904,14 +962,23 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     const int s = (int)S.found_bin;
     uint64_t goal = S.found_above;
     const int64_t k0 = nvec * s / slices, k1 = nvec * (s + 1) / slices;
-    auto weigh = [&](float x, int64_t pos) -> uint64_t {
-        if (!(x > -__builtin_huge_valf())) return 0;
-        if (lim < kBins) {
-            const int b = R.bin(x);
-            if (b > lim) return 0;
-            if (b == lim && ((uint64_t)(~key_of(x)) << 32 | (uint32_t)(pos - row.off)) > end) return 0;
+    // weights of a vector's kept tokens (0 for the others and for masked ones)
+    auto weigh = [&](const float (&x)[kPer], int64_t pos, uint64_t (&v)[kPer]) {
+        bool in[kPer], any = false;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = R.bin(x[i]);
+            const uint64_t entry = (uint64_t)(~key_of(x[i])) << 32 | (uint32_t)(pos + i - row.off);
+            in[i] = b < lim || (b == lim && entry <= end);
+            any |= in[i];
+            v[i] = 0;
         }
-        return R.W.of(x);
+        if (any)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const uint64_t w1 = R.W.of(x[i]);
+                v[i] = in[i] ? w1 : 0;
+            }
     };
     // Narrow the slice down: its vectors in 16 runs, a wave each, the run in
     // which the goal lies, again until 64 vectors are left for one wave.
@@ -924,9 +991,13 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
             float x[4][kPer];
             row.template load4<64>(k, e1, x);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q) {
+                if (k - lane + 64 * q >= e1) break;
+                uint64_t v[kPer];
+                weigh(x[q], (k + 64 * q) * kPer, v);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) t += weigh(x[q][i], (k + 64 * q) * kPer + i);
+                for (int i = 0; i < kPer; ++i) t += v[i];
+            }
         }
         t = wave_total(t);
         if (lane == 0) S.part[wave] = t;
@@ -947,11 +1018,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
 #pragma unroll
         for (int i = 0; i < kPer; ++i) x[i] = -__builtin_huge_valf();
     }
+    weigh(x, k * kPer, v);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        v[i] = weigh(x[i], k * kPer + i);
-        mine += v[i];
-    }
+    for (int i = 0; i < kPer; ++i) mine += v[i];
     uint64_t c = wave_scan(mine) - mine;
     if (c <= goal && c + mine > goal) {
         int pick = kPer;

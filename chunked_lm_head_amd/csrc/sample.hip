@@ -146,35 +146,27 @@ struct Row {
         }
     }
     // f(values, first position) for this thread's share of vectors k0 .. k1 - 1 (arrays of kPer values;
-    // of one at the row's ragged ends), four loads in flight
+    // of one at the row's ragged ends). One vector at a time: the waves of the other workgroups cover its
+    // load (256 rows of 151,936, histogram: 45 us; two or four at a time, or the next ones fetched ahead,
+    // 56 to 59 us)
     template <class F>
     __device__ __forceinline__ void each(int64_t k0, int64_t k1, F f) const {
         const int64_t a0 = k0 == 0 && off > 0 ? 1 : k0;               // the vectors inside the row
         const int64_t a1 = k1 * kPer > end ? end / kPer : k1;
-        for (int64_t b = a0 + threadIdx.x; b < a1; b += 4 * kRowThreads) {
-            uint32_t w[4][4];
+        for (int64_t k = a0 + threadIdx.x; k < a1; k += kRowThreads) {
+            const uint4 v = *reinterpret_cast<const uint4*>(base + k * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            float x[kPer];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t k = b + q * kRowThreads;
-                const uint4 v = *reinterpret_cast<const uint4*>(base + (k < a1 ? k : b) * 16);
-                w[q][0] = v.x, w[q][1] = v.y, w[q][2] = v.z, w[q][3] = v.w;
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t k = b + q * kRowThreads;
-                if (k >= a1) break;
-                float x[kPer];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (F32) {
-                        x[i] = __builtin_bit_cast(float, w[q][i]);
-                    } else {
-                        x[2 * i] = __builtin_bit_cast(float, w[q][i] << 16);
-                        x[2 * i + 1] = __builtin_bit_cast(float, w[q][i] & 0xffff0000u);
-                    }
+            for (int i = 0; i < 4; ++i) {
+                if (F32) {
+                    x[i] = __builtin_bit_cast(float, w[i]);
+                } else {
+                    x[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+                    x[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
                 }
-                f(x, k * kPer);
             }
+            f(x, k * kPer);
         }
         // the row's first and last positions outside whole vectors, one a thread
         const int64_t h1 = end < kPer ? end : kPer;
@@ -236,6 +228,16 @@ __device__ __forceinline__ uint64_t last_lane(uint64_t v) {
     return (uint64_t)hi << 32 | lo;
 }
 __device__ __forceinline__ uint64_t wave_total(uint64_t v) { return last_lane(wave_scan(v)); }
+
+// The lane at which the running sum of v passes the goal (it does), and the goal less the sum before it.
+__device__ __forceinline__ int lane_of(uint64_t v, uint64_t& goal) {
+    const uint64_t inc = wave_scan(v), before = inc - v;
+    const int at = __builtin_ctzll(__ballot(inc > goal));
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)before, at);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(before >> 32), at);
+    goal -= (uint64_t)hi << 32 | lo;
+    return at;
+}
 
 struct Shared {
     uint64_t hist[kBins];
@@ -795,6 +797,7 @@ struct PickShared {
     uint64_t list[kList];     // sorted: descending logit, ascending token
     uint64_t before[kList];   // running weight of the list
     int first[kBins];         // first list position of a bin
+    int rank[512];
     uint64_t slice[kMaxSlices + 1];
     uint64_t zk;
     int last, done;
@@ -838,9 +841,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     // a token is kept in bins below `lim`, and in `lim` up to `end` in the list's order
     int lim = kBins;
     uint64_t end = 0, all = 0;
-    if (!R.filtered) {
-        for (int s = 0; s < slices; ++s) all += w.total[(int64_t)local * slices + s];
-    } else {
+    if (R.filtered) {
         const uint32_t listed = w.listed[local];
         if (listed > kList) {
             whole_row<F32>(a, r, row, R.P, R.W, S);
@@ -858,14 +859,21 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
         if (tid == 0) L.last = -1;
         __syncthreads();
         if (listed <= 512) {
-            // each thread counts what comes before its entry (all entries differ)
-            if (tid < (int)listed) {
+            // an entry's rank is the number of entries before it (all differ); 1024 / size threads share the count
+            for (int i = tid; i < size; i += kRowThreads) L.rank[i] = 0;
+            __syncthreads();
+            const int e = tid & (size - 1), parts = kRowThreads / size;
+            const int each = ((int)listed + parts - 1) / parts, i0 = tid / size * each;
+            const int i1 = i0 + each < (int)listed ? i0 + each : (int)listed;
+            if (e < (int)listed) {
                 int rank = 0;
-                const uint64_t mine = L.before[tid];
+                const uint64_t mine = L.before[e];
 #pragma unroll 8
-                for (int i = 0; i < (int)listed; ++i) rank += L.before[i] < mine;
-                L.list[rank] = mine;
+                for (int i = i0; i < i1; ++i) rank += L.before[i] < mine;
+                atomicAdd(&L.rank[e], rank);
             }
+            __syncthreads();
+            if (tid < (int)listed) L.list[L.rank[tid]] = L.before[tid];
             __syncthreads();
         } else {
             for (int i = tid; i < size; i += kRowThreads) L.list[i] = L.before[i];
@@ -944,23 +952,13 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
                 }
         __syncthreads();
     }
-    if (tid == 0) {
-        uint64_t total = 0;
-        for (int s = 0; s < slices; ++s) {
-            if (!R.filtered) L.slice[s] = w.total[(int64_t)local * slices + s];
-            total += L.slice[s];
-        }
-        uint64_t goal = (uint64_t)((double)R.P.u * (double)total);
-        goal = goal < total ? goal : total - 1;
-        uint64_t before = 0;
-        int s = 0;
-        while (before + L.slice[s] <= goal) before += L.slice[s++];
-        S.found_bin = s;
-        S.found_above = goal - before;   // the goal within the slice
-    }
-    __syncthreads();
-    const int s = (int)S.found_bin;
-    uint64_t goal = S.found_above;
+    // the slice in which the goal lies, and the goal within it
+    const uint64_t sv = lane < slices ? (R.filtered ? L.slice[lane] : w.total[(int64_t)local * slices + lane]) : 0;
+    const uint64_t total = wave_total(sv);
+    if (!R.filtered) all = total;
+    uint64_t goal = (uint64_t)((double)R.P.u * (double)total);
+    goal = goal < total ? goal : total - 1;
+    const int s = lane_of(sv, goal);
     const int64_t k0 = nvec * s / slices, k1 = nvec * (s + 1) / slices;
     // weights of a vector's kept tokens (0 for the others and for masked ones)
     auto weigh = [&](const float (&x)[kPer], int64_t pos, uint64_t (&v)[kPer]) {
@@ -1002,9 +1000,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
         t = wave_total(t);
         if (lane == 0) S.part[wave] = t;
         __syncthreads();
-        int g = 0;
-        while (S.part[g] <= goal) goal -= S.part[g++];
-        lo += run * g;
+        lo += run * lane_of(lane < kRowWaves ? S.part[lane] : 0, goal);
         hi = lo + run < hi ? lo + run : hi;
         __syncthreads();
     }
@@ -1033,11 +1029,8 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     }
 }
 
-#ifndef SL
-#define SL 4
-#endif
 int slices_of(int64_t rows) {
-    const int64_t s = SL * 256 / rows;   // workgroups for four to a compute unit
+    const int64_t s = 4 * 256 / rows;   // four workgroups to a compute unit
     return (int)(s < 1 ? 1 : (s < kMaxSlices ? s : kMaxSlices));
 }
 

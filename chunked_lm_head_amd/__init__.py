@@ -150,8 +150,14 @@ def _p(x) -> Optional[int]:
     return int(x)
 
 
+# the current stream's handle without building a Stream object (2.7 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -326,7 +332,7 @@ def _on_device_of(arg: int):
         @functools.wraps(fn)
         def call(*args, **kwargs):
             t = args[arg] if len(args) > arg else None
-            if isinstance(t, torch.Tensor) and t.device.type == "cuda":
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch.cuda.current_device():
                 with torch.cuda.device(t.device):
                     return fn(*args, **kwargs)
             return fn(*args, **kwargs)

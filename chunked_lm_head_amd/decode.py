@@ -138,16 +138,25 @@ def lmhead_sample(p, logits, u, token, logprob, workspace, workspace_bytes, stre
 
 def _check_gpu(name, t, dtypes, shape, device=None):
     """A contiguous GPU tensor of one of the dtypes; None in shape: any size."""
+    # a call on one row is over in a few microseconds: the good case first, the reasons after
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous() and \
+            (device is None or t.device == device):
+        got = t.shape
+        if len(got) == len(shape):
+            for want, have in zip(shape, got):
+                if want is not None and want != have:
+                    break
+            else:
+                return
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name} must be a tensor on a GPU device")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on the inputs' device")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d).replace('torch.', '') for d in dtypes)}")
-    if t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have the shape {['any' if w is None else w for w in shape]}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must have the shape {['any' if w is None else w for w in shape]}")
 
 
 def _workspace(ws: Optional[torch.Tensor], nbytes: int, device, where: str) -> torch.Tensor:
@@ -162,7 +171,7 @@ def _workspace(ws: Optional[torch.Tensor], nbytes: int, device, where: str) -> t
 class NormOutputs(NamedTuple):
     y: Optional[torch.Tensor]              # bf16 [n, hidden]
     residual_out: Optional[torch.Tensor]   # bf16 [n, hidden], with a residual
-    rstd: torch.Tensor                     # fp32 [n]
+    rstd: Optional[torch.Tensor]           # fp32 [n]
     q: Optional[torch.Tensor]              # e4m3 [n, hidden]
     scale: Optional[torch.Tensor]          # fp32 [n, hidden / 128]
 
@@ -175,9 +184,10 @@ def _norm_problem(x, weight, eps, weight_offset):
 
 @_on_device_of(0)
 def rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0,
-                     out_bf16: bool = True, out_fp8: bool = False) -> NormOutputs:
+                     out_bf16: bool = True, out_fp8: bool = False, out_rstd: bool = True) -> NormOutputs:
     """RMS norm of the rows of x (+ residual): see lmhead_rms_norm_fwd. out_fp8
-    adds the 8-bit output with its scales, out_bf16=False leaves y out."""
+    adds the 8-bit output with its scales, out_bf16=False leaves y out,
+    out_rstd=False what only the backward needs."""
     p = _norm_problem(x, weight, eps, weight_offset)
     n, hidden = x.shape
     dev = x.device
@@ -190,7 +200,7 @@ def rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, weight_offset:
     y = torch.empty_like(x) if out_bf16 else None
     q = torch.empty(n, hidden, dtype=torch.float8_e4m3fn, device=dev) if out_fp8 else None
     scale = torch.empty(n, hidden // FP8_BLOCK, dtype=torch.float32, device=dev) if out_fp8 else None
-    rstd = torch.empty(n, dtype=torch.float32, device=dev)
+    rstd = torch.empty(n, dtype=torch.float32, device=dev) if out_rstd else None
     _ok(lmhead_rms_norm_fwd(p, x, residual, weight, r, y, q, scale, rstd), "lmhead_rms_norm_fwd")
     return NormOutputs(y, r, rstd, q, scale)
 
@@ -198,7 +208,7 @@ def rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, weight_offset:
 def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """The norm's 8-bit output for logits_fp8: (q e4m3 [n, hidden], scale fp32
     [n, hidden / 128], residual_out or None)."""
-    f = rms_norm_forward(x, weight, residual, eps, weight_offset, out_bf16=False, out_fp8=True)
+    f = rms_norm_forward(x, weight, residual, eps, weight_offset, out_bf16=False, out_fp8=True, out_rstd=False)
     return f.q, f.scale, f.residual_out
 
 

@@ -179,52 +179,86 @@ __global__ __launch_bounds__(group_threads(WAVES)) void rms_norm_bwd_kernel(Norm
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
         for (int c = 0; c < 8; ++c) dw[j].v[c] = 0.0f;
+    // The next row's operands are loaded while this one is reduced and written:
+    // with two workgroups to a compute unit the loads of one row alone do not
+    // cover the memory's latency (16,384 x 4096: 149 us without, 108 us with;
+    // 768 or 1024 workgroups: 116 and 121 us). Rows over 16 waves have no registers for it.
+    constexpr bool AHEAD = WAVES < 16, KEEP = AHEAD;
+    struct Operands {
+        uint4 dy[VPT], r[VPT], e[AHEAD ? VPT : 1];
+        float rstd;
+    };
+    const bool want_e = a.dx != nullptr && a.dresidual != nullptr;
+    auto load = [&](Operands& o, int64_t row0) {
+        const int64_t row = row0 + slot;
+        const int64_t base = (row < a.n ? row : a.n - 1) * nv;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = t + j * LANES;
+            o.dy[j] = o.r[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (AHEAD) o.e[AHEAD ? j : 0] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < nv && row < a.n) {
+                o.dy[j] = reinterpret_cast<const uint4*>(a.dy)[base + i];
+                o.r[j] = reinterpret_cast<const uint4*>(a.r)[base + i];
+                if (AHEAD && want_e) o.e[AHEAD ? j : 0] = reinterpret_cast<const uint4*>(a.dresidual)[base + i];
+            }
+        }
+        o.rstd = a.rstd[row < a.n ? row : a.n - 1];
+    };
+    // o + w of the lane's columns: kept where the registers allow it
+    F8 wk[KEEP ? VPT : 1];
+    auto weights = [&](int j) {
+        const int i = t + j * LANES;
+        F8 w = load_weight8(a.weight, a.weight_f32, i < nv ? i : 0);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w.v[c] += a.offset;
+        return w;
+    };
+    if (KEEP)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) wk[j] = weights(j);
     int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < a.n; row0 += (int64_t)a.groups * ROWS) {
+    Operands cur, nxt;
+    const int64_t stride = (int64_t)a.groups * ROWS;
+    int64_t row0 = (int64_t)blockIdx.x * ROWS;
+    if (AHEAD && row0 < a.n) load(cur, row0);
+    for (; row0 < a.n; row0 += stride) {
         const int64_t row = row0 + slot;
         const bool live = row < a.n;
         const int64_t base = (live ? row : a.n - 1) * nv;
-        uint4 dy[VPT], r[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int i = t + j * LANES;
-            dy[j] = r[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < nv && live) {
-                dy[j] = reinterpret_cast<const uint4*>(a.dy)[base + i];
-                r[j] = reinterpret_cast<const uint4*>(a.r)[base + i];
-            }
-        }
-        const float rstd = a.rstd[live ? row : a.n - 1];
+        if (!AHEAD) load(cur, row0);
+        else if (row0 + stride < a.n) load(nxt, row0 + stride);
+        const float rstd = cur.rstd;
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int i = t + j * LANES;
-            const F8 d = unpack8(dy[j]), x = unpack8(r[j]), w = load_weight8(a.weight, a.weight_f32, i < nv ? i : 0);
+            const F8 d = unpack8(cur.dy[j]), x = unpack8(cur.r[j]), w = KEEP ? wk[j] : weights(j);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const float h = x.v[c] * rstd;
-                dot = __builtin_fmaf(d.v[c] * (a.offset + w.v[c]), h, dot);
+                dot = __builtin_fmaf(d.v[c] * w.v[c], h, dot);
                 dw[j].v[c] = __builtin_fmaf(d.v[c], h, dw[j].v[c]);
             }
         }
-        if (a.dx == nullptr) continue;
-        const float mean = row_sum<WAVES>(dot, red, wave, turn) * inv_h;
+        if (a.dx != nullptr) {
+            const float mean = row_sum<WAVES>(dot, red, wave, turn) * inv_h;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int i = t + j * LANES;
-            if (i >= nv || !live) continue;
-            const F8 d = unpack8(dy[j]), x = unpack8(r[j]), w = load_weight8(a.weight, a.weight_f32, i);
-            F8 o;
+            for (int j = 0; j < VPT; ++j) {
+                const int i = t + j * LANES;
+                if (i >= nv || !live) continue;
+                const F8 d = unpack8(cur.dy[j]), x = unpack8(cur.r[j]), w = KEEP ? wk[j] : weights(j);
+                F8 o;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                o.v[c] = rstd * (d.v[c] * (a.offset + w.v[c]) - x.v[c] * rstd * mean);
-            if (a.dresidual != nullptr) {
-                const F8 e = unpack8(reinterpret_cast<const uint4*>(a.dresidual)[base + i]);
+                for (int c = 0; c < 8; ++c) o.v[c] = rstd * (d.v[c] * w.v[c] - x.v[c] * rstd * mean);
+                if (want_e) {
+                    const F8 e = unpack8(AHEAD ? cur.e[AHEAD ? j : 0] : reinterpret_cast<const uint4*>(a.dresidual)[base + i]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) o.v[c] += e.v[c];
+                    for (int c = 0; c < 8; ++c) o.v[c] += e.v[c];
+                }
+                reinterpret_cast<uint4*>(a.dx)[base + i] = pack8(o);
             }
-            reinterpret_cast<uint4*>(a.dx)[base + i] = pack8(o);
         }
+        if (AHEAD) cur = nxt;
     }
     if (a.partial == nullptr) return;
     // the row slots' sums in order, then one row of partials per workgroup

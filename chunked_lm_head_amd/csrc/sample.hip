@@ -960,14 +960,18 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     goal = goal < total ? goal : total - 1;
     const int s = lane_of(sv, goal);
     const int64_t k0 = nvec * s / slices, k1 = nvec * (s + 1) / slices;
-    // weights of a vector's kept tokens (0 for the others and for masked ones)
+    // Weights of a vector's kept tokens (0 for the others and for masked ones).
+    // With a last kept token in the list, the kept ones are those at or before
+    // it in the list's order: a larger logit, or an equal one and no larger an
+    // index (the bins need not be made again). Without one, the bins below lim.
+    const bool by_end = lim == kBins || end != 0;
+    const float x_end = lim == kBins ? -__builtin_huge_valf() : value_of(~(uint32_t)(end >> 32));
+    const int64_t p_end = lim == kBins ? -1 : (int64_t)(uint32_t)end + row.off;
     auto weigh = [&](const float (&x)[kPer], int64_t pos, uint64_t (&v)[kPer]) {
         bool in[kPer], any = false;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int b = R.bin(x[i]);
-            const uint64_t entry = (uint64_t)(~key_of(x[i])) << 32 | (uint32_t)(pos + i - row.off);
-            in[i] = b < lim || (b == lim && entry <= end);
+            in[i] = by_end ? x[i] > x_end || (x[i] == x_end && pos + i <= p_end) : R.bin(x[i]) < lim;
             any |= in[i];
             v[i] = 0;
         }

@@ -184,7 +184,7 @@ int lmhead_logits_fp8(const lmhead_fp8_problem* p, const void* a, const float* a
 }
 
 size_t lmhead_sample_workspace_size(const lmhead_sample_problem* p) {
-    return validate(p) == LMHEAD_OK ? sample_workspace(p->n) : 0;
+    return validate(p) == LMHEAD_OK ? sample_workspace(p->n, p->vocab) : 0;
 }
 
 int lmhead_sample(const lmhead_sample_problem* p, const void* logits, const float* u, int32_t* token,

@@ -78,7 +78,7 @@ struct SampleArgs {
     int32_t* hdr;
     int shift;   // weights are integers of 2^-shift
 };
-size_t sample_workspace(int64_t n);
+size_t sample_workspace(int64_t n, int64_t vocab);
 void launch_sample(const SampleArgs& a, void* workspace, hipStream_t s);
 
 }  // namespace lmhead

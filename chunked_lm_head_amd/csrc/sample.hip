@@ -983,9 +983,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
             }
     };
     // Narrow the slice down: its vectors in 16 runs, a wave each, the run in
-    // which the goal lies, again until 64 vectors are left for one wave.
+    // which the goal lies, again until a vector a thread is left.
     int64_t lo = k0, hi = k1;
-    while (hi - lo > 64) {
+    while (hi - lo > kRowThreads) {
         const int64_t run = (hi - lo + kRowWaves - 1) / kRowWaves;
         const int64_t e0 = lo + run * wave, e1 = e0 + run < hi ? e0 + run : hi;
         uint64_t t = 0;
@@ -1008,8 +1008,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
         hi = lo + run < hi ? lo + run : hi;
         __syncthreads();
     }
-    if (wave != 0) return;
-    const int64_t k = lo + lane;
+    const int64_t k = lo + tid;
     float x[kPer];
     uint64_t v[kPer], mine = 0;
     if (k < hi) {
@@ -1021,7 +1020,11 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     weigh(x, k * kPer, v);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) mine += v[i];
-    uint64_t c = wave_scan(mine) - mine;
+    const uint64_t inc = wave_scan(mine);
+    if (lane == 63) S.part[wave] = inc;
+    __syncthreads();
+    if (wave != lane_of(lane < kRowWaves ? S.part[lane] : 0, goal)) return;
+    uint64_t c = inc - mine;
     if (c <= goal && c + mine > goal) {
         int pick = kPer;
 #pragma unroll
@@ -1033,8 +1036,15 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     }
 }
 
-int slices_of(int64_t rows) {
-    const int64_t s = 4 * 256 / rows;   // four workgroups to a compute unit
+// Workgroups a row: four to a compute unit over all rows, each with some
+// kSliceTokens tokens at least (a slice costs its histogram's traffic and its
+// share of the row's; 64 rows of 128,256: 8 slices 73 us, 16 slices 81 us; 256
+// rows of 151,936: 4 slices 156 us, 2 slices 179 us, 8 slices 167 us).
+constexpr int64_t kSliceTokens = 16384;
+int slices_of(int64_t rows, int64_t vocab) {
+    int64_t s = 4 * 256 / rows;
+    const int64_t most = cdiv(vocab, kSliceTokens);
+    s = s < most ? s : most;
     return (int)(s < 1 ? 1 : (s < kMaxSlices ? s : kMaxSlices));
 }
 
@@ -1044,7 +1054,7 @@ void sample_rows(const SampleArgs& a, const SampleSpace& w, hipStream_t s) {
                          (a.top_p > 0.0f && a.top_p < 1.0f) || a.min_p > 0.0f;
     for (int64_t r0 = 0; r0 < a.n; r0 += kChunkRows) {
         const int rows = (int)(a.n - r0 < kChunkRows ? a.n - r0 : kChunkRows);
-        const int slices = slices_of(rows);
+        const int slices = slices_of(rows, a.vocab);
         const dim3 grid(slices, rows);
         sample_scan_kernel<F32><<<grid, kRowThreads, 0, s>>>(a, w, r0);
         sample_hist_kernel<F32><<<grid, kRowThreads, 0, s>>>(a, w, r0);
@@ -1055,11 +1065,11 @@ void sample_rows(const SampleArgs& a, const SampleSpace& w, hipStream_t s) {
 }
 
 // Regions after the header; returns the size.
-size_t carve(int64_t n, char* base, SampleSpace& w) {
+size_t carve(int64_t n, int64_t vocab, char* base, SampleSpace& w) {
     const int64_t rows = n < 1 ? 1 : (n < kChunkRows ? n : kChunkRows);
     // the most slices any set of up to `rows` rows has
     int64_t parts = 0;
-    for (int64_t r = 1; r <= rows; ++r) parts = r * slices_of(r) > parts ? r * slices_of(r) : parts;
+    for (int64_t r = 1; r <= rows; ++r) parts = r * slices_of(r, vocab) > parts ? r * slices_of(r, vocab) : parts;
     size_t off = 256;
     auto take = [&](int64_t bytes) {
         char* p = base + off;
@@ -1080,14 +1090,14 @@ size_t carve(int64_t n, char* base, SampleSpace& w) {
 
 }  // namespace
 
-size_t sample_workspace(int64_t n) {
+size_t sample_workspace(int64_t n, int64_t vocab) {
     SampleSpace w;
-    return carve(n, nullptr, w);
+    return carve(n, vocab, nullptr, w);
 }
 
 void launch_sample(const SampleArgs& a, void* workspace, hipStream_t s) {
     SampleSpace w;
-    carve(a.n, (char*)workspace, w);
+    carve(a.n, a.vocab, (char*)workspace, w);
     if (a.logits_f32)
         sample_rows<true>(a, w, s);
     else

@@ -150,7 +150,7 @@ int lmhead_quantize_fp8(int64_t rows, int64_t cols, int32_t block_rows, const vo
 }
 
 size_t lmhead_logits_fp8_workspace_size(const lmhead_fp8_problem* p) {
-    return validate(p) == LMHEAD_OK ? logits_workspace(p->n, (int)p->hidden) : 0;
+    return validate(p) == LMHEAD_OK ? logits_workspace(p->n, (int)p->hidden, p->out_dtype == LMHEAD_DTYPE_F32) : 0;
 }
 
 int lmhead_logits_fp8(const lmhead_fp8_problem* p, const void* a, const float* a_scale, const void* w,

@@ -59,7 +59,7 @@ struct LogitsArgs {
     int64_t n, vocab, ld;
     int hidden;
 };
-size_t logits_workspace(int64_t n, int hidden);
+size_t logits_workspace(int64_t n, int hidden, int out_f32);
 void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s);
 
 // -------------------------------------------------------------- sample.hip

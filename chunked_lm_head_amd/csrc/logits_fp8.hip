@@ -284,8 +284,7 @@ void stream_by_share(const LogitsArgs& a, const uint8_t* packed, const float* sc
 
 // ------------------------------------------------------------- many rows
 
-constexpr int kTileRows = 256;       // input rows of a tile
-constexpr int kTileThreads = 512;    // eight waves: 2 along the vocabulary, 4 along the rows
+constexpr int kTileThreads = 512;    // eight waves: VW along the vocabulary, 8 / VW along the rows
 constexpr int kStages = 4;
 
 struct TileArgs {
@@ -295,7 +294,8 @@ struct TileArgs {
     int64_t n_pad, tiles_n, tiles_v;
 };
 
-// One workgroup: 256 input rows x 32 VI vocabulary rows (2 VI fragments of 16).
+// One workgroup: 64 * 8 / VW input rows x 16 VI VW vocabulary rows; a wave has
+// 64 x 16 VI of them.
 // W goes through LDS: one 128-column step of the tile is rows of 128 bytes,
 // 16-byte chunk q of row r at q ^ ((r >> 1) & 7) (conflict-free fragment
 // reads), written by LDS-direct buffer loads, four steps in a ring. The rows'
@@ -304,14 +304,15 @@ struct TileArgs {
 // then the W loads of step b + 3: waiting for the former at the next step's start leaves
 // only the latter in flight, so W of step b + 1 has landed for every wave that
 // has begun step b, and one barrier per step is enough.
-template <bool EXACT, int VI>
+template <bool EXACT, int VI, int VW>
 __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t) {
-    constexpr int kV = 32 * VI, kStage = kV * 128, kLoads = kStage / (kTileThreads * 16);
+    static_assert(VI == 8 || VI == 4, "a step's loads are spread over eight (half) groups");
+    constexpr int kV = 16 * VI * VW, kRows = 64 * (8 / VW), kStage = kV * 128, kLoads = kStage / (kTileThreads * 16);
     __shared__ __attribute__((aligned(16))) char smem[kStages * kStage];
     const LogitsArgs& a = t.p;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wv = wave & 1, wn = wave >> 1;
+    const int wv = wave % VW, wn = wave / VW;
     const int c = lane & 15, g = lane >> 4;
     int64_t tn, tv;
     map_tile(blockIdx.x, t.tiles_n, t.tiles_v, tn, tv);
@@ -340,7 +341,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void_t*)(stage + (wave * kLoads + u) * 1024), 16, vw[u & 1],
                                                      (uint32_t)(u * 8 * a.hidden + bc * kQBlock), 0, 0);
     };
-    const int64_t i0 = tn * kTileRows + wn * 64;
+    const int64_t i0 = tn * kRows + wn * 64;
     const uint8_t* rows = t.rows + (i0 / 16) * nb * 2048 + lane * 16;
     const float* sat = t.scale_t + i0 + 4 * c;
     // a wave's rows of W share a scale block; where they lie past the vocabulary they are
@@ -428,7 +429,8 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
                     z[i & 1][j] = block_sum(ww, wx[j]);
                     if (j == 0 && i + 1 < VI) fw = w_frag(i + 1);
                     if (i > 0) add(i - 1, j);
-                    if (j == 2) issue(i);
+                    if (VI == 8 && j == 2) issue(i);
+                    if (VI == 4 && (j & 1)) issue(2 * i + (j >> 1));
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -469,37 +471,51 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
 
 }  // namespace
 
-// rows padded for the packed copy: none up to 16
-int64_t packed_rows(int64_t n) { return n <= 16 ? 0 : round_up(n, n <= kStreamRows ? 16 : kTileRows); }
+// Rows of a matrix tile. An fp32 output's tile of 128 rows x 256 columns takes
+// half the time of one of 256 x 128 per row, so 128 wherever 256 would leave the
+// last half tile empty (us at 151,936 x 4096, 128 against 256 rows a tile: n =
+// 128: 200, 291; 256: 336, 331; 300: 455, 593; 2048: 2388, 2349). A bf16
+// output's larger 256 x 256 tile reads less per product and loses to 128 only
+// when one tile holds all rows (n = 128: 186, 202; 200: 254, 208; 300: 331, 306).
+int64_t tile_rows(int64_t n, int out_f32) {
+    if (out_f32) return cdiv(n, 128) % 2 ? 128 : 256;
+    return n <= 128 ? 128 : 256;
+}
 
-size_t logits_workspace(int64_t n, int hidden) {
-    const int64_t n_pad = packed_rows(n);
+// rows padded for the packed copy: none up to 16
+int64_t packed_rows(int64_t n, int out_f32) {
+    return n <= 16 ? 0 : round_up(n, n <= kStreamRows ? 16 : tile_rows(n, out_f32));
+}
+
+size_t logits_workspace(int64_t n, int hidden, int out_f32) {
+    const int64_t n_pad = packed_rows(n, out_f32);
     return (size_t)(n_pad * hidden + round_up(4 * n_pad * (hidden / kQBlock) + 1, 256));
+}
+
+template <bool EXACT, int VI, int VW>
+void tiles(TileArgs t, hipStream_t s) {
+    t.tiles_n = t.n_pad / (64 * (8 / VW));
+    t.tiles_v = cdiv(t.p.vocab, 16 * VI * VW);
+    logits_tile_kernel<EXACT, VI, VW><<<(unsigned)(t.tiles_n * t.tiles_v), kTileThreads, 0, s>>>(t);
 }
 
 void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s) {
     if (a.n <= 16) return stream_by_share<1, false>(a, nullptr, nullptr, 0, s);
-    const int64_t n_pad = packed_rows(a.n);
-    uint8_t* rows = (uint8_t*)workspace;
-    float* scale_t = (float*)(rows + n_pad * a.hidden);
-    pack_rows_kernel<<<grid_1d(n_pad * a.hidden / 16, 256, 8192), 256, 0, s>>>(a.a, a.a_scale, a.n, n_pad, a.hidden,
-                                                                              rows, scale_t);
-    if (a.n <= 32) return stream_by_share<2, true>(a, rows, scale_t, (int)n_pad, s);
-    if (a.n <= 48) return stream_by_share<3, true>(a, rows, scale_t, (int)n_pad, s);
-    if (a.n <= kStreamRows) return stream_by_share<4, true>(a, rows, scale_t, (int)n_pad, s);
     TileArgs t;
     t.p = a;
+    t.n_pad = packed_rows(a.n, a.out_f32);
+    uint8_t* rows = (uint8_t*)workspace;
+    float* scale_t = (float*)(rows + t.n_pad * a.hidden);
     t.rows = rows;
     t.scale_t = scale_t;
-    t.n_pad = n_pad;
-    t.tiles_n = n_pad / kTileRows;
-    if (a.out_f32) {
-        t.tiles_v = cdiv(a.vocab, 128);
-        logits_tile_kernel<true, 4><<<(unsigned)(t.tiles_n * t.tiles_v), kTileThreads, 0, s>>>(t);
-    } else {
-        t.tiles_v = cdiv(a.vocab, 256);
-        logits_tile_kernel<false, 8><<<(unsigned)(t.tiles_n * t.tiles_v), kTileThreads, 0, s>>>(t);
-    }
+    pack_rows_kernel<<<grid_1d(t.n_pad * a.hidden / 16, 256, 8192), 256, 0, s>>>(a.a, a.a_scale, a.n, t.n_pad, a.hidden,
+                                                                                rows, scale_t);
+    if (a.n <= 32) return stream_by_share<2, true>(a, rows, scale_t, (int)t.n_pad, s);
+    if (a.n <= 48) return stream_by_share<3, true>(a, rows, scale_t, (int)t.n_pad, s);
+    if (a.n <= kStreamRows) return stream_by_share<4, true>(a, rows, scale_t, (int)t.n_pad, s);
+    const bool narrow = tile_rows(a.n, a.out_f32) == 128;
+    if (a.out_f32) return narrow ? tiles<true, 4, 4>(t, s) : tiles<true, 4, 2>(t, s);
+    return narrow ? tiles<false, 4, 4>(t, s) : tiles<false, 8, 2>(t, s);
 }
 
 }  // namespace lmhead

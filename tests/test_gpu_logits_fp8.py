@@ -1,8 +1,14 @@
 """Logits from 8-bit operands against the 64-bit product of the values they
-stand for. Tolerance: products of e4m3 values are exact in fp32; a block's 128
-products and the blocks' sums are fp32 additions, each off by at most one step
-(2^-23, truncation allowed) of a partial sum that the sum of magnitudes bounds:
-(128 + blocks) 2^-23 sum |a w|. A bf16 output adds half a step, 2^-8."""
+stand for.
+
+Tolerance. Products of e4m3 values are exact in fp32; a block's 128 products
+and the blocks' sums are fp32 additions, each off by at most one step (2^-23,
+truncation allowed) of a partial sum that the sum of magnitudes bounds: (128 +
+blocks) 2^-23 sum |a w|. A bf16 output adds half a step, 2^-8; with more than 64
+rows it comes from the 8-bit matrix instructions, which cut the eight products
+of aligned consecutive columns off 13 bits below the power of two of the
+largest one: at most 8 * 2^-13 of each eight's largest |a w| more
+(test_the_cut_off measures that the instructions do no worse)."""
 import numpy as np
 import pytest
 import torch
@@ -31,13 +37,16 @@ def check(out, a, sa, w, sw):
     tol = (128 + a.shape[1] // 128) * 2.0 ** -23 * size
     if out.dtype == torch.bfloat16:
         tol = tol + 2.0 ** -8 * 1.01 * np.abs(z)
-    bad = np.abs(f64(out) - z) > tol
+        if a.shape[0] > 64:
+            for k in range(0, a.shape[1], 8):
+                tol += 8 * 2.0 ** -13 * np.max(np.abs(A[:, None, k:k + 8] * B[None, :, k:k + 8]), axis=2)
+    bad = ~(np.abs(f64(out) - z) <= tol)   # NaN is bad too
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:5], np.abs(f64(out) - z).max())
 
 
 SHAPES = [(1, 1, 128), (1, 1000, 256), (3, 130, 384), (5, 16, 128), (15, 257, 512), (16, 128, 640), (17, 1000, 256),
-          (32, 63, 1152), (33, 2050, 128), (64, 512, 4096), (65, 300, 256), (100, 129, 1280), (128, 1000, 512),
-          (200, 700, 256), (257, 513, 384), (300, 1100, 2048), (513, 260, 128), (1030, 1030, 256)]
+          (32, 63, 1152), (33, 2050, 128), (64, 512, 4096), (65, 300, 256), (80, 260, 1280), (100, 129, 1280), (128, 1000, 512),
+          (200, 700, 256), (257, 513, 384), (300, 1100, 2048), (513, 260, 128), (300, 9000, 128), (1030, 1030, 256)]
 
 
 @pytest.mark.parametrize("n,vocab,hidden", SHAPES)
@@ -50,6 +59,24 @@ def test_against_definition(n, vocab, hidden, dtype):
     out = lm.logits_fp8(a, sa, w, sw, out_dtype=dtype)
     check(out, a, sa, w, sw)
     assert torch.equal(out, lm.logits_fp8(a, sa, w, sw, out_dtype=dtype))
+
+
+def test_the_cut_off():
+    """2^16 beside seven 2^e in one eight of columns, -2^16 beside seven 2^e in
+    the next, 2^e alone in the other 14: the large ones cancel, so the sum shows
+    how much of the small ones arrived. From 2^(16 - 13) up all of them do;
+    smaller ones may be lost beside 2^16, and only there."""
+    n, vocab = 80, 16
+    for e, whole in ((4, True), (3, True), (2, False), (-6, False)):
+        a, w = torch.zeros(n, 128), torch.zeros(vocab, 128)
+        a[:, :], w[:, :] = 2.0 ** (e // 2), 2.0 ** (e - e // 2)
+        a[:, 0], w[:, 0] = 256.0, 256.0
+        a[:, 8], w[:, 8] = 256.0, -256.0
+        out = lm.logits_fp8(a.to(torch.float8_e4m3fn).cuda(), torch.ones(n, 1, device="cuda"),
+                            w.to(torch.float8_e4m3fn).cuda(), torch.ones(1, 1, device="cuda"))
+        got = f64(out) / 2.0 ** e
+        least = 126 if whole else 112
+        assert (got >= least * (1 - 2.0 ** -8)).all() and (got <= 126 * (1 + 2.0 ** -8)).all(), (e, got[0, 0])
 
 
 @pytest.mark.parametrize("n", [2, 40, 150, 300])

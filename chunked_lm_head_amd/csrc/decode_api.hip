@@ -66,7 +66,7 @@ int lmhead_rms_norm_fwd(const lmhead_norm* p, const void* x, const void* residua
     }
     if (q != nullptr && p->hidden % kQBlock != 0) return LMHEAD_ERR_SHAPE;
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
-        !aligned(y, 16) || !aligned(q, 16) || !aligned(scale, 16) || !aligned(rstd, 16))
+        !aligned(y, 16) || !aligned(q, 16) || !aligned(scale, 4) || !aligned(rstd, 4))
         return LMHEAD_ERR_ALIGN;
     st = check_device();
     if (st != LMHEAD_OK) return st;
@@ -101,8 +101,8 @@ int lmhead_rms_norm_bwd(const lmhead_norm* p, const void* dy, const void* r, con
     if (st != LMHEAD_OK) return st;
     if (p->n > 0 && (dy == nullptr || r == nullptr || weight == nullptr || rstd == nullptr)) return LMHEAD_ERR_ARG;
     if (dweight != nullptr && p->n > 0 && workspace == nullptr) return LMHEAD_ERR_ARG;
-    if (!aligned(dy, 16) || !aligned(r, 16) || !aligned(weight, 16) || !aligned(rstd, 16) ||
-        !aligned(dresidual, 16) || !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(workspace, 256))
+    if (!aligned(dy, 16) || !aligned(r, 16) || !aligned(weight, 16) || !aligned(rstd, 4) ||
+        !aligned(dresidual, 16) || !aligned(dx, 16) || !aligned(dweight, 4) || !aligned(workspace, 256))
         return LMHEAD_ERR_ALIGN;
     if (dweight != nullptr && p->n > 0 && workspace_bytes < lmhead_rms_norm_bwd_workspace_size(p))
         return LMHEAD_ERR_WORKSPACE;
@@ -141,7 +141,7 @@ int lmhead_quantize_fp8(int64_t rows, int64_t cols, int32_t block_rows, const vo
         return LMHEAD_ERR_SHAPE;
     if (block_rows == kQBlock && cdiv(rows, kQBlock) * (cols / kQBlock) > kMaxGroups) return LMHEAD_ERR_SHAPE;
     if (rows > 0 && (x == nullptr || q == nullptr || scale == nullptr)) return LMHEAD_ERR_ARG;
-    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 16)) return LMHEAD_ERR_ALIGN;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return LMHEAD_ERR_ALIGN;
     const int st = check_device();
     if (st != LMHEAD_OK) return st;
     if (rows == 0) return LMHEAD_OK;
@@ -161,8 +161,9 @@ int lmhead_logits_fp8(const lmhead_fp8_problem* p, const void* a, const float* a
     if (workspace == nullptr) return LMHEAD_ERR_ARG;
     if (p->n > 0 && (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr))
         return LMHEAD_ERR_ARG;
-    if (!aligned(a, 16) || !aligned(a_scale, 16) || !aligned(w, 16) || !aligned(w_scale, 16) || !aligned(out, 16) ||
-        !aligned(workspace, 256))
+    const int out_bytes = p->out_dtype == LMHEAD_DTYPE_F32 ? 4 : 2;
+    if (!aligned(a, 16) || !aligned(a_scale, 4) || !aligned(w, 16) || !aligned(w_scale, 4) ||
+        !aligned(out, out_bytes) || !aligned(workspace, 256))
         return LMHEAD_ERR_ALIGN;
     if (workspace_bytes < lmhead_logits_fp8_workspace_size(p)) return LMHEAD_ERR_WORKSPACE;
     st = check_device();
@@ -179,6 +180,7 @@ int lmhead_logits_fp8(const lmhead_fp8_problem* p, const void* a, const float* a
     g.vocab = p->vocab;
     g.ld = p->ld;
     g.hidden = (int)p->hidden;
+    g.quads = p->ld % 4 == 0 && aligned(out, 4 * out_bytes);
     launch_logits(g, workspace, (hipStream_t)stream);
     return launched();
 }

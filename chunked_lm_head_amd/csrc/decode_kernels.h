@@ -58,6 +58,7 @@ struct LogitsArgs {
     int out_f32;
     int64_t n, vocab, ld;
     int hidden;
+    int quads;   // four consecutive logits of a row from a column that four divides are aligned to their size
 };
 size_t logits_workspace(int64_t n, int hidden, int out_f32);
 void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s);

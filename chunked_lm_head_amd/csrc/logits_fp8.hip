@@ -71,11 +71,11 @@ __device__ __forceinline__ floatx4 block_sum(const i32x8& a, const i32x8& b) {
 constexpr int kStreamRows = 64;
 
 // Four consecutive logits of a row per lane, `count` of them (<= 0: none)
-// inside the vocabulary: one store where the row pitch keeps them aligned.
+// inside the vocabulary: one store where the pitch and the buffer keep them aligned.
 __device__ __forceinline__ void store4(const LogitsArgs& a, int64_t row, int64_t v, int count, const floatx4& x) {
     if (row >= a.n || count <= 0) return;
     const int64_t at = row * a.ld + v;
-    if (count >= 4 && (a.ld & 3) == 0) {
+    if (count >= 4 && a.quads) {
         if (a.out_f32)
             *reinterpret_cast<floatx4*>(reinterpret_cast<float*>(a.out) + at) = x;
         else

@@ -80,7 +80,8 @@ typedef struct lmhead_norm {
  *                 both NULL: y (before any rounding to bf16) in 8 bits with
  *                 one scale per row and 128 columns.
  *   rstd          device, fp32 [n] or NULL: what the backward needs.
- * All pointers 16-byte aligned. At least one of y, q, rstd, residual_out.
+ * Pointers 16-byte aligned (scale and rstd: 4). At least one of y, q, rstd,
+ * residual_out.
  */
 int lmhead_rms_norm_fwd(const lmhead_norm* p, const void* x, const void* residual, const void* weight,
                         void* residual_out, void* y, void* q, float* scale, float* rstd, void* stream);
@@ -104,6 +105,7 @@ size_t lmhead_rms_norm_bwd_workspace_size(const lmhead_norm* p);
  *              dresidual.
  *   dweight    device, [hidden], weight_dtype, or NULL. n = 0 writes zeros.
  *   workspace  256-byte aligned; may be NULL without dweight.
+ * Other pointers 16-byte aligned (rstd and dweight: 4).
  */
 int lmhead_rms_norm_bwd(const lmhead_norm* p, const void* dy, const void* r, const void* weight,
                         const float* rstd, const void* dresidual, void* dx, void* dweight,
@@ -119,6 +121,7 @@ int lmhead_rms_norm_bwd(const lmhead_norm* p, const void* dy, const void* r, con
  *               rows may hold fewer).
  *   q           device, e4m3 [rows, cols].
  *   scale       device, fp32 [ceil(rows / block_rows), cols / 128].
+ * x and q 16-byte aligned, scale 4.
  */
 int lmhead_quantize_fp8(int64_t rows, int64_t cols, int32_t block_rows, const void* x, void* q,
                         float* scale, void* stream);
@@ -158,8 +161,9 @@ size_t lmhead_logits_fp8_workspace_size(const lmhead_fp8_problem* p);
  *               with block_rows 1).
  *   w, w_scale  device, e4m3 [vocab, hidden], fp32 [ceil(vocab / 128),
  *               hidden / 128] (lmhead_quantize_fp8 with block_rows 128).
- *   out         device, out_dtype [n, ld]; columns vocab .. ld - 1 are left
- *               as they are.
+ *   out         device, out_dtype [n, ld], aligned to its elements; columns
+ *               vocab .. ld - 1 are left as they are.
+ * a and w 16-byte aligned, the scales 4, the workspace 256.
  */
 int lmhead_logits_fp8(const lmhead_fp8_problem* p, const void* a, const float* a_scale, const void* w,
                       const float* w_scale, void* out, void* workspace, size_t workspace_bytes,

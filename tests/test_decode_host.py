@@ -54,7 +54,7 @@ def test_norm_refusals():
     assert call(norm(), x=None) == A and call(norm(), weight=None) == A
     assert call(norm(), residual_out=None, y=None, q=None, scale=None, rstd=None) == A
     for name in ("x", "residual", "weight", "residual_out", "y", "q", "scale", "rstd"):
-        assert call(norm(), **{name: F + 8 + (4096 if name == "y" else 0)}) == AL, name
+        assert call(norm(), **{name: F + (2 if name in ("scale", "rstd") else 8) + (4096 if name == "y" else 0)}) == AL, name
 
 
 def test_norm_backward_refusals():
@@ -83,7 +83,7 @@ def test_quantize_refusals():
     # one workgroup per 128 x 128 block: at most 2^24 - 1 of them
     assert f(128 * ((1 << 24) // 512 + 1), 65536, 128, F, F, F, 0) == S
     assert f(4, 256, 1, None, F, F, 0) == A and f(4, 256, 1, F, None, F, 0) == A and f(4, 256, 1, F, F, None, 0) == A
-    assert f(4, 256, 1, F + 2, F, F, 0) == AL and f(4, 256, 1, F, F, F + 4, 0) == AL
+    assert f(4, 256, 1, F + 2, F, F, 0) == AL and f(4, 256, 1, F, F, F + 2, 0) == AL
 
 
 def fp8(**kw):
@@ -101,7 +101,7 @@ def test_logits_refusals():
         assert f(fp8(**bad), F, F, F, F, F, F, BIG, 0) == S and size(fp8(**bad)) == 0, bad
     for i in range(6):
         assert f(fp8(), *[None if j == i else F for j in range(6)], BIG, 0) == A
-        assert f(fp8(), *[F + 8 if j == i else F for j in range(6)], BIG, 0) == AL
+        assert f(fp8(), *[F + (2 if i in (1, 3, 4) else 8) if j == i else F for j in range(6)], BIG, 0) == AL
     assert f(fp8(), F, F, F, F, F, F, 0, 0) == W
 
 

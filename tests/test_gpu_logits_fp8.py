@@ -92,6 +92,20 @@ def test_row_stride_leaves_the_rest(n, dtype, ld):
     assert (buf[:n, 333:] == 7.0).all() and (buf[n] == 7.0).all()
 
 
+@pytest.mark.parametrize("n", [3, 40, 70, 200])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_slices_of_rows_and_columns(n, dtype):
+    """Rows and their scales from the second on, and an output that starts at the
+    second column: aligned to their elements only."""
+    rng = np.random.default_rng(8)
+    a, sa = operand(n + 1, 128, 1, rng)
+    w, sw = operand(300, 128, 128, rng)
+    buf = torch.full((n, 304), 7.0, dtype=dtype, device="cuda")
+    out = lm.logits_fp8(a[1:], sa[1:], w, sw, out=buf[:, 1:301])
+    check(out, a[1:], sa[1:], w, sw)
+    assert (buf[:, 0] == 7.0).all() and (buf[:, 301:] == 7.0).all()
+
+
 def test_rows_do_not_touch_each_other():
     """A row with NaN, and a W block with an infinite scale, stay where they are."""
     rng = np.random.default_rng(6)

@@ -87,6 +87,45 @@ def test_equal_logits_go_to_the_lowest_index(dtype):
     assert t.tolist() == [0, 99]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab,values", [(1500, 2), (5000, 7), (20000, 3), (40000, 1), (70000, 40)])
+def test_borders_among_many_equal_logits(dtype, vocab, values):
+    """From some hundred to all tokens tied where the filters end: borders that
+    are listed and sorted, and more of them than the list holds."""
+    n = 12
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy(rng.integers(0, values, (n, vocab)).astype(np.float32) / 4).to(dtype).cuda()
+    x[3, ::3] = float("-inf")
+    u = torch.from_numpy(rng.random(n).astype(np.float32)).clamp(max=1 - 2.0 ** -24).cuda()
+    for kw in (dict(), dict(top_k=vocab // 3), dict(top_p=0.4), dict(top_p=0.97), dict(min_p=0.7),
+               dict(top_k=vocab // 2, top_p=0.6), dict(top_k=vocab - vocab // 9, top_p=0.9, min_p=0.3)):
+        print(f"[sample] vocab={vocab} values={values} {dtype} {kw}", flush=True)
+        check(x, u, **kw)
+
+
+def test_weights_that_vanish():
+    """Temperatures so low that most weights are 0: filters that would reach into
+    those, and a range of logits wider than weights can tell apart."""
+    x, u, rng = logits_of(16, 30000, torch.float32, 21, 5.0)
+    x[5, 100:] -= 1e30
+    x[6, 1:] = -3e38
+    for t in (0.01, 0.1, 1e-30):
+        for kw in (dict(), dict(top_k=50), dict(top_k=20000), dict(top_p=0.999999), dict(min_p=1e-30),
+                   dict(top_k=9000, top_p=0.5, min_p=1e-12)):
+            check(x, u, temperature=t, **kw)
+
+
+def test_more_rows_than_one_set_of_launches():
+    x, u, rng = logits_of(700, 300, torch.bfloat16, 22)
+    x[600, 5] = float("nan")
+    ws = torch.empty(lm.lmhead_sample_workspace_size(lm.lmhead_sample_problem(700, 300, 300, 0)), dtype=torch.uint8,
+                     device="cuda")
+    token, _ = lm.sample(x, u, top_k=20, top_p=0.8, ws=ws)
+    assert lm.lmhead_read_device_error(ws) == (lm.DEVERR_LOGIT, 600) and token[600] == -1
+    x[600, 5] = 0.0
+    check(x, u, top_k=rng.integers(0, 40, 700).astype(np.int32), top_p=0.8)
+
+
 def test_masks():
     n, vocab = 12, 2500
     x, u, rng = logits_of(n, vocab, torch.float32, 8)

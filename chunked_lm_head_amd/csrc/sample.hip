@@ -361,11 +361,11 @@ __device__ __forceinline__ uint64_t nucleus(float top_p, uint64_t kept) {
 }
 
 template <bool F32>
-__device__ __forceinline__ void write_token(const SampleArgs& a, int64_t r, const Row<F32>& row, int64_t pos,
+__device__ __forceinline__ void write_token(const SampleArgs& a, int64_t r, const Row<F32>& row, int64_t pos, float x,
                                             const Weights& W, float tau, uint64_t all) {
     a.token[r] = (int32_t)(pos - row.off);
     if (a.logprob != nullptr)
-        a.logprob[r] = (float)(((double)row.at(pos) - W.top) / (double)tau -
+        a.logprob[r] = (float)(((double)x - W.top) / (double)tau -
                                log((double)all * __builtin_amdgcn_ldexp(1.0, -W.shift)));
 }
 
@@ -490,7 +490,7 @@ __device__ __attribute__((noinline)) void whole_row(const SampleArgs& a, int64_t
                     if (!got && c > goal) pick = i, got = true;
                 }
                 const int64_t pos = k * kPer + pick;
-                write_token(a, r, row, pos, W, P.tau, all);
+                write_token(a, r, row, pos, row.at(pos), W, P.tau, all);
             }
             done = __any(mine);
             run += last_lane(w_inc);
@@ -669,20 +669,29 @@ struct Borders {
     uint64_t all;
 };
 
-__device__ Borders borders(const RowPlan& R, const SampleSpace& w, int local, int slices, Shared& S) {
-    const int b = 2 * threadIdx.x;
-    const bool counted = R.P.top_k > 0;
+// The bins 2 t and 2 t + 1 of thread t, over the row's slices.
+struct BinSums {
     uint64_t h0 = 0, h1 = 0, c0 = 0, c1 = 0;
-#pragma unroll 4
-    for (int s = 0; s < slices; ++s) {
-        const int64_t at = ((int64_t)local * slices + s) * kBins + b;
+};
+__device__ __forceinline__ BinSums bin_sums(const SampleSpace& w, int local, int slices, bool counted) {
+    BinSums s;
+#pragma unroll 8
+    for (int q = 0; q < slices; ++q) {
+        const int64_t at = ((int64_t)local * slices + q) * kBins + 2 * threadIdx.x;
         const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(w.weight + at);
-        h0 += h.x, h1 += h.y;
+        s.h0 += h.x, s.h1 += h.y;
         if (counted) {
             const uint2 c = *reinterpret_cast<const uint2*>(w.count + at);
-            c0 += c.x, c1 += c.y;
+            s.c0 += c.x, s.c1 += c.y;
         }
     }
+    return s;
+}
+
+__device__ Borders borders(const RowPlan& R, const BinSums& sums, Shared& S) {
+    const int b = 2 * threadIdx.x;
+    const bool counted = R.P.top_k > 0;
+    const uint64_t h0 = sums.h0, h1 = sums.h1, c0 = sums.c0, c1 = sums.c1;
     Borders B;
     uint64_t n;
     const uint64_t ew = block_scan(h0 + h1, S, B.all);
@@ -734,9 +743,11 @@ __device__ Borders borders(const RowPlan& R, const SampleSpace& w, int local, in
 __global__ __launch_bounds__(kRowThreads) void sample_border_kernel(SampleArgs a, SampleSpace w, int64_t r0, int slices) {
     __shared__ Shared S;
     const int local = blockIdx.x;
+    // the sums' loads go out with those of the row's scan (an unfiltered or bad row has no histogram: unused)
+    const BinSums sums = bin_sums(w, local, slices, row_params(a, r0 + local).top_k > 0);
     const RowPlan R = row_plan(a, w, r0 + local, local, slices);
     if (R.bad || !R.filtered) return;
-    const Borders B = borders(R, w, local, slices, S);
+    const Borders B = borders(R, sums, S);
     for (int i = threadIdx.x; i < kBins; i += kRowThreads) {
         w.run_weight[(int64_t)local * kBins + i] = S.hist[i];
         if (R.P.top_k > 0) w.run_count[(int64_t)local * kBins + i] = S.ties[i];
@@ -823,7 +834,18 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     Shared& S = L.S;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, local = blockIdx.x;
     const int64_t r = r0 + local;
+    // what the other kernels left, loaded at once with the row's scan (unused where the row has no filter)
+    const uint32_t listed = w.listed[local];
+    const Borders B = w.borders[local];
+    const uint64_t run0 = w.run_weight[(int64_t)local * kBins + tid];
+    const uint64_t run1 = w.run_weight[(int64_t)local * kBins + kRowThreads + tid];
+    const uint32_t cnt0 = w.run_count[(int64_t)local * kBins + tid];
+    const uint32_t cnt1 = w.run_count[(int64_t)local * kBins + kRowThreads + tid];
+    const uint64_t entry = w.list[(int64_t)local * kList + tid];
+    const uint64_t slice_total = w.total[(int64_t)local * slices + (lane < slices ? lane : 0)];
     const RowPlan R = row_plan(a, w, r, local, slices);
+    // keeps the loads above the branches
+    asm volatile("" ::"v"(run0), "v"(run1), "v"(cnt0), "v"(cnt1), "v"(entry), "v"(slice_total), "s"(listed));
     if (R.bad) {
         if (tid == 0) {
             a.token[r] = -1;
@@ -842,20 +864,17 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     int lim = kBins;
     uint64_t end = 0, all = 0;
     if (R.filtered) {
-        const uint32_t listed = w.listed[local];
         if (listed > kList) {
             whole_row<F32>(a, r, row, R.P, R.W, S);
             return;
         }
-        const Borders B = w.borders[local];
         all = B.all;
-        for (int i = tid; i < kBins; i += kRowThreads) {
-            S.hist[i] = w.run_weight[(int64_t)local * kBins + i];
-            if (R.P.top_k > 0) S.ties[i] = w.run_count[(int64_t)local * kBins + i];
-        }
+        S.hist[tid] = run0, S.hist[kRowThreads + tid] = run1;
+        if (R.P.top_k > 0) S.ties[tid] = cnt0, S.ties[kRowThreads + tid] = cnt1;
         int size = 64;
         while (size < (int)listed) size <<= 1;
-        for (int i = tid; i < size; i += kRowThreads) L.before[i] = i < (int)listed ? w.list[(int64_t)local * kList + i] : ~0ull;
+        for (int i = tid; i < size; i += kRowThreads)
+            L.before[i] = i >= (int)listed ? ~0ull : i == tid ? entry : w.list[(int64_t)local * kList + i];
         if (tid == 0) L.last = -1;
         __syncthreads();
         if (listed <= 512) {
@@ -937,7 +956,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
             uint64_t t = 0;
             for (int b = B.lo + lane; b < lim; b += 64) t += w.weight[at * kBins + b];
             t = wave_total(t);
-            if (lane == 0) L.slice[s] = w.total[at] + t;
+            if (lane == s) L.slice[s] = slice_total + t;
         }
         __syncthreads();
         if (last >= 0)
@@ -953,7 +972,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
         __syncthreads();
     }
     // the slice in which the goal lies, and the goal within it
-    const uint64_t sv = lane < slices ? (R.filtered ? L.slice[lane] : w.total[(int64_t)local * slices + lane]) : 0;
+    const uint64_t sv = lane < slices ? (R.filtered ? L.slice[lane] : slice_total) : 0;
     const uint64_t total = wave_total(sv);
     if (!R.filtered) all = total;
     uint64_t goal = (uint64_t)((double)R.P.u * (double)total);
@@ -1027,12 +1046,13 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
     uint64_t c = inc - mine;
     if (c <= goal && c + mine > goal) {
         int pick = kPer;
+        float logit = 0.0f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             c += v[i];
-            if (pick == kPer && c > goal) pick = i;
+            if (pick == kPer && c > goal) pick = i, logit = x[i];
         }
-        write_token(a, r, row, k * kPer + pick, R.W, R.P.tau, all);
+        write_token(a, r, row, k * kPer + pick, logit, R.W, R.P.tau, all);
     }
 }
 

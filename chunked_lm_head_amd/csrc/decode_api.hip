@@ -181,6 +181,7 @@ int lmhead_logits_fp8(const lmhead_fp8_problem* p, const void* a, const float* a
     g.ld = p->ld;
     g.hidden = (int)p->hidden;
     g.quads = p->ld % 4 == 0 && aligned(out, 4 * out_bytes);
+    g.lines = p->ld % (16 / out_bytes) == 0 && aligned(out, 16);
     launch_logits(g, workspace, (hipStream_t)stream);
     return launched();
 }

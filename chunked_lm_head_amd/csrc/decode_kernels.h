@@ -59,6 +59,7 @@ struct LogitsArgs {
     int64_t n, vocab, ld;
     int hidden;
     int quads;   // four consecutive logits of a row from a column that four divides are aligned to their size
+    int lines;   // so are 16 bytes of them
 };
 size_t logits_workspace(int64_t n, int hidden, int out_f32);
 void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s);

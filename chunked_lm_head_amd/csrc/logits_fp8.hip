@@ -308,7 +308,8 @@ template <bool EXACT, int VI, int VW>
 __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t) {
     static_assert(VI == 8 || VI == 4, "a step's loads are spread over eight (half) groups");
     constexpr int kV = 16 * VI * VW, kRows = 64 * (8 / VW), kStage = kV * 128, kLoads = kStage / (kTileThreads * 16);
-    __shared__ __attribute__((aligned(16))) char smem[kStages * kStage];
+    constexpr int kOut = 8 * 64 * 16 * VI * (EXACT ? 4 : 2);   // the results on their way out
+    __shared__ __attribute__((aligned(16))) char smem[kStages * kStage > kOut ? kStages * kStage : kOut];
     const LogitsArgs& a = t.p;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -458,8 +459,51 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
         step(b + 1, s1, s0);
     }
     if (b < nb) step(b, s0, s1);
-    // every LDS-direct load (the clamped ones past the last step included) lands before the end
+    // every LDS-direct load (the clamped ones past the last step included) has landed
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (a.lines) {
+        // Through LDS, a part of it per wave: rows of 16 VI logits, 16-byte piece q
+        // of row r at q ^ (r mod pieces), then whole rows of 128 or 256 bytes to
+        // memory, past the L2 that W and the rows live in. Stored from the
+        // fragments, a row's 32 bytes at a time, the results took 165 of 1262 us
+        // (2048 rows, bf16); this way 1178 us in all, 1165 us with the
+        // non-temporal hint (256 rows: 202, 187, 177 us).
+        __syncthreads();
+        constexpr int kSize = EXACT ? 4 : 2, kPitch = 16 * VI * kSize, kPieces = kPitch / 16;
+        char* part = smem + wave * 64 * kPitch;
+#pragma unroll
+        for (int i = 0; i < VI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 16 * j + c, at = (16 * i + 4 * g) * kSize;
+                char* p = part + r * kPitch + (((at >> 4) ^ (r & (kPieces - 1))) << 4);
+                if (EXACT)
+                    *reinterpret_cast<floatx4*>(p) = acc[i][j];
+                else
+                    *reinterpret_cast<uint2*>(p + (at & 8)) =
+                        make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const int q = lane % kPieces;
+        const int64_t v = v0 + wv * 16 * VI + q * (16 / kSize);
+#pragma unroll 4
+        for (int r = lane / kPieces; r < 64; r += 64 / kPieces) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(part + r * kPitch + ((q ^ (r & (kPieces - 1))) << 4));
+            if (i0 + r >= a.n) break;
+            char* out = reinterpret_cast<char*>(a.out) + ((i0 + r) * a.ld + v) * kSize;
+            if (v + 16 / kSize <= a.vocab) {
+                __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(out));
+            } else {
+                for (int e = 0; e < 16 / kSize && v + e < a.vocab; ++e) {
+                    if (EXACT)
+                        reinterpret_cast<uint32_t*>(out)[e] = x[e];
+                    else
+                        reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+                }
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
         const int64_t v = v0 + wv * 16 * VI + 16 * i + 4 * g;
@@ -473,10 +517,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
 
 // Rows of a matrix tile. An fp32 output's tile of 128 rows x 256 columns takes
 // half the time of one of 256 x 128 per row, so 128 wherever 256 would leave the
-// last half tile empty (us at 151,936 x 4096, 128 against 256 rows a tile: n =
-// 128: 200, 291; 256: 336, 331; 300: 455, 593; 2048: 2388, 2349). A bf16
-// output's larger 256 x 256 tile reads less per product and loses to 128 only
-// when one tile holds all rows (n = 128: 186, 202; 200: 254, 208; 300: 331, 306).
+// last half tile empty (us at 151,936 x 4096, 128 against 256 rows a tile, before
+// the results went through LDS: n = 128: 200, 291; 256: 336, 331; 300: 455, 593;
+// 2048: 2388, 2349). A bf16 output's larger 256 x 256 tile reads less per
+// product and loses to 128 only when one tile holds all rows (n = 128: 186, 202;
+// 200: 254, 208; 300: 331, 306).
 int64_t tile_rows(int64_t n, int out_f32) {
     if (out_f32) return cdiv(n, 128) % 2 ? 128 : 256;
     return n <= 128 ? 128 : 256;

@@ -304,7 +304,7 @@ struct TileArgs {
 // then the W loads of step b + 3: waiting for the former at the next step's start leaves
 // only the latter in flight, so W of step b + 1 has landed for every wave that
 // has begun step b, and one barrier per step is enough.
-template <bool EXACT, int VI, int VW>
+template <bool EXACT, int VI, int VW, bool LINES>
 __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t) {
     static_assert(VI == 8 || VI == 4, "a step's loads are spread over eight (half) groups");
     constexpr int kV = 16 * VI * VW, kRows = 64 * (8 / VW), kStage = kV * 128, kLoads = kStage / (kTileThreads * 16);
@@ -461,55 +461,76 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
     if (b < nb) step(b, s0, s1);
     // every LDS-direct load (the clamped ones past the last step included) has landed
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (a.lines) {
-        // Through LDS, a part of it per wave: rows of 16 VI logits, 16-byte piece q
-        // of row r at q ^ (r mod pieces), then whole rows of 128 or 256 bytes to
-        // memory, past the L2 that W and the rows live in. Stored from the
-        // fragments, a row's 32 bytes at a time, the results took 165 of 1262 us
-        // (2048 rows, bf16); this way 1178 us in all, 1165 us with the
-        // non-temporal hint (256 rows: 202, 187, 177 us).
-        __syncthreads();
-        constexpr int kSize = EXACT ? 4 : 2, kPitch = 16 * VI * kSize, kPieces = kPitch / 16;
-        char* part = smem + wave * 64 * kPitch;
+    // Through LDS, a part of it per wave: rows of 16 VI logits, 16-byte piece q
+    // of row r at q ^ (r mod pieces), then whole rows of 128 or 256 bytes to
+    // memory, past the L2 that W and the rows live in. Stored from the
+    // fragments, a row's 32 bytes at a time, the results took 165 of 1262 us
+    // (2048 rows, bf16); this way 1178 us in all, 1165 us with the
+    // non-temporal hint (256 rows: 202, 187, 177 us).
+    __syncthreads();
+    constexpr int kSize = EXACT ? 4 : 2, kPitch = 16 * VI * kSize, kPieces = kPitch / 16;
+    char* const part = smem + wave * 64 * kPitch;
+    auto place = [&](int r, int at) { return part + r * kPitch + (((at >> 4) ^ (r & (kPieces - 1))) << 4) + (at & 15); };
 #pragma unroll
-        for (int i = 0; i < VI; ++i)
+    for (int i = 0; i < VI; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = 16 * j + c, at = (16 * i + 4 * g) * kSize;
-                char* p = part + r * kPitch + (((at >> 4) ^ (r & (kPieces - 1))) << 4);
-                if (EXACT)
-                    *reinterpret_cast<floatx4*>(p) = acc[i][j];
-                else
-                    *reinterpret_cast<uint2*>(p + (at & 8)) =
-                        make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
-            }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        const int q = lane % kPieces;
-        const int64_t v = v0 + wv * 16 * VI + q * (16 / kSize);
+        for (int j = 0; j < 4; ++j) {
+            char* p = place(16 * j + c, (16 * i + 4 * g) * kSize);
+            if (EXACT)
+                *reinterpret_cast<floatx4*>(p) = acc[i][j];
+            else
+                *reinterpret_cast<uint2*>(p) =
+                    make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
+        }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    // the tile's place made again: kept through the loop it cost registers that the loop needs
+    int bid = blockIdx.x;
+    asm volatile("" : "+s"(bid));
+    map_tile(bid, t.tiles_n, t.tiles_v, tn, tv);
+    const int64_t i1 = tn * kRows + wn * 64, v1 = tv * kV + wv * 16 * VI;
+    const int left = a.vocab - v1 < 16 * VI ? (int)(a.vocab - v1) : 16 * VI;   // logits of a row inside the vocabulary
+    char* const out = reinterpret_cast<char*>(a.out) + (i1 * a.ld + v1) * kSize;
+    const int rows_left = a.n - i1 < 64 ? (int)(a.n - i1) : 64;
+    if constexpr (LINES) {
+        const int q = lane % kPieces, e0 = q * (16 / kSize);
 #pragma unroll 4
-        for (int r = lane / kPieces; r < 64; r += 64 / kPieces) {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(part + r * kPitch + ((q ^ (r & (kPieces - 1))) << 4));
-            if (i0 + r >= a.n) break;
-            char* out = reinterpret_cast<char*>(a.out) + ((i0 + r) * a.ld + v) * kSize;
-            if (v + 16 / kSize <= a.vocab) {
-                __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(out));
+        for (int r = lane / kPieces; r < rows_left; r += 64 / kPieces) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(place(r, 16 * q));
+            char* to = out + r * a.ld * kSize + 16 * q;
+            if (e0 + 16 / kSize <= left) {
+                __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(to));
             } else {
-                for (int e = 0; e < 16 / kSize && v + e < a.vocab; ++e) {
+                for (int e = 0; e < 16 / kSize && e0 + e < left; ++e) {
                     if (EXACT)
-                        reinterpret_cast<uint32_t*>(out)[e] = x[e];
+                        reinterpret_cast<uint32_t*>(to)[e] = x[e];
                     else
-                        reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+                        reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
                 }
             }
         }
         return;
     }
-#pragma unroll
-    for (int i = 0; i < VI; ++i) {
-        const int64_t v = v0 + wv * 16 * VI + 16 * i + 4 * g;
-        const int64_t left = a.vocab - v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) store4(a, i0 + 16 * j + c, v, left < 4 ? (int)left : 4, acc[i][j]);
+    // Rows that start at any element: four bytes a lane, bf16 pairs from the
+    // row's first aligned one on (151,935 columns, 2048 rows: 1260 us; element by
+    // element 1426 us).
+    constexpr int kLanes = EXACT ? 16 * VI : 8 * VI;
+    const int l = lane % kLanes;
+#pragma unroll 4
+    for (int r = lane / kLanes; r < rows_left; r += 64 / kLanes) {
+        char* to = out + r * a.ld * kSize;
+        if (EXACT) {
+            if (l < left) reinterpret_cast<uint32_t*>(to)[l] = *reinterpret_cast<const uint32_t*>(place(r, 4 * l));
+        } else {
+            const int odd = (int)(reinterpret_cast<uintptr_t>(to) >> 1) & 1, e = 2 * l + odd;
+            const uint32_t lo = *reinterpret_cast<const uint16_t*>(place(r, 2 * e));
+            const uint32_t hi = *reinterpret_cast<const uint16_t*>(place(r, 2 * (e + 1 < 16 * VI ? e + 1 : e)));
+            if (e + 1 < left)
+                *reinterpret_cast<uint32_t*>(to + 2 * e) = lo | hi << 16;
+            else if (e < left)
+                reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)lo;
+            if (odd && l == 0 && left > 0)
+                reinterpret_cast<uint16_t*>(to)[0] = *reinterpret_cast<const uint16_t*>(place(r, 0));
+        }
     }
 }
 
@@ -541,7 +562,11 @@ template <bool EXACT, int VI, int VW>
 void tiles(TileArgs t, hipStream_t s) {
     t.tiles_n = t.n_pad / (64 * (8 / VW));
     t.tiles_v = cdiv(t.p.vocab, 16 * VI * VW);
-    logits_tile_kernel<EXACT, VI, VW><<<(unsigned)(t.tiles_n * t.tiles_v), kTileThreads, 0, s>>>(t);
+    const unsigned grid = (unsigned)(t.tiles_n * t.tiles_v);
+    if (t.p.lines)
+        logits_tile_kernel<EXACT, VI, VW, true><<<grid, kTileThreads, 0, s>>>(t);
+    else
+        logits_tile_kernel<EXACT, VI, VW, false><<<grid, kTileThreads, 0, s>>>(t);
 }
 
 void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s) {

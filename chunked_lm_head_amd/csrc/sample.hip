@@ -108,40 +108,31 @@ struct Row {
         end = off + vocab;
     }
     __device__ __forceinline__ int64_t vectors() const { return (end + kPer - 1) / kPer; }
-    // vectors k, k + STEP, k + 2 STEP, k + 3 STEP, those from k1 on as -infinity
-    template <int STEP>
+    // the vectors that lie inside the row: whole_from() .. whole_to() - 1 (none when not below)
+    __device__ __forceinline__ int64_t whole_from() const { return off > 0 ? 1 : 0; }
+    __device__ __forceinline__ int64_t whole_to() const { return end / kPer; }
+    // vectors k, k + 64, k + 128, k + 192; as -infinity those from k1 on and the row's ragged ones
     __device__ __forceinline__ void load4(int64_t k, int64_t k1, float (&x)[4][kPer]) const {
-        const int64_t a0 = off > 0 ? 1 : 0, a1 = end / kPer;   // the vectors inside the row
-        if (a0 < a1) {
-            uint4 v[4];
+        const int64_t a0 = whole_from(), a1 = whole_to();
+        uint4 v[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t kq = k + q * STEP;
-                v[q] = *reinterpret_cast<const uint4*>(base + (kq < a0 ? a0 : kq < a1 ? kq : a1 - 1) * 16);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (F32) {
-                        x[q][i] = __builtin_bit_cast(float, w[i]);
-                    } else {
-                        x[q][2 * i] = __builtin_bit_cast(float, w[i] << 16);
-                        x[q][2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
-                    }
-                }
-            }
+        for (int q = 0; q < 4; ++q) {
+            const int64_t kq = k + q * 64;
+            v[q] = *reinterpret_cast<const uint4*>(base + (kq < a0 ? a0 : kq < a1 ? kq : a1 - 1) * 16);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int64_t kq = k + q * STEP;
-            if (kq < k1 && kq >= a0 && kq < a1) continue;
-            if (kq < k1) {
-                load(kq, x[q]);   // a ragged end
-            } else {
+            const int64_t kq = k + q * 64;
+            const bool in = kq < k1 && kq >= a0 && kq < a1;
+            const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) x[q][i] = -__builtin_huge_valf();
+            for (int i = 0; i < 4; ++i) {
+                if (F32) {
+                    x[q][i] = in ? __builtin_bit_cast(float, w[i]) : -__builtin_huge_valf();
+                } else {
+                    x[q][2 * i] = in ? __builtin_bit_cast(float, w[i] << 16) : -__builtin_huge_valf();
+                    x[q][2 * i + 1] = in ? __builtin_bit_cast(float, w[i] & 0xffff0000u) : -__builtin_huge_valf();
+                }
             }
         }
     }
@@ -1008,16 +999,30 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
         const int64_t run = (hi - lo + kRowWaves - 1) / kRowWaves;
         const int64_t e0 = lo + run * wave, e1 = e0 + run < hi ? e0 + run : hi;
         uint64_t t = 0;
-        for (int64_t k = e0 + lane; k < e1; k += 4 * 64) {
-            float x[4][kPer];
-            row.template load4<64>(k, e1, x);
+        if (row.whole_from() < row.whole_to())
+            for (int64_t k = e0 + lane; k < e1; k += 4 * 64) {
+                float x[4][kPer];
+                row.load4(k, e1, x);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (k - lane + 64 * q >= e1) break;
+                for (int q = 0; q < 4; ++q) {
+                    if (k - lane + 64 * q >= e1) break;
+                    uint64_t v[kPer];
+                    weigh(x[q], (k + 64 * q) * kPer, v);
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) t += v[i];
+                }
+            }
+        // the run's ragged vectors, a position a lane
+        for (int64_t k = e0; k < e1; k = k + 1 < row.whole_to() ? row.whole_to() : k + 1) {
+            const int64_t pos = k * kPer + lane;
+            if ((k < row.whole_from() || k >= row.whole_to()) && lane < kPer && pos >= row.off && pos < row.end) {
+                float x[kPer];
                 uint64_t v[kPer];
-                weigh(x[q], (k + 64 * q) * kPer, v);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) t += v[i];
+                for (int i = 0; i < kPer; ++i) x[i] = -__builtin_huge_valf();
+                x[0] = row.at(pos);
+                weigh(x, pos, v);
+                t += v[0];
             }
         }
         t = wave_total(t);

@@ -800,10 +800,74 @@ struct PickShared {
     uint64_t before[kList];   // running weight of the list
     int first[kBins];         // first list position of a bin
     int rank[512];
-    uint64_t slice[kMaxSlices + 1];
-    uint64_t zk;
-    int last, done;
+    uint64_t slice[kMaxSlices];   // kept weight
+    uint64_t end;
+    int last, lim;
 };
+
+// Slice of a token.
+template <bool F32>
+__device__ __forceinline__ int slice_of(const Row<F32>& row, int64_t token, int slices) {
+    const int64_t nvec = row.vectors(), vec = (token + row.off) / Row<F32>::kPer;
+    int s = (int)(vec * slices / nvec);
+    while (s + 1 < slices && vec >= nvec * (s + 1) / slices) ++s;
+    while (s > 0 && vec < nvec * s / slices) --s;
+    return s;
+}
+
+// The end of the kept prefix by one wave, a listed token a lane: lim and end
+// (see the kernel), and the slices' kept weight.
+template <bool F32>
+__device__ __forceinline__ void short_list(const RowPlan& R, const Borders& B, const SampleSpace& w, const Row<F32>& row,
+                                           int local, int slices, uint64_t entry, int listed, uint64_t slice_total,
+                                           uint64_t all, PickShared& L) {
+    const Shared& S = L.S;
+    const int lane = threadIdx.x & 63;
+    // sorted: lane p gets the entry of rank p
+    int rank = 0;
+    for (int i = 0; i < listed; ++i) {
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)entry, i);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(entry >> 32), i);
+        rank += ((uint64_t)hi << 32 | lo) < entry;
+    }
+    if (lane >= listed) rank = lane;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_permute(4 * rank, (int)(uint32_t)entry);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_permute(4 * rank, (int)(uint32_t)(entry >> 32));
+    const uint64_t mine = (uint64_t)hi << 32 | lo;
+    const bool in = lane < listed;
+    const float x = value_of(~hi);
+    const uint64_t v = in ? R.W.of(x) : 0;
+    const int bin = in ? R.bin(x) : -1;
+    const uint64_t before = wave_scan(v) - v;
+    // the first entry of the lane's bin
+    const int left = __shfl_up(bin, 1);   // by every lane: an idle one gives nothing
+    const bool head = lane == 0 || left != bin;
+    const uint64_t heads = __ballot(head) & (~0ull >> (63 - lane));
+    const int first = 63 - __builtin_clzll(heads);
+    const uint64_t in_bin = before - __shfl(before, first);
+    const uint64_t k = (uint64_t)R.P.top_k;
+    const uint64_t place = in && B.bk >= 0 ? S.ties[bin] + (uint64_t)(lane - first) : 0;
+    const uint64_t bk_kept = wave_total(in && bin == B.bk && place < k ? v : 0);
+    const uint64_t zk = B.bk >= 0 ? S.hist[B.bk] + bk_kept : all;
+    const uint64_t target = R.P.top_p < 1.0f ? nucleus(R.P.top_p, zk) : ~0ull;
+    const bool kept = in && (B.bk < 0 || place < k) && S.hist[in ? bin : 0] + in_bin < target &&
+                      v >= weight_floor(R.P.min_p, R.W.shift);
+    const uint64_t keep = __ballot(kept);
+    const int last = keep != 0 ? 63 - __builtin_clzll(keep) : -1;
+    const int lim = last >= 0 ? __builtin_amdgcn_readlane(bin, last) : B.lo;
+    if (lane < slices) {
+        uint64_t t = slice_total;
+        for (int b = B.lo; b < lim; ++b) t += w.weight[((int64_t)local * slices + lane) * kBins + b];
+        L.slice[lane] = t;
+    }
+    if (bin == lim && lane <= last)
+        atomicAdd((unsigned long long*)&L.slice[slice_of(row, (int64_t)lo, slices)], (unsigned long long)v);
+    if (lane == last) L.end = mine;
+    if (lane == 0) {
+        if (last < 0) L.end = 0;
+        L.lim = lim;
+    }
+}
 
 // Ascending bitonic sort in LDS; size a power of two.
 __device__ __forceinline__ void sort_list(uint64_t* list, int size) {
@@ -862,105 +926,111 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
         all = B.all;
         S.hist[tid] = run0, S.hist[kRowThreads + tid] = run1;
         if (R.P.top_k > 0) S.ties[tid] = cnt0, S.ties[kRowThreads + tid] = cnt1;
-        int size = 64;
-        while (size < (int)listed) size <<= 1;
-        for (int i = tid; i < size; i += kRowThreads)
-            L.before[i] = i >= (int)listed ? ~0ull : i == tid ? entry : w.list[(int64_t)local * kList + i];
-        if (tid == 0) L.last = -1;
-        __syncthreads();
-        if (listed <= 512) {
-            // an entry's rank is the number of entries before it (all differ); 1024 / size threads share the count
-            for (int i = tid; i < size; i += kRowThreads) L.rank[i] = 0;
+        if (listed <= 64) {
+            // a wave holds the list: no workgroup-wide step until the answer
             __syncthreads();
-            const int e = tid & (size - 1), parts = kRowThreads / size;
-            const int each = ((int)listed + parts - 1) / parts, i0 = tid / size * each;
-            const int i1 = i0 + each < (int)listed ? i0 + each : (int)listed;
-            if (e < (int)listed) {
-                int rank = 0;
-                const uint64_t mine = L.before[e];
-#pragma unroll 8
-                for (int i = i0; i < i1; ++i) rank += L.before[i] < mine;
-                atomicAdd(&L.rank[e], rank);
-            }
+            if (wave == 0) short_list<F32>(R, B, w, row, local, slices, entry, (int)listed, slice_total, all, L);
             __syncthreads();
-            if (tid < (int)listed) L.list[L.rank[tid]] = L.before[tid];
-            __syncthreads();
+            lim = L.lim;
+            end = L.end;
         } else {
-            for (int i = tid; i < size; i += kRowThreads) L.list[i] = L.before[i];
+            int size = 64;
+            while (size < (int)listed) size <<= 1;
+            for (int i = tid; i < size; i += kRowThreads)
+                L.before[i] = i >= (int)listed ? ~0ull : i == tid ? entry : w.list[(int64_t)local * kList + i];
+            if (tid == 0) L.last = -1;
             __syncthreads();
-            sort_list(L.list, size);
-        }
-        // running weight of the list: four consecutive entries a thread
-        const int p0 = 4 * tid;
-        uint64_t v[4], sum = 0;
-        int bin[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in = p0 + i < (int)listed;
-            const float x = value_of(~(uint32_t)((in ? L.list[p0 + i] : 0) >> 32));
-            v[i] = in ? R.W.of(x) : 0;
-            bin[i] = in ? R.bin(x) : -1;
-            sum += v[i];
-        }
-        uint64_t total;
-        uint64_t run = block_scan(sum, S, total);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (bin[i] >= 0) {
-                const int p = p0 + i;
-                L.before[p] = run;
-                run += v[i];
-                const float px = p > 0 ? value_of(~(uint32_t)(L.list[p - 1] >> 32)) : 0.0f;
-                if (p == 0 || R.bin(px) != bin[i]) L.first[bin[i]] = p;
+            if (listed <= 512) {
+                // an entry's rank is the number of entries before it (all differ); 1024 / size threads share the count
+                for (int i = tid; i < size; i += kRowThreads) L.rank[i] = 0;
+                __syncthreads();
+                const int e = tid & (size - 1), parts = kRowThreads / size;
+                const int each = ((int)listed + parts - 1) / parts, i0 = tid / size * each;
+                const int i1 = i0 + each < (int)listed ? i0 + each : (int)listed;
+                if (e < (int)listed) {
+                    int rank = 0;
+                    const uint64_t mine = L.before[e];
+#pragma unroll 8
+                    for (int i = i0; i < i1; ++i) rank += L.before[i] < mine;
+                    atomicAdd(&L.rank[e], rank);
+                }
+                __syncthreads();
+                if (tid < (int)listed) L.list[L.rank[tid]] = L.before[tid];
+                __syncthreads();
+            } else {
+                for (int i = tid; i < size; i += kRowThreads) L.list[i] = L.before[i];
+                __syncthreads();
+                sort_list(L.list, size);
             }
-        __syncthreads();
-        // what top-k keeps, then the three rules for each listed token
-        uint64_t in_bk = 0;
-        const uint64_t k = (uint64_t)R.P.top_k;
+            // running weight of the list: four consecutive entries a thread
+            const int p0 = 4 * tid;
+            uint64_t v[4], sum = 0;
+            int bin[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (bin[i] >= 0 && bin[i] == B.bk && S.ties[B.bk] + (uint64_t)(p0 + i - L.first[B.bk]) < k) in_bk += v[i];
-        block_scan(in_bk, S, total);
-        const uint64_t zk = B.bk >= 0 ? S.hist[B.bk] + total : all;
-        const uint64_t target = R.P.top_p < 1.0f ? nucleus(R.P.top_p, zk) : ~0ull;
-        int last = -1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (bin[i] >= 0) {
-                const int p = p0 + i, f = L.first[bin[i]];
-                const bool rank_ok = B.bk < 0 || S.ties[bin[i]] + (uint64_t)(p - f) < k;
-                const bool sum_ok = S.hist[bin[i]] + (L.before[p] - L.before[f]) < target;
-                if (rank_ok && sum_ok && v[i] >= floor_w) last = p;
+            for (int i = 0; i < 4; ++i) {
+                const bool in = p0 + i < (int)listed;
+                const float x = value_of(~(uint32_t)((in ? L.list[p0 + i] : 0) >> 32));
+                v[i] = in ? R.W.of(x) : 0;
+                bin[i] = in ? R.bin(x) : -1;
+                sum += v[i];
             }
-        if (last >= 0) atomicMax(&L.last, last);
-        __syncthreads();
-        last = L.last;
-        lim = B.lo;   // nothing listed is kept: the prefix ends before the listed bins
-        if (last >= 0) {
-            end = L.list[last];
-            lim = R.bin(value_of(~(uint32_t)(end >> 32)));
-        }
-        // kept weight of each slice: its bins below lo (from the gather kernel) and on to lim, and the
-        // listed tokens of lim
-        for (int s = wave; s < slices; s += kRowWaves) {
-            const int64_t at = (int64_t)local * slices + s;
-            uint64_t t = 0;
-            for (int b = B.lo + lane; b < lim; b += 64) t += w.weight[at * kBins + b];
-            t = wave_total(t);
-            if (lane == s) L.slice[s] = slice_total + t;
-        }
-        __syncthreads();
-        if (last >= 0)
+            uint64_t total;
+            uint64_t run = block_scan(sum, S, total);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (bin[i] == lim && p0 + i <= last) {
-                    const int64_t vec = ((int64_t)(uint32_t)L.list[p0 + i] + row.off) / kPer;
-                    int s = (int)(vec * slices / nvec);
-                    while (s + 1 < slices && vec >= nvec * (s + 1) / slices) ++s;
-                    while (s > 0 && vec < nvec * s / slices) --s;
-                    atomicAdd((unsigned long long*)&L.slice[s], (unsigned long long)v[i]);
+                if (bin[i] >= 0) {
+                    const int p = p0 + i;
+                    L.before[p] = run;
+                    run += v[i];
+                    const float px = p > 0 ? value_of(~(uint32_t)(L.list[p - 1] >> 32)) : 0.0f;
+                    if (p == 0 || R.bin(px) != bin[i]) L.first[bin[i]] = p;
                 }
-        __syncthreads();
+            __syncthreads();
+            // what top-k keeps, then the three rules for each listed token
+            uint64_t in_bk = 0;
+            const uint64_t k = (uint64_t)R.P.top_k;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (bin[i] >= 0 && bin[i] == B.bk && S.ties[B.bk] + (uint64_t)(p0 + i - L.first[B.bk]) < k) in_bk += v[i];
+            block_scan(in_bk, S, total);
+            const uint64_t zk = B.bk >= 0 ? S.hist[B.bk] + total : all;
+            const uint64_t target = R.P.top_p < 1.0f ? nucleus(R.P.top_p, zk) : ~0ull;
+            int last = -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (bin[i] >= 0) {
+                    const int p = p0 + i, f = L.first[bin[i]];
+                    const bool rank_ok = B.bk < 0 || S.ties[bin[i]] + (uint64_t)(p - f) < k;
+                    const bool sum_ok = S.hist[bin[i]] + (L.before[p] - L.before[f]) < target;
+                    if (rank_ok && sum_ok && v[i] >= floor_w) last = p;
+                }
+            if (last >= 0) atomicMax(&L.last, last);
+            __syncthreads();
+            last = L.last;
+            lim = B.lo;   // nothing listed is kept: the prefix ends before the listed bins
+            if (last >= 0) {
+                end = L.list[last];
+                lim = R.bin(value_of(~(uint32_t)(end >> 32)));
+            }
+            // kept weight of each slice: its bins below lo (from the gather kernel) and on to lim, and the
+            // listed tokens of lim
+            for (int s = wave; s < slices; s += kRowWaves) {
+                const int64_t at = (int64_t)local * slices + s;
+                uint64_t t = 0;
+                for (int b = B.lo + lane; b < lim; b += 64) t += w.weight[at * kBins + b];
+                t = wave_total(t);
+                if (lane == s) L.slice[s] = slice_total + t;
+            }
+            __syncthreads();
+            if (last >= 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (bin[i] == lim && p0 + i <= last) {
+                        const int s = slice_of(row, (int64_t)(uint32_t)L.list[p0 + i], slices);
+                        atomicAdd((unsigned long long*)&L.slice[s], (unsigned long long)v[i]);
+                    }
+            __syncthreads();
+        }
     }
     // the slice in which the goal lies, and the goal within it
     const uint64_t sv = lane < slices ? (R.filtered ? L.slice[lane] : slice_total) : 0;

@@ -235,8 +235,7 @@ struct Shared {
     uint32_t ties[kSegs];
     uint64_t part[kRowWaves + 1];
     uint64_t found_above;
-    uint32_t found_bin, flags;
-    uint32_t top;
+    uint32_t found_bin;
 };
 
 // Exclusive prefix of v over the workgroup's threads; total to all.
@@ -490,7 +489,7 @@ __device__ __attribute__((noinline)) void whole_row(const SampleArgs& a, int64_t
     }
 }
 
-// ------------------------------------------------------------ the four launches
+// ------------------------------------------------------------ the five launches
 
 struct SliceStat {
     uint32_t top, low, bad, valid;   // keys of the unmasked logits
@@ -720,11 +719,16 @@ __device__ Borders borders(const RowPlan& R, const BinSums& sums, Shared& S) {
         B.lim = p1 < B.lim ? p1 : B.lim;
     }
     if (R.P.min_p > 0.0f) {
-        // within one bin of where the weight falls to min_p (float rounding of bin())
-        const double d = -log2((double)R.P.min_p) / R.W.scale * (double)R.c;
-        const int m = d < (double)kBins ? (int)d : kBins;
-        B.lo = m - 1 < B.lo ? (m > 0 ? m - 1 : 0) : B.lo;
-        B.lim = m + 1 < B.lim ? m + 1 : B.lim;
+        // Of weights that round to the floor: a bin more than those of floor + 1/2 and floor - 1/2 (float
+        // rounding of bin()). Where the row's range passes the largest float, bin() puts what lies farther
+        // from the top into the last bin.
+        const double f = (double)weight_floor(R.P.min_p, R.W.shift), one = (double)(1ull << R.W.shift);
+        const double per = (double)R.c / R.W.scale;   // bins per binary order
+        const double d0 = -log2((f + 0.5) / one) * per, d1 = -log2((f - 0.5) / one) * per;
+        const int m0 = d0 < (double)kBins ? (int)d0 - 1 : kBins, m1 = d1 < (double)kBins ? (int)d1 + 1 : kBins;
+        const bool far = (double)R.c * 3.4028234663852886e38 < (double)(kBins - 1);
+        B.lo = m0 < B.lo ? (m0 > 0 ? m0 : 0) : B.lo;
+        B.lim = m1 < B.lim && !far ? m1 : B.lim;
     }
     if (R.capped && B.lim == kBins - 1) B.lim = kBins - 2;
     __syncthreads();

@@ -115,6 +115,31 @@ def test_weights_that_vanish():
             check(x, u, temperature=t, **kw)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_min_p_at_the_smallest_integer_weights(dtype):
+    """min-p compares integers of 2^-44; u = 0 draws the first token that is kept."""
+    order = float(np.log(2.0))
+    x = torch.linspace(-47 * order, 0, 4000, dtype=torch.float64).flip(0)
+    x = torch.cat([x, x.flip(0)]).to(dtype)     # 0 down to 47 orders and up again
+    w = np.round(np.exp2(44 + f64(x) / order))
+    for first in (3300, 3500, 3700, 3730, 3760, 3800, 3990):   # the row begins about there, goes down, then up
+        row, v = x[first:], w[first:]
+        for min_p in (2.0 ** -44, 1.01 * 2.0 ** -44, 1.5 * 2.0 ** -44, 2.0 ** -43, 3.3 * 2.0 ** -44, 1e-13, 1e-12, 1e-30):
+            floor = np.ceil(float(np.float32(min_p)) * 2.0 ** 44)
+            kept = np.flatnonzero((v >= floor) & (v > 0))
+            token, _ = lm.sample(row[None].cuda(), torch.zeros(1, device="cuda"), min_p=min_p)
+            assert int(token) == kept[0], (first, min_p, int(token), kept[0])
+
+
+def test_a_range_past_the_largest_float():
+    rng = np.random.default_rng(8)
+    x = torch.from_numpy(rng.uniform(-3.3e38, 3.3e38, (20, 3000)).astype(np.float32)).cuda()
+    u = torch.from_numpy(rng.random(20).astype(np.float32)).clamp(max=1 - 2.0 ** -24).cuda()
+    for kw in (dict(min_p=0.01), dict(min_p=0.04), dict(min_p=0.2), dict(top_p=0.9), dict(top_k=2000, min_p=0.045),
+               dict(top_k=2900, top_p=0.999), dict()):
+        check(x, u, temperature=2e38, **kw)
+
+
 def test_more_rows_than_one_set_of_launches():
     x, u, rng = logits_of(700, 300, torch.bfloat16, 22)
     x[600, 5] = float("nan")

@@ -196,8 +196,8 @@ int lmhead_sample(const lmhead_sample_problem* p, const void* logits, const floa
     if (st != LMHEAD_OK) return st;
     if (workspace == nullptr) return LMHEAD_ERR_ARG;
     if (p->n > 0 && (logits == nullptr || u == nullptr || token == nullptr)) return LMHEAD_ERR_ARG;
-    if (!aligned(logits, p->logits_dtype == LMHEAD_DTYPE_F32 ? 4 : 2) || !aligned(workspace, 256) || !aligned(u, 4) || !aligned(token, 4) ||
-        !aligned(logprob, 4) || !aligned(p->row_temperature, 4) || !aligned(p->row_top_k, 4) ||
+    if (!aligned(logits, p->logits_dtype == LMHEAD_DTYPE_F32 ? 4 : 2) || !aligned(workspace, 256) || !aligned(u, 4) ||
+        !aligned(token, 4) || !aligned(logprob, 4) || !aligned(p->row_temperature, 4) || !aligned(p->row_top_k, 4) ||
         !aligned(p->row_top_p, 4) || !aligned(p->row_min_p, 4))
         return LMHEAD_ERR_ALIGN;
     if (workspace_bytes < lmhead_sample_workspace_size(p)) return LMHEAD_ERR_WORKSPACE;
@@ -209,7 +209,6 @@ int lmhead_sample(const lmhead_sample_problem* p, const void* logits, const floa
         return launched();
     }
     SampleArgs a;   // the first launch clears the header
-
     a.logits = logits;
     a.logits_f32 = p->logits_dtype == LMHEAD_DTYPE_F32;
     a.n = p->n;

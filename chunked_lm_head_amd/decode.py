@@ -13,6 +13,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (LMHEAD_ERR_SHAPE, LMHeadError, _check_f32, _ok, _on_device_of, _p, _stream, lib)
 
@@ -244,6 +245,7 @@ class RMSNorm(torch.autograd.Function):
         return (f.y, f.residual_out) if residual is not None else f.y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dr=None):
         r, weight, rstd = ctx.saved_tensors
         need_x, need_w, need_res = ctx.needs_input_grad[:3]
@@ -256,7 +258,10 @@ class RMSNorm(torch.autograd.Function):
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """RMS norm with gradients for x, weight and residual: y, or (y, residual_out)
-    with a residual. weight_offset 1 for zero-centred weights."""
+    with a residual. weight_offset 1 for zero-centred weights. Differentiable once.
+    A backward captured into a graph must be the leaves' only one: drop eager
+    graphs of the same leaves first (torch's gradient accumulation ties a leaf
+    to the stream of its first use), or take torch.autograd.grad."""
     return RMSNorm.apply(x, weight, residual, eps, weight_offset)
 
 
@@ -340,8 +345,11 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, want
             _check_gpu(name, v, (torch.int32 if name == "top_k" else torch.float32,), (n,), dev)
             rows[name] = v
         elif v is not None:
-            if name in ("temperature", "top_p") and not v > 0:
+            # as the fp32 number that the C call gets, where 0 means off
+            if name in ("temperature", "top_p") and not ctypes.c_float(v).value > 0:
                 raise ValueError(f"{name} must be positive")
+            if name == "top_k" and (v != int(v) or not -1 << 31 <= v < 1 << 31):
+                raise ValueError("top_k must be a 32-bit integer")
             scalars[name] = v
     p = lmhead_sample_problem(n, vocab, ld, _DTYPES[logits.dtype], int(scalars.get("top_k", 0)),
                               float(scalars.get("temperature", 0.0)), float(scalars.get("top_p", 0.0)),

@@ -92,6 +92,39 @@ def test_training_step_captured():
             assert torch.equal(a, b), rep
 
 
+def test_autograd_captured():
+    """The norm's gradients through autograd in a graph, and no second derivative."""
+    n, hidden = 65, 512
+    x, res, nw, _, _ = setup(n, hidden, 8, 6)
+    leaves = [t.clone().requires_grad_() for t in (x, res, nw)]
+    dy, dr = torch.randn_like(x), torch.randn_like(x)
+
+    def step():
+        y, r = lm.rms_norm(leaves[0], leaves[2], leaves[1])
+        return (y.detach(),) + torch.autograd.grad((y, r), (leaves[0], leaves[2], leaves[1]), (dy, dr))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for rep in range(3):
+        with torch.no_grad():
+            leaves[0].normal_()
+        dy.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, step()):
+            assert torch.equal(a, b), rep
+    y, _ = lm.rms_norm(leaves[0], leaves[2], leaves[1])
+    g, = torch.autograd.grad(y, leaves[0], dy.clone().requires_grad_(), create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 def test_streams_at_once():
     """Two streams with their own inputs and workspaces, interleaved."""
     hidden, vocab = 512, 20000

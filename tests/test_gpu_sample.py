@@ -251,6 +251,8 @@ def test_python_checks():
     for bad in (lambda: lm.sample(x.half(), u), lambda: lm.sample(x, u[:2]), lambda: lm.sample(x, u.double()),
                 lambda: lm.sample(x.t(), u), lambda: lm.sample(x, u, temperature=0.0), lambda: lm.sample(x, u, top_p=0.0),
                 lambda: lm.sample(x, u, top_k=torch.ones(3, device="cuda")), lambda: lm.sample(x, u, min_p=u[:1]),
+                lambda: lm.sample(x, u, temperature=1e-50), lambda: lm.sample(x, u, top_p=1e-50),
+                lambda: lm.sample(x, u, top_k=(1 << 32) + 5), lambda: lm.sample(x, u, top_k=2.5),
                 lambda: lm.sample(x[0], u), lambda: lm.sample(x[:1].expand(3, 100), u)):
         with pytest.raises(ValueError):
             bad()

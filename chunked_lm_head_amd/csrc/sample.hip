@@ -1137,8 +1137,8 @@ __global__ __launch_bounds__(kRowThreads) void sample_pick_kernel(SampleArgs a, 
 
 // Workgroups a row: four to a compute unit over all rows, each with some
 // kSliceTokens tokens at least (a slice costs its histogram's traffic and its
-// share of the row's; 64 rows of 128,256: 8 slices 73 us, 16 slices 81 us; 256
-// rows of 151,936: 4 slices 156 us, 2 slices 179 us, 8 slices 167 us).
+// share of the row's; 64 rows of 128,256: 8 slices 72 us, 16 slices 82 us; 256
+// rows of 151,936: 4 slices 153 us, 2 slices 171 us, 8 slices 164 us).
 constexpr int64_t kSliceTokens = 16384;
 int slices_of(int64_t rows, int64_t vocab) {
     int64_t s = 4 * 256 / rows;

@@ -217,8 +217,8 @@ size_t lmhead_sample_workspace_size(const lmhead_sample_problem* p);
  *      0 .. v passes u times all kept weight.
  * A logit of -infinity masks a token (never kept). Weights are held as
  * integers of 2^-s, s = min(44, 62 - ceil(log2(vocab))), so every sum is
- * exact and independent of its order; a token below half of that step
- * beside the most likely one is never drawn.
+ * exact and independent of its order, and min-p compares those integers; a
+ * token below half of that step beside the most likely one is never drawn.
  *   logits    device, logits_dtype [n, ld], aligned to its elements (any ld).
  *   u         device, fp32 [n], in [0, 1).
  *   token     device, int32 [n].

@@ -192,6 +192,26 @@ def test_autograd_norm_in_front_of_the_loss():
     assert torch.equal(x3.grad, torch.ones_like(x3)) and torch.equal(r3.grad, torch.ones_like(r3))
 
 
+def test_one_tensor_in_two_places():
+    """x as its own residual, and gradients that do not share memory."""
+    x, dy = (torch.randn(9, 256, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w = torch.randn(256, device="cuda").to(torch.bfloat16)
+    f = lm.rms_norm_forward(x, w, x)
+    dx, _ = lm.rms_norm_backward(dy, f.residual_out, w, f.rstd)
+    a = x.clone().requires_grad_()
+    y, _ = lm.rms_norm(a, w, a)
+    y.backward(dy)
+    assert torch.equal(y, f.y) and torch.equal(a.grad, dx + dx)
+    a, b = x.clone().requires_grad_(), x.clone().requires_grad_()
+    lm.rms_norm(a, w, b)[0].backward(dy)
+    assert torch.equal(a.grad, dx) and torch.equal(b.grad, dx)
+    a.grad.zero_()
+    assert torch.equal(b.grad, dx)
+    a, b = x.clone().requires_grad_(), x.clone().requires_grad_()
+    lm.rms_norm(a, w, b)[1].backward(dy)       # the residual stream alone
+    assert torch.equal(a.grad, dy) and torch.equal(b.grad, dy)
+
+
 def test_empty():
     x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(256, dtype=torch.bfloat16, device="cuda")

@@ -12,11 +12,10 @@
 // block's sum is added to the fp32 accumulator after the two scales.
 //
 // Few rows (up to kStreamRows): the W stream from memory decides (Hd bytes per
-// vocabulary row and pass). Waves read W fragments straight into registers,
-// and the four waves of a workgroup take a quarter of the columns each, so a
-// workgroup is small enough to spread evenly over the chip and nothing is
-// staged or waited for inside the loop; their sums are joined in wave order
-// through LDS. More rows: the matrix instructions decide, on 256-row tiles.
+// vocabulary row and pass). Every wave takes a share of the vocabulary with an
+// LDS ring of its own and no barrier. More rows: the matrix instructions
+// decide, on 256-row tiles (or the same stream over sets of 64 rows where the
+// tiles would be few).
 #include "decode_kernels.h"
 #include "host_util.h"
 
@@ -136,7 +135,7 @@ constexpr int kStreamGroup = 8;      // waves per workgroup
 
 template <int VT, int NT, bool PACKED>
 __global__ __launch_bounds__(64 * kStreamGroup) void logits_stream_kernel(LogitsArgs a, const uint8_t* packed,
-                                                                         const float* scale_t, int n_pad) {
+                                                                         const float* scale_t, int n_pad, int waves) {
     constexpr int kStage = 16 * VT * 128;
     __shared__ __attribute__((aligned(16))) char smem[kStreamGroup * 2 * kStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -150,7 +149,8 @@ __global__ __launch_bounds__(64 * kStreamGroup) void logits_stream_kernel(Logits
     auto block_of = [&](int k) { return k + rot < nb ? k + rot : k + rot - nb; };
     const int64_t groups = (a.vocab + 15) / 16;
     const int id = (int)blockIdx.x * kStreamGroup + wave;
-    const int64_t first = groups * id / kStreamWaves, last = groups * (id + 1) / kStreamWaves;
+    const int64_t first = groups * id / waves, last = groups * (id + 1) / waves;
+    const int set = blockIdx.y;   // of 64 rows
     char* const ring = smem + wave * 2 * kStage;
     // load u: rows 8 u .. + 8 in lane order; row r + 8 has swizzle(r) ^ 4
     const int lr = lane >> 3, lq = (lane & 7) ^ swizzle(lr);
@@ -160,8 +160,8 @@ __global__ __launch_bounds__(64 * kStreamGroup) void logits_stream_kernel(Logits
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         if (PACKED) {
-            x[j] = packed + (int64_t)j * nb * 2048 + lane * 16;
-            sa[j] = scale_t + (n_pad == 64 ? 4 * c + j : 16 * j + c);
+            x[j] = packed + (int64_t)(4 * set + j) * nb * 2048 + lane * 16;
+            sa[j] = scale_t + 64 * set + (n_pad % 64 == 0 ? 4 * c + j : 16 * j + c);
         } else {
             const int64_t r = 16 * j + c < a.n ? 16 * j + c : a.n - 1;
             x[j] = a.a + r * a.hidden + 16 * g;
@@ -259,27 +259,35 @@ __global__ __launch_bounds__(64 * kStreamGroup) void logits_stream_kernel(Logits
         for (int i = 0; i < VT; ++i)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                store4(a, 16 * j + c, v0 + 16 * i + 4 * g, 16 * i + 4 * g < vrows ? vrows - 16 * i - 4 * g : 0, acc[i][j]);
+                store4(a, 64 * set + 16 * j + c, v0 + 16 * i + 4 * g, 16 * i + 4 * g < vrows ? vrows - 16 * i - 4 * g : 0, acc[i][j]);
     }
 }
 
+// Waves for each of the sets of 64 rows: an equal part of the chip's, whole workgroups.
+int64_t stream_waves(int64_t sets) {
+    const int64_t w = kStreamWaves / sets / kStreamGroup * kStreamGroup;
+    return w > kStreamGroup ? w : kStreamGroup;
+}
+
 template <int VT, int NT, bool PACKED>
-void stream(const LogitsArgs& a, const uint8_t* packed, const float* scale_t, int n_pad, hipStream_t s) {
+void stream(const LogitsArgs& a, const uint8_t* packed, const float* scale_t, int64_t n_pad, int sets, hipStream_t s) {
+    const int waves = (int)stream_waves(sets);
     logits_stream_kernel<VT, NT, PACKED>
-        <<<kStreamWaves / kStreamGroup, 64 * kStreamGroup, 0, s>>>(a, packed, scale_t, n_pad);
+        <<<dim3(waves / kStreamGroup, sets), 64 * kStreamGroup, 0, s>>>(a, packed, scale_t, (int)n_pad, waves);
 }
 
 // Groups of 16 rows at a time: the wave's whole share where it is at most five
 // (more would not fit the LDS or the registers), else a divisor-like part of it.
 template <int NT, bool PACKED>
-void stream_by_share(const LogitsArgs& a, const uint8_t* packed, const float* scale_t, int n_pad, hipStream_t s) {
-    const int64_t share = cdiv(cdiv(a.vocab, 16), kStreamWaves);
+void stream_by_share(const LogitsArgs& a, const uint8_t* packed, const float* scale_t, int64_t n_pad, int sets,
+                     hipStream_t s) {
+    const int64_t share = cdiv(cdiv(a.vocab, 16), stream_waves(sets));
     const int64_t vt = cdiv(share, cdiv(share, 5));
-    if (vt <= 1) return stream<1, NT, PACKED>(a, packed, scale_t, n_pad, s);
-    if (vt == 2) return stream<2, NT, PACKED>(a, packed, scale_t, n_pad, s);
-    if (vt == 3) return stream<3, NT, PACKED>(a, packed, scale_t, n_pad, s);
-    if (vt == 4) return stream<4, NT, PACKED>(a, packed, scale_t, n_pad, s);
-    return stream<5, NT, PACKED>(a, packed, scale_t, n_pad, s);
+    if (vt <= 1) return stream<1, NT, PACKED>(a, packed, scale_t, n_pad, sets, s);
+    if (vt == 2) return stream<2, NT, PACKED>(a, packed, scale_t, n_pad, sets, s);
+    if (vt == 3) return stream<3, NT, PACKED>(a, packed, scale_t, n_pad, sets, s);
+    if (vt == 4) return stream<4, NT, PACKED>(a, packed, scale_t, n_pad, sets, s);
+    return stream<5, NT, PACKED>(a, packed, scale_t, n_pad, sets, s);
 }
 
 // ------------------------------------------------------------- many rows
@@ -558,6 +566,25 @@ size_t logits_workspace(int64_t n, int hidden, int out_f32) {
     return (size_t)(n_pad * hidden + round_up(4 * n_pad * (hidden / kQBlock) + 1, 256));
 }
 
+// More rows than kStreamRows against so few columns that tiles leave most of the
+// chip idle: the stream kernel over sets of 64 rows, while a wave has one group
+// of 16 columns (two for an fp32 output, whose tile takes longer; half the waves
+// at most one where a bf16 tile of 128 rows, the quickest, is the other way).
+// us at hidden 5120, stream and tiles:
+//                        70 rows   130 rows   300 rows   700 rows   2048 rows
+//   1000 columns, fp32    26, 67     26, 66     29, 69     34, 70      55, 74
+//   1000, bf16            26, 41     26, 53     29, 55     34, 57      54, 61
+//   4000, fp32            34, 68     31, 67     39, 70     63, 71
+//   4000, bf16            33, 41     31, 54     38, 56     60, 57 (two groups)
+//   16000, fp32           50, 69     60, 69     86, 75 (three groups)
+//   16000, bf16           48, 42     58, 54     84, 55 (three)
+bool few_groups(int64_t n, int64_t vocab, int out_f32) {
+    const int64_t sets = cdiv(n, kStreamRows), groups = cdiv(vocab, 16);
+    if (sets > kStreamWaves / kStreamGroup) return false;
+    if (!out_f32 && n <= 128 && sets * groups > kStreamWaves / 2) return false;
+    return cdiv(groups, stream_waves(sets)) <= (out_f32 ? 2 : 1);
+}
+
 template <bool EXACT, int VI, int VW>
 void tiles(TileArgs t, hipStream_t s) {
     t.tiles_n = t.n_pad / (64 * (8 / VW));
@@ -570,7 +597,7 @@ void tiles(TileArgs t, hipStream_t s) {
 }
 
 void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s) {
-    if (a.n <= 16) return stream_by_share<1, false>(a, nullptr, nullptr, 0, s);
+    if (a.n <= 16) return stream_by_share<1, false>(a, nullptr, nullptr, 0, 1, s);
     TileArgs t;
     t.p = a;
     t.n_pad = packed_rows(a.n, a.out_f32);
@@ -580,9 +607,11 @@ void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s) {
     t.scale_t = scale_t;
     pack_rows_kernel<<<grid_1d(t.n_pad * a.hidden / 16, 256, 8192), 256, 0, s>>>(a.a, a.a_scale, a.n, t.n_pad, a.hidden,
                                                                                 rows, scale_t);
-    if (a.n <= 32) return stream_by_share<2, true>(a, rows, scale_t, (int)t.n_pad, s);
-    if (a.n <= 48) return stream_by_share<3, true>(a, rows, scale_t, (int)t.n_pad, s);
-    if (a.n <= kStreamRows) return stream_by_share<4, true>(a, rows, scale_t, (int)t.n_pad, s);
+    if (a.n <= 32) return stream_by_share<2, true>(a, rows, scale_t, t.n_pad, 1, s);
+    if (a.n <= 48) return stream_by_share<3, true>(a, rows, scale_t, t.n_pad, 1, s);
+    if (a.n <= kStreamRows) return stream_by_share<4, true>(a, rows, scale_t, t.n_pad, 1, s);
+    if (few_groups(a.n, a.vocab, a.out_f32))
+        return stream_by_share<4, true>(a, rows, scale_t, t.n_pad, (int)cdiv(a.n, kStreamRows), s);
     const bool narrow = tile_rows(a.n, a.out_f32) == 128;
     if (a.out_f32) return narrow ? tiles<true, 4, 4>(t, s) : tiles<true, 4, 2>(t, s);
     return narrow ? tiles<false, 4, 4>(t, s) : tiles<false, 8, 2>(t, s);

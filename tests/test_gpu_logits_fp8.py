@@ -5,7 +5,7 @@ Tolerance. Products of e4m3 values are exact in fp32; a block's 128 products
 and the blocks' sums are fp32 additions, each off by at most one step (2^-23,
 truncation allowed) of a partial sum that the sum of magnitudes bounds: (128 +
 blocks) 2^-23 sum |a w|. A bf16 output adds half a step, 2^-8; with more than 64
-rows it comes from the 8-bit matrix instructions, which cut the eight products
+rows it may come from the 8-bit matrix instructions, which cut the eight products
 of aligned consecutive columns off 13 bits below the power of two of the
 largest one: at most 8 * 2^-13 of each eight's largest |a w| more
 (test_the_cut_off measures that the instructions do no worse)."""
@@ -61,19 +61,54 @@ def test_against_definition(n, vocab, hidden, dtype):
     assert torch.equal(out, lm.logits_fp8(a, sa, w, sw, out_dtype=dtype))
 
 
-def test_the_cut_off():
+# columns enough for the tiles on both output types (few columns go through the stream in sets of 64 rows)
+TILED = [(65, 16400, 256), (70, 16500, 128), (100, 16700, 384), (128, 16385, 640), (130, 22001, 128), (200, 16500, 256),
+         (257, 13300, 128), (300, 13200, 384), (513, 7300, 128), (1030, 4100, 256), (2048, 2200, 128)]
+
+
+@pytest.mark.parametrize("n,vocab,hidden", TILED)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_tiles_against_definition(n, vocab, hidden, dtype):
+    test_against_definition(n, vocab, hidden, dtype)
+
+
+@pytest.mark.parametrize("n,vocab,hidden", [(65, 17, 128), (129, 2000, 256), (700, 1000, 384), (1000, 33, 1280),
+                                            (2048, 1024, 128), (16384, 20, 128), (16400, 20, 128), (64, 300, 256)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sets_of_rows_against_definition(n, vocab, hidden, dtype):
+    test_against_definition(n, vocab, hidden, dtype)
+
+
+@pytest.mark.parametrize("n", [70, 200, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ld", [16500, 16501, 16504, 16512])
+@pytest.mark.parametrize("first", [0, 1, 4])
+def test_tiles_in_slices(n, dtype, ld, first):
+    """Row strides and first columns of every alignment: the values of whole rows, and the rest stays."""
+    rng = np.random.default_rng(9)
+    vocab = 16490
+    a, sa = operand(n + 1, 128, 1, rng)
+    w, sw = operand(vocab, 128, 128, rng)
+    buf = torch.full((n + 1, ld), 7.0, dtype=dtype, device="cuda")
+    out = lm.logits_fp8(a[1:], sa[1:], w, sw, out=buf[:n, first:first + vocab])
+    assert torch.equal(out, lm.logits_fp8(a[1:], sa[1:], w, sw, out_dtype=dtype))
+    assert (buf[:n, :first] == 7.0).all() and (buf[:n, first + vocab:] == 7.0).all() and (buf[n] == 7.0).all()
+
+
+@pytest.mark.parametrize("vocab", [16, 9008])
+def test_the_cut_off(vocab):
     """2^16 beside seven 2^e in one eight of columns, -2^16 beside seven 2^e in
     the next, 2^e alone in the other 14: the large ones cancel, so the sum shows
     how much of the small ones arrived. From 2^(16 - 13) up all of them do;
     smaller ones may be lost beside 2^16, and only there."""
-    n, vocab = 80, 16
+    n = 80
     for e, whole in ((4, True), (3, True), (2, False), (-6, False)):
         a, w = torch.zeros(n, 128), torch.zeros(vocab, 128)
         a[:, :], w[:, :] = 2.0 ** (e // 2), 2.0 ** (e - e // 2)
         a[:, 0], w[:, 0] = 256.0, 256.0
         a[:, 8], w[:, 8] = 256.0, -256.0
         out = lm.logits_fp8(a.to(torch.float8_e4m3fn).cuda(), torch.ones(n, 1, device="cuda"),
-                            w.to(torch.float8_e4m3fn).cuda(), torch.ones(1, 1, device="cuda"))
+                            w.to(torch.float8_e4m3fn).cuda(), torch.ones(-(-vocab // 128), 1, device="cuda"))
         got = f64(out) / 2.0 ** e
         least = 126 if whole else 112
         assert (got >= least * (1 - 2.0 ** -8)).all() and (got <= 126 * (1 + 2.0 ** -8)).all(), (e, got[0, 0])

@@ -21,9 +21,9 @@
  * output may be the same buffer as an input only where an entry says so.
  *
  * 8-bit values are OCP e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest
- * 448, no infinity), rounded to nearest even. A block scale is fp32: the value
- * is q * scale. The scale of a block is its largest magnitude / 448, at least
- * 2^-126 (1 for a block of zeros).
+ * 448, no infinity), rounded to nearest even from the fp32 quotient of value
+ * and scale. A block scale is fp32: the value is q * scale. The scale of a block
+ * is its largest magnitude / 448, at least 2^-126 (1 for a block of zeros).
  */
 #ifndef LMHEAD_DECODE_H
 #define LMHEAD_DECODE_H

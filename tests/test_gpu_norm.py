@@ -250,3 +250,50 @@ def test_quantize_bad_values(block_rows):
     else:
         clean[:128, :128] = clean[128:, 128:] = False
     assert (v[clean] == 1.0).all()
+
+
+def e4m3_of(v):
+    """Nearest e4m3 value (ties to even) of fp64 numbers within +-448."""
+    mag = np.abs(v)
+    e = np.maximum(np.floor(np.log2(np.where(mag > 0, mag, 1.0))), -6.0)
+    step = np.exp2(e - 3.0)
+    return np.sign(v) * np.minimum(np.round(mag / step) * step, 448.0)
+
+
+def quotients(top):
+    """Blocks of 128 fp32 values, the first of each the largest: every bf16
+    mantissa below it, at eight binary orders and both signs. Their number, and
+    the quotients and scales as one fp32 division each."""
+    m = (128 + np.arange(128)) / 128.0
+    orders = np.exp2(-np.arange(1, 9))[:, None] * m * np.where(np.arange(128) % 3 == 0, -1.0, 1.0)
+    low, high = orders[:, :64], orders[:, 64:]
+    blocks = np.zeros((16, 128))
+    blocks[:8, 1:65], blocks[8:, 1:65] = low, high
+    blocks[:, 65:] = -blocks[:, 2:65]
+    x = blocks[None] * np.exp2(np.floor(np.log2(top)))[:, None, None]
+    x[:, :, 0] = top[:, None]
+    x = x.astype(np.float32)
+    s = (np.abs(x).max(2) / np.float32(448)).astype(np.float32)
+    return x.reshape(len(top), -1), s, (x / s[:, :, None]).astype(np.float64).reshape(len(top), -1)
+
+
+@pytest.mark.parametrize("order", [0, 7, -60, 90, -110, 127])
+def test_quotients_are_one_division(order):
+    """q is the e4m3 rounding of the fp32 quotient y / s, s that of max / 448: a
+    product with 1 / s is off by a step where the quotient is a tie (153 of 204
+    is 336, halfway between 320 and 352)."""
+    top = (128 + np.arange(128)) / 128.0 * 2.0 ** order
+    x, s, want = quotients(top)
+    want = e4m3_of(want)
+    q, scale = lm.quantize_fp8(bf(x), 1)
+    assert np.array_equal(scale.cpu().numpy(), s)
+    assert np.array_equal(f64(q), want), np.argwhere(f64(q) != want)[:5]
+    # the same rows as 128 x 128 blocks of one row each
+    q, scale = lm.quantize_fp8(bf(x).repeat_interleave(128, 0), 128)
+    assert np.array_equal(scale.cpu().numpy(), s)
+    assert np.array_equal(f64(q), np.repeat(want, 128, 0))
+    # a row of ones has rstd 1 at eps 0, so the norm's y is the weight
+    for i in (0, 10, 63, 76, 80, 127):
+        w = torch.from_numpy(x[i]).cuda()
+        q, scale, _ = lm.rms_norm_quant(torch.ones(1, x.shape[1], dtype=torch.bfloat16, device="cuda"), w, eps=0.0)
+        assert np.array_equal(scale.cpu().numpy()[0], s[i]) and np.array_equal(f64(q)[0], want[i]), i

@@ -325,13 +325,15 @@ def _check_row_temperature(rt, n: int):
 
 
 def _on_device_of(arg: int):
-    """Run a helper with the device of its positional argument `arg` (H)
-    current, so that the library's device check, its launches and the
-    current-stream lookup all refer to the tensors' GPU."""
+    """Run a helper with the device of its parameter number `arg` (H) current,
+    given by place or by keyword, so that the library's device check, its
+    launches and the current-stream lookup all refer to the tensors' GPU."""
     def wrap(fn):
+        name = fn.__code__.co_varnames[arg]
+
         @functools.wraps(fn)
         def call(*args, **kwargs):
-            t = args[arg] if len(args) > arg else None
+            t = args[arg] if len(args) > arg else kwargs.get(name)
             if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch.cuda.current_device():
                 with torch.cuda.device(t.device):
                     return fn(*args, **kwargs)

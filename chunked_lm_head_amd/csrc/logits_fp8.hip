@@ -335,9 +335,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
     const int lr = wave * 8 * kLoads + (lane >> 3);
     const int lq = (lane & 7) ^ swizzle(lr);
     const uint32_t vw[2] = {(uint32_t)(lr * a.hidden + lq * 16), (uint32_t)(lr * a.hidden + (lq ^ 4) * 16)};
-    // step k is column block (k + rot) mod nb, an eighth of the way on from one XCD to the
-    // next (fewer waves at the same columns of memory; 256 rows: 233 us without, 215 us with)
-    const int rot = (int)(blockIdx.x % 8) * nb / 8;
+    // step k is column block (k + rot) mod nb, an eighth of the way on from one eighth of
+    // the vocabulary to the next: the XCDs are at different ones (map_tile), so fewer waves
+    // meet at the same columns of memory (256 rows: 233 us without, 215 us with), and every
+    // row of the batch sums a logit in the same order
+    const int rot = (int)(tv * 8 / t.tiles_v) * nb / 8;
     auto block_of = [&](int k) {
         const int kc = (k < nb ? k : nb - 1) + rot;
         return kc < nb ? kc : kc - nb;

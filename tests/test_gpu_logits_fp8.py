@@ -169,3 +169,16 @@ def test_empty_and_python_checks():
                 lambda: lm.logits_fp8(a, sa, w, sw, out=torch.empty(300, 4, device="cuda").t())):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("n,vocab", [(2048, 2200), (1500, 4500), (300, 16500), (700, 1000), (64, 5000)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_equal_rows_get_equal_logits(n, vocab, dtype):
+    """One hidden state at every place of the batch: the same bits everywhere."""
+    rng = np.random.default_rng(n + vocab)
+    hidden = 1280
+    a, sa = operand(1, hidden, 1, rng)
+    w, sw = operand(vocab, hidden, 128, rng)
+    many = a.view(torch.uint8).expand(n, hidden).contiguous().view(torch.float8_e4m3fn)
+    out = lm.logits_fp8(many, sa.expand(n, -1).contiguous(), w, sw, out_dtype=dtype)
+    assert torch.equal(out, out[:1].expand_as(out)), (out != out[:1]).sum()

@@ -229,7 +229,7 @@ int lmhead_sample(const lmhead_sample_problem* p, const void* logits, const floa
     // vocab weights of at most 2^shift each sum below 2^63
     int bits = 0;
     while ((int64_t(1) << bits) < p->vocab) ++bits;
-    a.shift = 62 - bits < 44 ? 62 - bits : 44;
+    a.shift = 62 - bits < kWeightBits ? 62 - bits : kWeightBits;
     launch_sample(a, workspace, s);
     return launched();
 }

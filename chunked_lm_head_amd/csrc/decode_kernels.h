@@ -65,6 +65,7 @@ size_t logits_workspace(int64_t n, int hidden, int out_f32);
 void launch_logits(const LogitsArgs& a, void* workspace, hipStream_t s);
 
 // -------------------------------------------------------------- sample.hip
+constexpr int kWeightBits = 44;   // finest step of the integer weights: 2^-44
 struct SampleArgs {
     const void* logits;
     int logits_f32;

@@ -225,7 +225,8 @@ size_t lmhead_sample_workspace_size(const lmhead_sample_problem* p);
  *   token     device, int32 [n].
  *   logprob   device, fp32 [n] or NULL: (x_token - max x) / tau - log sum_v
  *             w_v, over all unmasked tokens (lmhead_logprob's definition with
- *             the same temperature, for any filter).
+ *             the same temperature, for any filter). Its sum includes what
+ *             the integers round away.
  *   workspace 256-byte aligned; its error word as everywhere
  *             (lmhead_read_device_error).
  * A row whose tokens are all masked gives token -1 and logprob 0 (-1 is an

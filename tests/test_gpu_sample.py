@@ -260,3 +260,23 @@ def test_python_checks():
         lm.sample(x, u, top_k=-2)
     t, lp = lm.sample(x[:0], u[:0])
     assert t.shape == (0,) and lp.shape == (0,)
+
+
+@pytest.mark.parametrize("vocab,dtype,below", [(1 << 20, torch.float32, 28.0), (1 << 22, torch.float32, 28.5),
+                                               (1 << 22, torch.bfloat16, 27.75), (3000001, torch.float32, 28.1),
+                                               (1 << 26, torch.bfloat16, 26.0)])
+def test_logprob_of_vocabularies_beyond_the_integers(vocab, dtype, below):
+    """Millions of tokens near or below half of the integer weights' step: the
+    log-probability counts what they weigh, whatever the filters."""
+    x = torch.full((2, vocab), -below, dtype=dtype, device="cuda")
+    x[0, 12345] = 0.0
+    x[1, :5] = 0.0
+    x[1, 5::7] = float("-inf")
+    u = torch.tensor([0.3, 0.7], device="cuda")
+    v = float(x[0, 0])
+    left = vocab - 5 - len(range(5, vocab, 7))
+    want = -np.log(np.array([1 + (vocab - 1) * np.exp(v), 5 + left * np.exp(v)]))
+    for kw in (dict(), dict(top_k=3), dict(top_p=0.9), dict(min_p=0.5), dict(top_k=vocab // 2, top_p=0.5)):
+        token, lp = lm.sample(x, u, **kw)
+        assert token[0] == 12345 and token[1] < 5
+        assert (np.abs(f64(lp) - want) <= 2.0 ** -24 * 1.01 * np.abs(want) + 1e-8).all(), (kw, f64(lp) - want)

@@ -160,9 +160,9 @@ def _check_gpu(name, t, dtypes, shape, device=None):
     raise ValueError(f"{name} must have the shape {['any' if w is None else w for w in shape]}")
 
 
-def _workspace(ws: Optional[torch.Tensor], nbytes: int, device, where: str) -> torch.Tensor:
-    if nbytes == 0:
-        raise LMHeadError(LMHEAD_ERR_SHAPE, where)
+def _workspace(ws: Optional[torch.Tensor], nbytes: int, device, entry, p, pointers: int) -> torch.Tensor:
+    if nbytes == 0:   # an invalid problem: the entry, which checks that first, says why
+        raise LMHeadError(entry(p, *[None] * pointers, 0, stream=0), entry.__name__)
     if ws is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     _check_gpu("ws", ws, (torch.uint8,), (None,), device)
@@ -227,7 +227,7 @@ def rms_norm_backward(dy, r, weight, rstd, dresidual=None, weight_offset: float 
     dx = torch.empty_like(r) if need_dx else None
     dw = torch.empty_like(weight) if need_dweight else None
     if need_dweight:
-        ws = _workspace(ws, lmhead_rms_norm_bwd_workspace_size(p), r.device, "lmhead_rms_norm_bwd_workspace_size")
+        ws = _workspace(ws, lmhead_rms_norm_bwd_workspace_size(p), r.device, lmhead_rms_norm_bwd, p, 8)
     _ok(lmhead_rms_norm_bwd(p, dy, r, weight, rstd, dresidual, dx, dw, ws, ws.numel() if ws is not None else 0),
         "lmhead_rms_norm_bwd")
     return dx, dw
@@ -301,7 +301,7 @@ def logits_fp8(a, a_scale, w, w_scale, out_dtype=torch.bfloat16, out: Optional[t
         out = torch.empty(n, vocab, dtype=out_dtype, device=a.device)
     ld = _row_stride("out", out, (n, vocab), a.device)
     p = lmhead_fp8_problem(n, vocab, hidden, ld, _DTYPES[out.dtype], 0)
-    ws = _workspace(ws, lmhead_logits_fp8_workspace_size(p), a.device, "lmhead_logits_fp8_workspace_size")
+    ws = _workspace(ws, lmhead_logits_fp8_workspace_size(p), a.device, lmhead_logits_fp8, p, 6)
     _ok(lmhead_logits_fp8(p, a, a_scale, w, w_scale, out, ws, ws.numel()), "lmhead_logits_fp8")
     return out
 
@@ -355,8 +355,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, want
                               float(scalars.get("temperature", 0.0)), float(scalars.get("top_p", 0.0)),
                               float(scalars.get("min_p", 0.0)), 0, _p(rows.get("temperature")),
                               _p(rows.get("top_k")), _p(rows.get("top_p")), _p(rows.get("min_p")))
-    nbytes = lmhead_sample_workspace_size(p)
-    ws = _workspace(ws, nbytes, dev, "lmhead_sample_workspace_size")
+    ws = _workspace(ws, lmhead_sample_workspace_size(p), dev, lmhead_sample, p, 5)
     token = torch.empty(n, dtype=torch.int32, device=dev)
     logprob = torch.empty(n, dtype=torch.float32, device=dev) if want_logprob else None
     _ok(lmhead_sample(p, logits, u, token, logprob, ws, ws.numel()), "lmhead_sample")

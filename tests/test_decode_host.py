@@ -179,3 +179,14 @@ def test_reference_norm_gradients_against_differences():
         vx, vw = rng.standard_normal(x.shape), rng.standard_normal(64)
         d = (loss(x + h * vx, w + h * vw) - loss(x - h * vx, w - h * vw)) / (2 * h)
         assert abs(d - ((dx * vx).sum() + (dw * vw).sum())) < 1e-7 * max(1.0, abs(d))
+
+
+def test_a_bad_problem_is_named_by_its_entry():
+    """Where the size function says 0, the helpers raise the entry's own status."""
+    from chunked_lm_head_amd import decode
+    for entry, p, pointers, want in ((lm.lmhead_sample, samp(top_p=1.5), 5, A), (lm.lmhead_sample, samp(vocab=0), 5, S),
+                                     (lm.lmhead_sample, samp(n=0, top_k=-2), 5, A), (lm.lmhead_logits_fp8, fp8(hidden=192), 6, S),
+                                     (lm.lmhead_rms_norm_bwd, norm(eps=-1.0), 8, A), (lm.lmhead_rms_norm_bwd, norm(hidden=100), 8, S)):
+        with pytest.raises(lm.LMHeadError) as e:
+            decode._workspace(None, 0, "cpu", entry, p, pointers)
+        assert e.value.status == want and entry.__name__ in str(e.value)

@@ -182,3 +182,11 @@ def test_equal_rows_get_equal_logits(n, vocab, dtype):
     many = a.view(torch.uint8).expand(n, hidden).contiguous().view(torch.float8_e4m3fn)
     out = lm.logits_fp8(many, sa.expand(n, -1).contiguous(), w, sw, out_dtype=dtype)
     assert torch.equal(out, out[:1].expand_as(out)), (out != out[:1]).sum()
+
+
+def test_refusals_keep_the_entry_status():
+    q = torch.zeros(4, 65664, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    s = torch.ones(4, 513, device="cuda")
+    with pytest.raises(lm.LMHeadError) as e:
+        lm.logits_fp8(q, s, q, s[:1])
+    assert e.value.status == lm.LMHEAD_ERR_SHAPE

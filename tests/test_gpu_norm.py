@@ -297,3 +297,15 @@ def test_quotients_are_one_division(order):
         w = torch.from_numpy(x[i]).cuda()
         q, scale, _ = lm.rms_norm_quant(torch.ones(1, x.shape[1], dtype=torch.bfloat16, device="cuda"), w, eps=0.0)
         assert np.array_equal(scale.cpu().numpy()[0], s[i]) and np.array_equal(f64(q)[0], want[i]), i
+
+
+def test_refusals_keep_the_entry_status():
+    x, _, w, _ = inputs(3, 256, 1, False)
+    rstd = torch.ones(3, device="cuda")
+    with pytest.raises(lm.LMHeadError) as e:
+        lm.rms_norm_backward(x, x, w, rstd, weight_offset=float("inf"))
+    assert e.value.status == lm.LMHEAD_ERR_ARG
+    y = torch.zeros(3, 96, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(lm.LMHeadError) as e:
+        lm.rms_norm_backward(y, y, w[:96], rstd)
+    assert e.value.status == lm.LMHEAD_ERR_SHAPE

@@ -280,3 +280,11 @@ def test_logprob_of_vocabularies_beyond_the_integers(vocab, dtype, below):
         token, lp = lm.sample(x, u, **kw)
         assert token[0] == 12345 and token[1] < 5
         assert (np.abs(f64(lp) - want) <= 2.0 ** -24 * 1.01 * np.abs(want) + 1e-8).all(), (kw, f64(lp) - want)
+
+
+def test_refusals_keep_the_entry_status():
+    x, u, _ = logits_of(3, 100, torch.float32, 15)
+    for kw in (dict(top_p=1.5), dict(min_p=float("nan")), dict(min_p=-0.5), dict(top_k=-2), dict(temperature=float("inf"))):
+        with pytest.raises(lm.LMHeadError) as e:
+            lm.sample(x, u, **kw)
+        assert e.value.status == lm.LMHEAD_ERR_ARG, kw

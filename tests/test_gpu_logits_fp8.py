@@ -62,6 +62,7 @@ def test_against_definition(n, vocab, hidden, dtype):
 
 
 # columns enough for the tiles on both output types (few columns go through the stream in sets of 64 rows)
+# (fp32 output: from n = 130 on; the smaller n go through the stream too, see LONG for their tiles)
 TILED = [(65, 16400, 256), (70, 16500, 128), (100, 16700, 384), (128, 16385, 640), (130, 22001, 128), (200, 16500, 256),
          (257, 13300, 128), (300, 13200, 384), (513, 7300, 128), (1030, 4100, 256), (2048, 2200, 128)]
 
@@ -190,3 +191,60 @@ def test_refusals_keep_the_entry_status():
     with pytest.raises(lm.LMHeadError) as e:
         lm.logits_fp8(q, s, q, s[:1])
     assert e.value.status == lm.LMHEAD_ERR_SHAPE
+
+
+def wide_operand(rows, cols, block_rows, seed):
+    """operand(), made on the device."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    q = (torch.randn(rows, cols, generator=g, device="cuda") * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    return q, torch.exp(torch.rand(-(-rows // block_rows), cols // 128, generator=g, device="cuda") * 6 - 3)
+
+
+def check_wide(out, a, sa, w, sw):
+    """check(), on the device: long sums of many rows and columns."""
+    A = a.double() * sa.double().repeat_interleave(128, 1)
+    B = w.double() * sw.double().repeat_interleave(128, 0)[:w.shape[0]].repeat_interleave(128, 1)
+    z = A @ B.t().contiguous()
+    A.abs_(), B.abs_()
+    tol = (A @ B.t().contiguous()) * ((128 + a.shape[1] // 128) * 2.0 ** -23)
+    if out.dtype == torch.bfloat16:
+        tol += 2.0 ** -8 * 1.01 * z.abs()
+        if a.shape[0] > 64:
+            for k in range(0, a.shape[1], 8):
+                most = A[:, k, None] * B[None, :, k]
+                for j in range(k + 1, k + 8):
+                    most = torch.maximum(most, A[:, j, None] * B[None, :, j])
+                tol += 8 * 2.0 ** -13 * most
+    bad = ~((out.double() - z).abs() <= tol)   # NaN is bad too
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:5].tolist(), float((out.double() - z).abs().max()))
+
+
+# More columns than the stream over sets of rows takes (two groups of 16 a wave for fp32, one for bf16),
+# so every one of these runs tiles: of 128 rows for n <= 128 and, with an fp32 output, wherever
+# ceil(n / 128) is odd; of 256 rows for the others. 9 to 40 column blocks: the ring of four steps is
+# used over and over, an odd and an even number of times.
+LONG = [(70, 33001, 1280), (100, 32900, 1152), (128, 33000, 2048), (129, 22100, 1280), (200, 16500, 2048),
+        (256, 16400, 4096), (300, 13101, 1152), (300, 13100, 4096), (480, 8300, 5120), (1030, 4500, 2176)]
+
+
+@pytest.mark.parametrize("n,vocab,hidden", LONG)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_tiles_over_long_sums(n, vocab, hidden, dtype):
+    print(f"[logits] n={n} vocab={vocab} hidden={hidden} {dtype}", flush=True)
+    a, sa = wide_operand(n, hidden, 1, n + hidden)
+    w, sw = wide_operand(vocab, hidden, 128, vocab)
+    check_wide(lm.logits_fp8(a, sa, w, sw, out_dtype=dtype), a, sa, w, sw)
+
+
+# 2048 waves share the groups of 16 columns: 2, 3, 4, 5 at once, two trips of 3, 4 and 5 (shares that
+# differ by a group, a last trip that is not whole), and four trips of 4
+@pytest.mark.parametrize("n", [1, 16, 17, 33, 64])
+@pytest.mark.parametrize("vocab,hidden", [(40000, 640), (70001, 384), (100003, 640), (151936, 256), (170000, 512),
+                                          (200001, 384), (262144, 128), (310001, 256), (500009, 256)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_stream_of_many_columns(n, vocab, hidden, dtype):
+    print(f"[logits] n={n} vocab={vocab} hidden={hidden} {dtype}", flush=True)
+    a, sa = wide_operand(n, hidden, 1, n + hidden)
+    w, sw = wide_operand(vocab, hidden, 128, vocab)
+    check_wide(lm.logits_fp8(a, sa, w, sw, out_dtype=dtype), a, sa, w, sw)

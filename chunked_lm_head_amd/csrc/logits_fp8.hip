@@ -546,13 +546,14 @@ __global__ __launch_bounds__(kTileThreads, 1) void logits_tile_kernel(TileArgs t
 
 }  // namespace
 
-// Rows of a matrix tile. An fp32 output's tile of 128 rows x 256 columns takes
-// half the time of one of 256 x 128 per row, so 128 wherever 256 would leave the
-// last half tile empty (us at 151,936 x 4096, 128 against 256 rows a tile, before
-// the results went through LDS: n = 128: 200, 291; 256: 336, 331; 300: 455, 593;
-// 2048: 2388, 2349). A bf16 output's larger 256 x 256 tile reads less per
-// product and loses to 128 only when one tile holds all rows (n = 128: 186, 202;
-// 200: 254, 208; 300: 331, 306).
+// Rows of a matrix tile. With an fp32 output, tiles of 128 rows x 256 columns and
+// of 256 x 128 take the same time per row, so 128 wherever 256 would leave the
+// last half tile empty. A bf16 output's larger 256 x 256 tile reads less per
+// product and loses to 128 only when one tile holds all rows. us at 151,936 x
+// 4096, 128 and 256 rows a tile:
+//   rows    70        128       200       256       300       400       512       1024        1100        2048
+//   fp32    185, 289  203, 291  326, 326  343, 340  459, 579  616, 601  657, 637  1251, 1219  1407, 1467  2422, 2423
+//   bf16    160, 193  170, 197  245, 198  242, 198  318, 296  429, 305  432, 317   808, 602    927, 700   1548, 1138
 int64_t tile_rows(int64_t n, int out_f32) {
     if (out_f32) return cdiv(n, 128) % 2 ? 128 : 256;
     return n <= 128 ? 128 : 256;

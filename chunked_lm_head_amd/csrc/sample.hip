@@ -362,7 +362,10 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, int64_t r, cons
                                log(all * __builtin_amdgcn_ldexp(1.0, -W.shift)));
 }
 
-// A whole row by radix descent: what the listed border tokens cannot resolve.
+// A whole row by radix descent: what the listed border tokens cannot resolve, in
+// two to eight passes of one workgroup over the row (151,936 tokens, most of them
+// in ties of thousands: top-p 427 us for one row, 560 us for 256; with top-k 595 and
+// 765 us; the list takes 47 and 137 us).
 // rest: what its integer weights leave out.
 template <bool F32>
 __device__ __attribute__((noinline)) void whole_row(const SampleArgs& a, int64_t r, const Row<F32>& row, const Params& P, const Weights& W,

@@ -23,7 +23,9 @@
  * 8-bit values are OCP e4m3 (1 sign, 4 exponent, 3 mantissa bits, largest
  * 448, no infinity), rounded to nearest even from the fp32 quotient of value
  * and scale. A block scale is fp32: the value is q * scale. The scale of a block
- * is its largest magnitude / 448, at least 2^-126 (1 for a block of zeros).
+ * is its largest magnitude / 448, at least 2^-126 (1 for a block of zeros). A
+ * NaN stays in its element and out of the scale; an infinity makes its block's
+ * scale infinite, so that no value of the block is finite again.
  */
 #ifndef LMHEAD_DECODE_H
 #define LMHEAD_DECODE_H

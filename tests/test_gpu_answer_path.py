@@ -166,3 +166,47 @@ def test_next_token_scores_as_its_operands_say(n):
     B = (Wq.double() * Ws.double().repeat_interleave(128, 0)[:vocab].repeat_interleave(128, 1)).cpu()
     want = torch.log_softmax(A @ B.t() / float(np.float32(0.8)), 1).gather(1, token.long().cpu()[:, None])[:, 0]
     assert (lp.double().cpu() - want).abs().max() <= 1e-4
+
+
+def test_offsets_past_32_bits():
+    """Rows, logits and draws behind the first 4 GiB: the last rows of a large
+    call are those of a call on them alone."""
+    def normal(rows, cols, std=1.0):
+        x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+        for r in range(0, rows, 1 << 16):
+            x[r:r + (1 << 16)].normal_(0.0, std)
+        return x
+    print("[large] norm 1,060,000 x 4096", flush=True)
+    n, hidden = 1060000, 4096
+    x = normal(n, hidden)
+    w = 1 + normal(1, hidden, 0.1)[0]
+    f = lm.rms_norm_forward(x, w, x, out_fp8=True)
+    want = lm.rms_norm_forward(x[-5:], w, x[-5:], out_fp8=True)
+    for a, b in zip(f, want):
+        assert torch.equal(a[-5:].view(torch.uint8), b.view(torch.uint8))
+    r, rstd = f.residual_out, f.rstd
+    del f
+    dx, _ = lm.rms_norm_backward(x, r, w, rstd, need_dweight=False)
+    assert torch.equal(dx[-5:], lm.rms_norm_backward(x[-5:], r[-5:], w, rstd[-5:], need_dweight=False)[0])
+    del dx, r
+    q, s = lm.quantize_fp8(x)
+    q1, s1 = lm.quantize_fp8(x[-5:])
+    assert torch.equal(q[-5:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[-5:], s1)
+    q, s = lm.quantize_fp8(x, 128)
+    tail = (n - 1) // 128 * 128
+    q1, s1 = lm.quantize_fp8(x[tail:], 128)
+    assert torch.equal(q[tail:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[-1:], s1)
+    del x, q, s
+    for dtype in (torch.float32, torch.bfloat16):
+        print(f"[large] logits and draws 20,000 x 151,936 {dtype}", flush=True)
+        n, hidden, vocab = 20000, 128, 151936
+        rows = normal(1, hidden).expand(n, hidden).contiguous()
+        a, sa = lm.quantize_fp8(rows)
+        W, sw = lm.quantize_fp8(normal(vocab, hidden), 128)
+        z = lm.logits_fp8(a, sa, W, sw, out_dtype=dtype)
+        # the same hidden state in every row: its logits are those of the first
+        assert torch.equal(z[-700:], z[:1].expand(700, vocab)) and torch.equal(z[9999], z[0])
+        u = torch.full((n,), 0.37, device="cuda")
+        token, lp = lm.sample(z, u, top_p=0.9)
+        assert (token == token[0]).all() and (lp == lp[0]).all() and token[0] >= 0
+        del z

@@ -164,6 +164,24 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+def _on_device_of(arg: int):
+    """Run a helper with the device of its parameter number `arg` (H) current,
+    given by place or by keyword, so that the library's device check, its
+    launches and the current-stream lookup all refer to the tensors' GPU."""
+    def wrap(fn):
+        name = fn.__code__.co_varnames[arg]
+
+        @functools.wraps(fn)
+        def call(*args, **kwargs):
+            t = args[arg] if len(args) > arg else kwargs.get(name)
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch.cuda.current_device():
+                with torch.cuda.device(t.device):
+                    return fn(*args, **kwargs)
+            return fn(*args, **kwargs)
+        return call
+    return wrap
+
+
 # ----------------------------------------------------------- C entry points
 
 def lmhead_workspace_size(p: lmhead_problem, entry: int, with_backward: int) -> int:
@@ -251,6 +269,7 @@ def lmhead_status_string(status: int) -> str:
     return lib().lmhead_status_string(int(status)).decode()
 
 
+@_on_device_of(0)   # the helpers ran there
 def lmhead_read_device_error(workspace, stream=None):
     code = ctypes.c_int32(0)
     row = ctypes.c_int64(0)
@@ -322,24 +341,6 @@ def _check_row_temperature(rt, n: int):
         raise ValueError("row_temperature must be a tensor on a GPU device")
     if rt.dtype != torch.float32 or not rt.is_contiguous() or tuple(rt.shape) != (n,):
         raise ValueError("row_temperature must be a contiguous float32 tensor of shape [n]")
-
-
-def _on_device_of(arg: int):
-    """Run a helper with the device of its parameter number `arg` (H) current,
-    given by place or by keyword, so that the library's device check, its
-    launches and the current-stream lookup all refer to the tensors' GPU."""
-    def wrap(fn):
-        name = fn.__code__.co_varnames[arg]
-
-        @functools.wraps(fn)
-        def call(*args, **kwargs):
-            t = args[arg] if len(args) > arg else kwargs.get(name)
-            if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != torch.cuda.current_device():
-                with torch.cuda.device(t.device):
-                    return fn(*args, **kwargs)
-            return fn(*args, **kwargs)
-        return call
-    return wrap
 
 
 def workspace(p: lmhead_problem, entry: int, with_backward: bool, device) -> torch.Tensor:

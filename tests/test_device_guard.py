@@ -25,7 +25,8 @@ class Entered(Exception):
 CALLS = [("ce_loss_forward", "H", 0, 4), ("logprob_forward", "H", 0, 4), ("support_forward", "H", 0, 5),
          ("support_logprob_forward", "H", 0, 4), ("support_kl_forward", "H", 0, 4), ("backward", "H", 1, 7),
          ("backward_accumulate", "H", 1, 7), ("rms_norm_forward", "x", 0, 2), ("rms_norm_backward", "dy", 0, 4),
-         ("quantize_fp8", "x", 0, 1), ("logits_fp8", "a", 0, 4), ("sample", "logits", 0, 2), ("rms_norm_quant", "x", 0, 2)]
+         ("quantize_fp8", "x", 0, 1), ("logits_fp8", "a", 0, 4), ("sample", "logits", 0, 2), ("rms_norm_quant", "x", 0, 2),
+         ("lmhead_read_device_error", "workspace", 0, 1)]
 
 
 @pytest.fixture

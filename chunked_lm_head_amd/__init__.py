@@ -661,3 +661,15 @@ from .decode import (  # noqa: E402
     lmhead_rms_norm_bwd_workspace_size, lmhead_rms_norm_fwd, lmhead_sample, lmhead_sample_problem,
     lmhead_sample_workspace_size, logits_fp8, next_token, quantize_fp8, rms_norm, rms_norm_backward,
     rms_norm_forward, rms_norm_quant, sample)
+
+# ----------------------------------------- in a training step (lmhead_train.h)
+
+from .train import (  # noqa: E402
+    DEVERR_TOKEN, DTYPE_E4M3, KL_K1, KL_K2, KL_K3, PREFERENCE_HINGE, PREFERENCE_SIGMOID, PREFERENCE_SQUARED,
+    REDUCE_MEAN, REDUCE_SEQUENCE_MEAN, REDUCE_SUM, AdamWPlan, AdamWState, Embedding, PolicyLoss, PolicyOutputs,
+    PreferenceLoss, PreferenceOutputs, adamw_plan, adamw_state, adamw_step, embedding, embedding_backward,
+    embedding_forward, lmhead_adamw, lmhead_adamw_step, lmhead_adamw_tensor, lmhead_embedding, lmhead_embedding_bwd,
+    lmhead_embedding_bwd_workspace_size, lmhead_embedding_fwd, lmhead_policy_loss_bwd, lmhead_policy_loss_fwd,
+    lmhead_policy_loss_workspace_size, lmhead_policy_problem, lmhead_preference_loss_bwd, lmhead_preference_loss_fwd,
+    lmhead_preference_loss_workspace_size, lmhead_preference_problem, policy_loss, policy_loss_backward,
+    policy_loss_forward, preference_loss, preference_loss_backward, preference_loss_forward)

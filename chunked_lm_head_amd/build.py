@@ -12,8 +12,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblmhead.so")
 SOURCES = ["lmhead_kernels.hip", "lmhead_candidates.hip", "lmhead_api.hip", "rms_norm.hip",
-           "logits_fp8.hip", "sample.hip", "decode_api.hip"]
-HEADERS = ["gemm_core.h", "lmhead_kernels.h", "decode_kernels.h", "host_util.h"]
+           "logits_fp8.hip", "sample.hip", "decode_api.hip", "embedding.hip", "token_losses.hip", "adamw.hip",
+           "train_api.hip"]
+HEADERS = ["gemm_core.h", "lmhead_kernels.h", "decode_kernels.h", "train_kernels.h", "vec8.h", "host_util.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,0 +1,251 @@
+// adamw.hip — one AdamW step over many tensors, states in fp32 or in 8 bits.
+//
+// Mathematics (lmhead_train.h): m' = b1 m + (1 - b1) g, v' = b2 v + (1 - b2) g^2,
+// p' = p (1 - lr wd) - lr / (1 - b1^t) m' / (sqrt(v') / sqrt(1 - b2^t) + eps), all
+// in fp32. 8-bit states are e4m3 over blocks of 128: of m, and of sqrt(v), whose
+// range is the square root of v's (e4m3 spans 2^17.8 of a block's largest value).
+// They round to nearest, or at random (unbiased) where a seed is given: nearest
+// rounding swallows changes below half a code's step, which with beta2 = 0.99
+// left sqrt(v) 1.15 times too large in the median after 300 steps.
+//
+// Bound by memory: 10 to 28 bytes per element and about 40 operations. Each
+// element is read and written once; eight consecutive ones per lane, so that 16
+// lanes hold a block of 128 and its maximum is four shuffles. Tensors share a
+// launch: the table of up to 48 travels as a kernel argument (no copy to the
+// device, nothing to keep), a workgroup finds its tensor by its chunk's number.
+#include "host_util.h"
+#include "train_kernels.h"
+#include "vec8.h"
+
+namespace lmhead {
+
+namespace {
+
+constexpr int kTrips = kAdamWChunk / 2048;
+
+// lane's eight values at element e; zeros past the end
+template <bool F32>
+__device__ __forceinline__ V8 fetch(const void* p, int64_t e, int64_t numel, bool wide) {
+    if (wide && e + 8 <= numel) return load8<F32>(p, e >> 3);
+    V8 f = zeros8();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (e + c < numel)
+            f.v[c] = F32 ? reinterpret_cast<const float*>(p)[e + c]
+                         : __builtin_bit_cast(float, (uint32_t)reinterpret_cast<const bf16_bits*>(p)[e + c] << 16);
+    return f;
+}
+template <bool F32>
+__device__ __forceinline__ void put(void* p, int64_t e, int64_t numel, bool wide, const V8& f) {
+    if (wide && e + 8 <= numel) {
+        store8<F32>(p, e >> 3, f);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (e + c < numel) {
+            if (F32) reinterpret_cast<float*>(p)[e + c] = f.v[c];
+            else reinterpret_cast<__bf16*>(p)[e + c] = (__bf16)f.v[c];
+        }
+}
+__device__ __forceinline__ uint2 fetch_codes(const void* p, int64_t e, int64_t numel, bool wide) {
+    if (wide && e + 8 <= numel) return reinterpret_cast<const uint2*>(p)[e >> 3];
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (e + c < numel) w[c >> 2] |= (uint32_t)reinterpret_cast<const uint8_t*>(p)[e + c] << (8 * (c & 3));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void put_codes(void* p, int64_t e, int64_t numel, bool wide, const uint2& q) {
+    if (wide && e + 8 <= numel) {
+        reinterpret_cast<uint2*>(p)[e >> 3] = q;
+        return;
+    }
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        if (e + c < numel) reinterpret_cast<uint8_t*>(p)[e + c] = (uint8_t)(w[c >> 2] >> (8 * (c & 3)));
+}
+
+// over the 16 lanes that hold a block of 128 (NaN left out)
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
+    return v;
+}
+
+// Two rounds of multiplying and folding by odd constants (the golden ratio's and
+// e's fractions): every bit of x moves about half of the result's.
+__device__ __forceinline__ uint32_t scramble(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x9e3779b9u;
+    x ^= x >> 15;
+    x *= 0xb7e15163u;
+    return x ^ x >> 16;
+}
+
+// |y| plus a random part of its code's step (20 bits of the fp32 value), cut to
+// the code below. Below 2^-6 the codes' step is that of 2^-6 .. 2^-5, so the
+// value is moved there and back.
+__device__ __forceinline__ float cut_at_random(float y, uint32_t random20) {
+    const float mag = fabsf(y), base = mag < 0x1p-6f ? 0x1p-6f : 0.0f;
+    const uint32_t bits = (__builtin_bit_cast(uint32_t, mag + base) + random20) & 0xfff00000u;
+    return __builtin_copysignf(__builtin_bit_cast(float, bits) - base, y);
+}
+
+// e4m3 of eight quotients by the block's scale. ROOT: a value above zero gets at
+// least the least code. RANDOM: noise of the eight, in bits 4 .. 19.
+template <bool ROOT, bool RANDOM>
+__device__ __forceinline__ uint2 codes(const V8& f, float scale, const uint32_t* noise) {
+    V8 y;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        y.v[c] = f.v[c] / scale;
+        if (ROOT && f.v[c] > 0.0f) y.v[c] = y.v[c] < 0x1p-9f ? 0x1p-9f : y.v[c];
+        if (RANDOM) y.v[c] = cut_at_random(y.v[c], ROOT ? noise[c] >> 16 << 4 : (noise[c] & 0xffffu) << 4);
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(y.v[4 * i], y.v[4 * i + 1], 0, false);
+        v = __builtin_amdgcn_cvt_pk_fp8_f32(y.v[4 * i + 2], y.v[4 * i + 3], v, true);
+        w[i] = (uint32_t)v;
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+struct Step {
+    float beta1, rest1, beta2, rest2, eps, keep, step_size, root_scale, grad_scale;
+    uint32_t mix;   // of the random rounding
+};
+
+template <bool P32, bool G32, bool S8, bool RANDOM>
+__device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int64_t chunk) {
+    const bool wide = (t.kind & kAdamWWide) != 0;
+    const int64_t e0 = chunk * kAdamWChunk + threadIdx.x * 8;
+    V8 p[kTrips], g[kTrips], m[kTrips], v[kTrips];
+    uint2 mq[S8 ? kTrips : 1], vq[S8 ? kTrips : 1];
+    float ms[S8 ? kTrips : 1], vs[S8 ? kTrips : 1];
+    // every load before the first store
+#pragma unroll
+    for (int j = 0; j < kTrips; ++j) {
+        const int64_t e = e0 + j * 2048;
+        p[j] = fetch<P32>(t.param, e, t.numel, wide);
+        g[j] = fetch<G32>(t.grad, e, t.numel, wide);
+        if (S8) {
+            mq[S8 ? j : 0] = fetch_codes(t.m, e, t.numel, wide);
+            vq[S8 ? j : 0] = fetch_codes(t.v, e, t.numel, wide);
+            ms[S8 ? j : 0] = e < t.numel ? t.m_scale[e >> 7] : 0.0f;
+            vs[S8 ? j : 0] = e < t.numel ? t.v_scale[e >> 7] : 0.0f;
+        } else {
+            m[j] = fetch<true>(t.m, e, t.numel, wide);
+            v[j] = fetch<true>(t.v, e, t.numel, wide);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kTrips; ++j) {
+        const int64_t e = e0 + j * 2048;
+        if (S8) {
+            m[j] = e4m3_to8(mq[S8 ? j : 0]);
+            v[j] = e4m3_to8(vq[S8 ? j : 0]);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                m[j].v[c] *= ms[S8 ? j : 0];
+                v[j].v[c] *= vs[S8 ? j : 0];
+                v[j].v[c] *= v[j].v[c];
+            }
+        }
+        V8 root;
+        float m_max = 0.0f, v_max = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float gc = g[j].v[c] * k.grad_scale;
+            const float mc = __builtin_fmaf(k.rest1, gc, k.beta1 * m[j].v[c]);
+            const float vc = __builtin_fmaf(k.rest2 * gc, gc, k.beta2 * v[j].v[c]);
+            const float rc = sqrtf(vc);
+            p[j].v[c] = __builtin_fmaf(-k.step_size, mc / __builtin_fmaf(rc, k.root_scale, k.eps), p[j].v[c] * k.keep);
+            m[j].v[c] = mc;
+            v[j].v[c] = vc;
+            root.v[c] = rc;
+            if (S8) {
+                m_max = fmaxf(m_max, fabsf(mc));
+                v_max = fmaxf(v_max, rc);
+            }
+        }
+        put<P32>(t.param, e, t.numel, wide, p[j]);
+        if (t.copy != nullptr) put<false>(t.copy, e, t.numel, wide, p[j]);
+        if (S8) {
+            uint32_t noise[RANDOM ? 8 : 1];
+            if (RANDOM)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    noise[RANDOM ? c : 0] = scramble((uint32_t)(e + c) ^ k.mix ^ (uint32_t)(e >> 32) * 0x9e3779b9u);
+            const float sm = block_scale(max16(m_max)), sv = block_scale(max16(v_max));
+            put_codes(t.m, e, t.numel, wide, codes<false, RANDOM>(m[j], sm, noise));
+            put_codes(t.v, e, t.numel, wide, codes<true, RANDOM>(root, sv, noise));
+            if ((threadIdx.x & 15) == 0 && e < t.numel) {
+                t.m_scale[e >> 7] = sm;
+                t.v_scale[e >> 7] = sv;
+            }
+        } else {
+            put<true>(t.m, e, t.numel, wide, m[j]);
+            put<true>(t.v, e, t.numel, wide, v[j]);
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
+    __shared__ float now[3];
+    const AdamWScalars& k = a.k;
+    Step s = {k.beta1, k.rest1, k.beta2, k.rest2, k.eps, k.keep, k.step_size, k.root_scale, 1.0f, 0u};
+    if (k.grad_scale != nullptr) s.grad_scale = k.grad_scale[0];
+    if (k.step != nullptr || k.device_lr != nullptr) {
+        if (threadIdx.x == 0) {
+            int64_t t = k.step != nullptr ? (int64_t)k.step[0] : k.host_step;
+            if (t < 1) t = 1;
+            const double lr = k.device_lr != nullptr ? (double)k.device_lr[0] : k.host_lr;
+            now[0] = (float)(1.0 - lr * k.weight_decay);
+            now[1] = (float)(lr / -expm1((double)t * k.log_beta1));
+            now[2] = (float)(1.0 / sqrt(-expm1((double)t * k.log_beta2)));
+        }
+        __syncthreads();
+        s.keep = now[0];
+        s.step_size = now[1];
+        s.root_scale = now[2];
+    }
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.tensor[mid].first <= blockIdx.x) lo = mid;
+        else hi = mid - 1;
+    }
+    const AdamWTensor t = a.tensor[lo];
+    const int64_t chunk = blockIdx.x - t.first;
+    if (k.stochastic) {
+        const int64_t step = k.step != nullptr ? (k.step[0] < 1 ? 1 : k.step[0]) : k.host_step;
+        s.mix = scramble(k.seed + scramble((uint32_t)step + scramble(t.kind >> kAdamWPlace)));
+        switch (t.kind & 7) {
+            case 4: return update<false, false, true, true>(t, s, chunk);
+            case 5: return update<true, false, true, true>(t, s, chunk);
+            case 6: return update<false, true, true, true>(t, s, chunk);
+            case 7: return update<true, true, true, true>(t, s, chunk);
+            default: break;   // fp32 states
+        }
+    }
+    switch (t.kind & 7) {
+        case 0: update<false, false, false, false>(t, s, chunk); break;
+        case 1: update<true, false, false, false>(t, s, chunk); break;
+        case 2: update<false, true, false, false>(t, s, chunk); break;
+        case 3: update<true, true, false, false>(t, s, chunk); break;
+        case 4: update<false, false, true, false>(t, s, chunk); break;
+        case 5: update<true, false, true, false>(t, s, chunk); break;
+        case 6: update<false, true, true, false>(t, s, chunk); break;
+        default: update<true, true, true, false>(t, s, chunk); break;
+    }
+}
+
+}  // namespace
+
+void launch_adamw(const AdamWArgs& a, hipStream_t s) { adamw_kernel<<<a.chunks, 256, 0, s>>>(a); }
+
+}  // namespace lmhead

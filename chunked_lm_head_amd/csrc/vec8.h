@@ -1,0 +1,66 @@
+// vec8.h — eight consecutive values of a row in registers: bf16 (16 bytes),
+// fp32 (two of 16) or e4m3 (8 bytes) in memory, fp32 in between.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_core.h"
+
+namespace lmhead {
+
+struct V8 {
+    float v[8];
+};
+
+__device__ __forceinline__ V8 zeros8() { return V8{{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}}; }
+
+__device__ __forceinline__ V8 bf16_to8(const uint4& p) {
+    V8 f;
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f.v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+        f.v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
+    }
+    return f;
+}
+__device__ __forceinline__ uint4 to_bf16x8(const V8& f) {
+    return make_uint4(pack_bf16x2(f.v[0], f.v[1]), pack_bf16x2(f.v[2], f.v[3]), pack_bf16x2(f.v[4], f.v[5]),
+                      pack_bf16x2(f.v[6], f.v[7]));
+}
+__device__ __forceinline__ V8 e4m3_to8(const uint2& p) {
+    V8 f;
+    const uint32_t w[2] = {p.x, p.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+        const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+        f.v[4 * i] = lo[0];
+        f.v[4 * i + 1] = lo[1];
+        f.v[4 * i + 2] = hi[0];
+        f.v[4 * i + 3] = hi[1];
+    }
+    return f;
+}
+
+// vector i of a row: elements 8 i .. 8 i + 7
+template <bool F32>
+__device__ __forceinline__ V8 load8(const void* p, int64_t i) {
+    if (F32) {
+        const float4 a = reinterpret_cast<const float4*>(p)[2 * i], b = reinterpret_cast<const float4*>(p)[2 * i + 1];
+        return V8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    }
+    return bf16_to8(reinterpret_cast<const uint4*>(p)[i]);
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t i, const V8& f) {
+    if (F32) {
+        reinterpret_cast<float4*>(p)[2 * i] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+        reinterpret_cast<float4*>(p)[2 * i + 1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+    } else {
+        reinterpret_cast<uint4*>(p)[i] = to_bf16x8(f);
+    }
+}
+
+}  // namespace lmhead

@@ -1,0 +1,566 @@
+"""Binding of include/lmhead_train.h: token embedding and its gradient, the
+clipped policy loss and the preference loss on log-probabilities, and the AdamW
+step over many tensors.
+
+The same two layers as the rest of the binding: the C entry points under their
+own names (tensor, address or None; the status is returned), and torch helpers
+that check their arguments, allocate outputs and workspace and raise
+``LMHeadError``. Importable from the package itself.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional, Sequence
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import LMHEAD_ERR_SHAPE, LMHeadError, _check_f32, _ok, _on_device_of, _p, _stream, lib
+from .decode import _DTYPES, FP8_BLOCK, _check_gpu, _workspace
+
+DTYPE_E4M3 = 2
+DEVERR_TOKEN = 32
+
+KL_K1, KL_K2, KL_K3 = 1, 2, 3
+REDUCE_MEAN, REDUCE_SUM, REDUCE_SEQUENCE_MEAN = 0, 1, 2
+PREFERENCE_SIGMOID, PREFERENCE_HINGE, PREFERENCE_SQUARED = 0, 1, 2
+
+_KL = {"k1": KL_K1, "k2": KL_K2, "k3": KL_K3}
+_REDUCE = {"mean": REDUCE_MEAN, "sum": REDUCE_SUM, "sequence_mean": REDUCE_SEQUENCE_MEAN}
+_PREFERENCE = {"sigmoid": PREFERENCE_SIGMOID, "hinge": PREFERENCE_HINGE, "squared": PREFERENCE_SQUARED}
+_WEIGHT_DTYPES = {**_DTYPES, torch.float8_e4m3fn: DTYPE_E4M3}
+_I32 = (torch.int32,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+class lmhead_embedding(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("vocab", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("weight_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+    ]
+
+
+class lmhead_policy_problem(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("sequences", ctypes.c_int64),
+        ("num_valid", ctypes.c_int64),
+        ("clip_low", ctypes.c_double),
+        ("clip_high", ctypes.c_double),
+        ("dual_clip", ctypes.c_double),
+        ("kl_weight", ctypes.c_double),
+        ("kl_kind", ctypes.c_int32),
+        ("reduction", ctypes.c_int32),
+        ("advantage_per_sequence", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class lmhead_preference_problem(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("pairs", ctypes.c_int64),
+        ("num_pairs", ctypes.c_int64),
+        ("beta", ctypes.c_double),
+        ("margin", ctypes.c_double),
+        ("label_smoothing", ctypes.c_double),
+        ("kind", ctypes.c_int32),
+        ("average", ctypes.c_int32),
+    ]
+
+
+class lmhead_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p),
+        ("exp_avg_sq", ctypes.c_void_p),
+        ("exp_avg_scale", ctypes.c_void_p),
+        ("exp_avg_sq_scale", ctypes.c_void_p),
+        ("copy", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("state_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class lmhead_adamw(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("step", ctypes.c_int64),
+        ("device_step", ctypes.c_void_p),
+        ("device_lr", ctypes.c_void_p),
+        ("grad_scale", ctypes.c_void_p),
+        ("stochastic", ctypes.c_int32),
+        ("seed", ctypes.c_uint32),
+    ]
+
+
+_ready = False
+
+
+def _lib() -> ctypes.CDLL:
+    """The library with the argument types of this header's entries set."""
+    global _ready
+    L = lib()
+    if not _ready:
+        vp, sz, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64
+        E, P, F, A, T = (ctypes.POINTER(t) for t in (lmhead_embedding, lmhead_policy_problem, lmhead_preference_problem,
+                                                     lmhead_adamw, lmhead_adamw_tensor))
+        L.lmhead_embedding_fwd.argtypes = [E] + [vp] * 5 + [sz, vp]
+        L.lmhead_embedding_bwd_workspace_size.argtypes = [E]
+        L.lmhead_embedding_bwd.argtypes = [E] + [vp] * 4 + [sz, vp]
+        L.lmhead_policy_loss_workspace_size.argtypes = [P]
+        L.lmhead_policy_loss_fwd.argtypes = [P] + [vp] * 10 + [sz, vp]
+        L.lmhead_policy_loss_bwd.argtypes = [P] + [vp] * 10
+        L.lmhead_preference_loss_workspace_size.argtypes = [F]
+        L.lmhead_preference_loss_fwd.argtypes = [F] + [vp] * 8 + [sz, vp]
+        L.lmhead_preference_loss_bwd.argtypes = [F] + [vp] * 6
+        L.lmhead_adamw_step.argtypes = [A, T, i64, vp]
+        for f in (L.lmhead_embedding_bwd_workspace_size, L.lmhead_policy_loss_workspace_size,
+                  L.lmhead_preference_loss_workspace_size):
+            f.restype = sz
+        for f in (L.lmhead_embedding_fwd, L.lmhead_embedding_bwd, L.lmhead_policy_loss_fwd, L.lmhead_policy_loss_bwd,
+                  L.lmhead_preference_loss_fwd, L.lmhead_preference_loss_bwd, L.lmhead_adamw_step):
+            f.restype = ctypes.c_int
+        _ready = True
+    return L
+
+
+# ----------------------------------------------------------- C entry points
+
+def lmhead_embedding_fwd(p, ids, weight, weight_scale, out, workspace, workspace_bytes, stream=None) -> int:
+    return _lib().lmhead_embedding_fwd(ctypes.byref(p), _p(ids), _p(weight), _p(weight_scale), _p(out), _p(workspace),
+                                       workspace_bytes, _stream(stream))
+
+
+def lmhead_embedding_bwd_workspace_size(p) -> int:
+    return int(_lib().lmhead_embedding_bwd_workspace_size(ctypes.byref(p)))
+
+
+def lmhead_embedding_bwd(p, ids, dout, dweight, workspace, workspace_bytes, stream=None) -> int:
+    return _lib().lmhead_embedding_bwd(ctypes.byref(p), _p(ids), _p(dout), _p(dweight), _p(workspace), workspace_bytes,
+                                       _stream(stream))
+
+
+def lmhead_policy_loss_workspace_size(p) -> int:
+    return int(_lib().lmhead_policy_loss_workspace_size(ctypes.byref(p)))
+
+
+def lmhead_policy_loss_fwd(p, logp, old_logp, ref_logp, advantage, targets, cu_seqlens, loss, stats, weights,
+                           workspace, workspace_bytes, stream=None) -> int:
+    return _lib().lmhead_policy_loss_fwd(ctypes.byref(p), _p(logp), _p(old_logp), _p(ref_logp), _p(advantage),
+                                         _p(targets), _p(cu_seqlens), _p(loss), _p(stats), _p(weights), _p(workspace),
+                                         workspace_bytes, _stream(stream))
+
+
+def lmhead_policy_loss_bwd(p, grad, weights, logp, old_logp, ref_logp, advantage, targets, cu_seqlens, dlogp,
+                           stream=None) -> int:
+    return _lib().lmhead_policy_loss_bwd(ctypes.byref(p), _p(grad), _p(weights), _p(logp), _p(old_logp), _p(ref_logp),
+                                         _p(advantage), _p(targets), _p(cu_seqlens), _p(dlogp), _stream(stream))
+
+
+def lmhead_preference_loss_workspace_size(p) -> int:
+    return int(_lib().lmhead_preference_loss_workspace_size(ctypes.byref(p)))
+
+
+def lmhead_preference_loss_fwd(p, logp, ref_logp, targets, cu_seqlens, loss, rewards, coef, workspace,
+                               workspace_bytes, stream=None) -> int:
+    return _lib().lmhead_preference_loss_fwd(ctypes.byref(p), _p(logp), _p(ref_logp), _p(targets), _p(cu_seqlens),
+                                             _p(loss), _p(rewards), _p(coef), _p(workspace), workspace_bytes,
+                                             _stream(stream))
+
+
+def lmhead_preference_loss_bwd(p, grad, coef, targets, cu_seqlens, dlogp, stream=None) -> int:
+    return _lib().lmhead_preference_loss_bwd(ctypes.byref(p), _p(grad), _p(coef), _p(targets), _p(cu_seqlens),
+                                             _p(dlogp), _stream(stream))
+
+
+def lmhead_adamw_step(p, tensors, count, stream=None) -> int:
+    """tensors: a ctypes array of lmhead_adamw_tensor (host), or None."""
+    return _lib().lmhead_adamw_step(ctypes.byref(p), tensors, count, _stream(stream))
+
+
+# --------------------------------------------------------------- embedding
+
+@_on_device_of(0)
+def embedding_forward(ids, weight, scale: float = 1.0, weight_scale=None, out_dtype=None,
+                      ws: Optional[torch.Tensor] = None):
+    """scale * weight[ids] [n, hidden]; see lmhead_embedding_fwd. ids int32 [n],
+    negative: a zero row. weight bf16 or fp32 [vocab, hidden], or e4m3 with
+    weight_scale (quantize_fp8 with block_rows 128). out_dtype: the weight's
+    (bf16 for e4m3) unless given. ws: 256 bytes, to read the error word."""
+    _check_gpu("ids", ids, _I32, (None,))
+    _check_gpu("weight", weight, tuple(_WEIGHT_DTYPES), (None, None), ids.device)
+    n = ids.shape[0]
+    vocab, hidden = weight.shape
+    if (weight_scale is not None) != (weight.dtype == torch.float8_e4m3fn):
+        raise ValueError("weight_scale goes with an e4m3 weight")
+    if weight_scale is not None:
+        if hidden % FP8_BLOCK != 0:
+            raise LMHeadError(LMHEAD_ERR_SHAPE, "lmhead_embedding_fwd")
+        _check_gpu("weight_scale", weight_scale, (torch.float32,), (-(-vocab // FP8_BLOCK), hidden // FP8_BLOCK),
+                   ids.device)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if weight_scale is not None else weight.dtype
+    if out_dtype not in _DTYPES:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    if ws is not None:
+        _check_gpu("ws", ws, (torch.uint8,), (None,), ids.device)
+    p = lmhead_embedding(n, vocab, hidden, float(scale), _WEIGHT_DTYPES[weight.dtype], _DTYPES[out_dtype], 0)
+    out = torch.empty(n, hidden, dtype=out_dtype, device=ids.device)
+    _ok(lmhead_embedding_fwd(p, ids, weight, weight_scale, out, ws, ws.numel() if ws is not None else 0),
+        "lmhead_embedding_fwd")
+    return out
+
+
+@_on_device_of(0)
+def embedding_backward(dout, ids, vocab: int, scale: float = 1.0, out_dtype=torch.bfloat16,
+                       acc: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """The gradient of embedding_forward's weight: dweight [vocab, hidden] of
+    out_dtype, zeros where no token has the id; or, with acc (bf16 or fp32
+    [vocab, hidden], for instance backward_accumulate's dW_acc), acc with the
+    gradient added, other rows untouched. See lmhead_embedding_bwd."""
+    _check_gpu("dout", dout, _BF16_F32, (None, None))
+    n, hidden = dout.shape
+    _check_gpu("ids", ids, _I32, (n,), dout.device)
+    if acc is not None:
+        _check_gpu("acc", acc, _BF16_F32, (vocab, hidden), dout.device)
+        out_dtype = acc.dtype
+    elif out_dtype not in _DTYPES:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    p = lmhead_embedding(n, vocab, hidden, float(scale), _DTYPES[out_dtype], _DTYPES[dout.dtype], int(acc is not None))
+    ws = _workspace(ws, lmhead_embedding_bwd_workspace_size(p), dout.device, lmhead_embedding_bwd, p, 4)
+    dweight = torch.empty(vocab, hidden, dtype=out_dtype, device=dout.device) if acc is None else acc
+    _ok(lmhead_embedding_bwd(p, ids, dout, dweight, ws, ws.numel()), "lmhead_embedding_bwd")
+    return dweight
+
+
+class Embedding(torch.autograd.Function):
+    """Rows of a bf16 or fp32 weight by token, scaled."""
+
+    @staticmethod
+    def forward(ctx, ids, weight, scale, out_dtype):
+        ctx.save_for_backward(ids)
+        ctx.cfg = (weight.shape[0], scale, weight.dtype)
+        return embedding_forward(ids, weight, scale, out_dtype=out_dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        vocab, scale, dtype = ctx.cfg
+        return None, embedding_backward(dout.contiguous(), ctx.saved_tensors[0], vocab, scale, dtype), None, None
+
+
+def embedding(ids, weight, scale: float = 1.0, weight_scale=None, out_dtype=None):
+    """embedding_forward with the gradient of a bf16 or fp32 weight (whole, as
+    autograd adds it up; embedding_backward adds to an accumulator in place). An
+    e4m3 weight has none. Differentiable once."""
+    if weight_scale is not None or not isinstance(weight, torch.Tensor) or weight.dtype not in _DTYPES:
+        return embedding_forward(ids, weight, scale, weight_scale, out_dtype)
+    return Embedding.apply(ids, weight, scale, out_dtype)
+
+
+# ------------------------------------------------- losses on log-probabilities
+
+class PolicyOutputs(NamedTuple):
+    loss: torch.Tensor      # fp32 []
+    stats: torch.Tensor     # fp32 [4]: means over counted tokens of KL, clipped, r, exp(-d) - 1 + d
+    weights: torch.Tensor   # fp32 [max(sequences, 1)], for the backward
+
+
+def _check_tokens(logp, targets, cu_seqlens, n=None):
+    _check_gpu("logp", logp, (torch.float32,), (n,))
+    if targets is not None:
+        _check_gpu("targets", targets, _I32, (logp.shape[0],), logp.device)
+    if cu_seqlens is not None:
+        _check_gpu("cu_seqlens", cu_seqlens, _I32, (None,), logp.device)
+        if cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must be int32 [sequences + 1], at least one sequence")
+
+
+def _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
+                    kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence):
+    _check_tokens(logp, targets, cu_seqlens)
+    n = logp.shape[0]
+    sequences = cu_seqlens.shape[0] - 1 if cu_seqlens is not None else 0
+    _check_gpu("advantage", advantage, (torch.float32,), (None,), logp.device)
+    per_sequence = advantage_per_sequence
+    if per_sequence is None:
+        if sequences == n and n > 1:
+            raise ValueError("as many sequences as tokens: say by advantage_per_sequence whose advantages they are")
+        per_sequence = advantage.shape[0] != n
+    if (per_sequence and sequences == 0) or advantage.shape[0] != (sequences if per_sequence else n):
+        raise ValueError("advantage must be float32 [n], or [sequences] with cu_seqlens")
+    for name, t in (("old_logp", old_logp), ("ref_logp", ref_logp)):
+        _check_f32(name, t, (n,), logp.device)
+    if kl_kind not in _KL:
+        raise ValueError("kl_kind must be 'k1', 'k2' or 'k3'")
+    if reduction not in _REDUCE:
+        raise ValueError("reduction must be 'mean', 'sum' or 'sequence_mean'")
+    return lmhead_policy_problem(n, sequences, num_valid, clip_low, clip_high, dual_clip, kl_weight, _KL[kl_kind],
+                                 _REDUCE[reduction], int(per_sequence), 0)
+
+
+@_on_device_of(0)
+def policy_loss_forward(logp, advantage, old_logp=None, ref_logp=None, targets=None, cu_seqlens=None,
+                        clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0,
+                        kl_weight: float = 0.0, kl_kind: str = "k3", reduction: str = "mean", num_valid: int = -1,
+                        advantage_per_sequence: Optional[bool] = None, ws: Optional[torch.Tensor] = None) -> PolicyOutputs:
+    """Clipped policy loss of packed tokens; see lmhead_policy_loss_fwd. logp fp32
+    [n] (logprob's); advantage fp32 [n], or [sequences] with cu_seqlens (int32
+    [sequences + 1]), told apart by its length unless advantage_per_sequence says
+    which; targets int32 [n], negative: the token does not count."""
+    p = _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
+                        kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence)
+    ws = _workspace(ws, lmhead_policy_loss_workspace_size(p), logp.device, lmhead_policy_loss_fwd, p, 10)
+    out = torch.empty(5 + max(p.sequences, 1), dtype=torch.float32, device=logp.device)
+    loss, stats, weights = out[0], out[1:5], out[5:]
+    _ok(lmhead_policy_loss_fwd(p, logp, old_logp, ref_logp, advantage, targets, cu_seqlens, loss, stats, weights, ws,
+                               ws.numel()), "lmhead_policy_loss_fwd")
+    return PolicyOutputs(loss, stats, weights)
+
+
+@_on_device_of(0)
+def policy_loss_backward(grad, weights, logp, advantage, old_logp=None, ref_logp=None, targets=None, cu_seqlens=None,
+                         clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0,
+                         kl_weight: float = 0.0, kl_kind: str = "k3", reduction: str = "mean", num_valid: int = -1,
+                         advantage_per_sequence: Optional[bool] = None):
+    """dlogp fp32 [n]. grad: fp32 [1] or []; weights: the forward's; the rest as
+    given to the forward."""
+    p = _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
+                        kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence)
+    _check_scalar("grad", grad, torch.float32, logp.device)
+    _check_f32("weights", weights, (max(p.sequences, 1),), logp.device, required=True)
+    dlogp = torch.empty_like(logp)
+    _ok(lmhead_policy_loss_bwd(p, grad, weights, logp, old_logp, ref_logp, advantage, targets, cu_seqlens, dlogp),
+        "lmhead_policy_loss_bwd")
+    return dlogp
+
+
+def _check_scalar(name, t, dtype, device=None):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a tensor on a GPU device, that of the inputs")
+    if t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"{name} must hold one {str(dtype).replace('torch.', '')}")
+
+
+class PolicyLoss(torch.autograd.Function):
+    """(loss, stats) of policy_loss_forward."""
+
+    @staticmethod
+    def forward(ctx, logp, advantage, old_logp, ref_logp, targets, cu_seqlens, how):
+        f = policy_loss_forward(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, *how)
+        ctx.save_for_backward(f.weights, logp, advantage, old_logp, ref_logp, targets, cu_seqlens)
+        ctx.how = how
+        ctx.mark_non_differentiable(f.stats)
+        ctx.set_materialize_grads(False)
+        return f.loss, f.stats
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g, _):
+        if g is None:
+            return (None,) * 7
+        return (policy_loss_backward(g.to(torch.float32), *ctx.saved_tensors, *ctx.how),) + (None,) * 6
+
+
+def policy_loss(logp, advantage, old_logp=None, ref_logp=None, targets=None, cu_seqlens=None, clip_low: float = 0.2,
+                clip_high: float = 0.2, dual_clip: float = 0.0, kl_weight: float = 0.0, kl_kind: str = "k3",
+                reduction: str = "mean", num_valid: int = -1, advantage_per_sequence: Optional[bool] = None):
+    """(loss, stats) with the gradient of logp alone (old_logp, ref_logp and the
+    advantages are constants); see policy_loss_forward. Differentiable once."""
+    return PolicyLoss.apply(logp, advantage, old_logp, ref_logp, targets, cu_seqlens,
+                            (clip_low, clip_high, dual_clip, kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence))
+
+
+class PreferenceOutputs(NamedTuple):
+    loss: torch.Tensor      # fp32 []
+    rewards: torch.Tensor   # fp32 [2 pairs]: beta s of the chosen answers, then of the rejected ones
+    coef: torch.Tensor      # fp32 [2 pairs], for the backward
+
+
+@_on_device_of(0)
+def preference_loss_forward(logp, cu_seqlens, ref_logp=None, targets=None, kind: str = "sigmoid", beta: float = 0.1,
+                            margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False,
+                            num_pairs: int = -1, ws: Optional[torch.Tensor] = None) -> PreferenceOutputs:
+    """Loss of pairs of packed answers, the chosen ones first; see
+    lmhead_preference_loss_fwd. cu_seqlens int32 [2 pairs + 1]."""
+    _check_tokens(logp, targets, cu_seqlens)
+    n = logp.shape[0]
+    _check_f32("ref_logp", ref_logp, (n,), logp.device)
+    pairs = _pairs(cu_seqlens)
+    if kind not in _PREFERENCE:
+        raise ValueError("kind must be 'sigmoid', 'hinge' or 'squared'")
+    p = lmhead_preference_problem(n, pairs, num_pairs, beta, margin, label_smoothing, _PREFERENCE[kind], int(bool(average)))
+    ws = _workspace(ws, lmhead_preference_loss_workspace_size(p), logp.device, lmhead_preference_loss_fwd, p, 8)
+    out = torch.empty(1 + 4 * pairs, dtype=torch.float32, device=logp.device)
+    loss, rewards, coef = out[0], out[1:1 + 2 * pairs], out[1 + 2 * pairs:]
+    _ok(lmhead_preference_loss_fwd(p, logp, ref_logp, targets, cu_seqlens, loss, rewards, coef, ws, ws.numel()),
+        "lmhead_preference_loss_fwd")
+    return PreferenceOutputs(loss, rewards, coef)
+
+
+def _pairs(cu_seqlens) -> int:
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 3 or \
+            cu_seqlens.shape[0] % 2 != 1:
+        raise ValueError("cu_seqlens must be int32 [2 pairs + 1], at least one pair")
+    return (cu_seqlens.shape[0] - 1) // 2
+
+
+@_on_device_of(0)
+def preference_loss_backward(grad, coef, n: int, cu_seqlens, targets=None):
+    """dlogp fp32 [n]. grad: fp32 [1] or []; coef: the forward's."""
+    _check_scalar("grad", grad, torch.float32)
+    pairs = _pairs(cu_seqlens)
+    _check_gpu("cu_seqlens", cu_seqlens, _I32, (None,), grad.device)
+    _check_f32("coef", coef, (2 * pairs,), grad.device, required=True)
+    if targets is not None:
+        _check_gpu("targets", targets, _I32, (n,), grad.device)
+    p = lmhead_preference_problem(n, pairs, -1, 1.0, 0.0, 0.0, PREFERENCE_SIGMOID, 0)
+    dlogp = torch.empty(n, dtype=torch.float32, device=grad.device)
+    _ok(lmhead_preference_loss_bwd(p, grad, coef, targets, cu_seqlens, dlogp), "lmhead_preference_loss_bwd")
+    return dlogp
+
+
+class PreferenceLoss(torch.autograd.Function):
+    """(loss, rewards) of preference_loss_forward."""
+
+    @staticmethod
+    def forward(ctx, logp, cu_seqlens, ref_logp, targets, how):
+        f = preference_loss_forward(logp, cu_seqlens, ref_logp, targets, *how)
+        ctx.save_for_backward(f.coef, cu_seqlens, targets)
+        ctx.n = logp.shape[0]
+        ctx.mark_non_differentiable(f.rewards)
+        ctx.set_materialize_grads(False)
+        return f.loss, f.rewards
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g, _):
+        if g is None:
+            return (None,) * 5
+        coef, cu_seqlens, targets = ctx.saved_tensors
+        return (preference_loss_backward(g.to(torch.float32), coef, ctx.n, cu_seqlens, targets),) + (None,) * 4
+
+
+def preference_loss(logp, cu_seqlens, ref_logp=None, targets=None, kind: str = "sigmoid", beta: float = 0.1,
+                    margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False, num_pairs: int = -1):
+    """(loss, rewards) with the gradient of logp alone; see
+    preference_loss_forward. Differentiable once."""
+    return PreferenceLoss.apply(logp, cu_seqlens, ref_logp, targets,
+                                (kind, beta, margin, label_smoothing, average, num_pairs))
+
+
+# ------------------------------------------------------------------- AdamW
+
+class AdamWState(NamedTuple):
+    exp_avg: torch.Tensor                              # fp32 or e4m3, the parameter's elements
+    exp_avg_sq: torch.Tensor                           # fp32 v, or e4m3 sqrt(v)
+    exp_avg_scale: Optional[torch.Tensor] = None       # e4m3: fp32 [ceil(numel / 128)]
+    exp_avg_sq_scale: Optional[torch.Tensor] = None
+
+
+def adamw_state(param, dtype=torch.float32) -> AdamWState:
+    """A parameter's states before its first step: fp32, or float8_e4m3fn with
+    block scales (2.06 bytes per element instead of 8)."""
+    if dtype == torch.float32:
+        return AdamWState(torch.zeros_like(param, dtype=dtype), torch.zeros_like(param, dtype=dtype))
+    if dtype != torch.float8_e4m3fn:
+        raise ValueError("dtype must be float32 or float8_e4m3fn")
+    blocks = -(-param.numel() // FP8_BLOCK)
+    m, v = (torch.zeros(param.shape, dtype=torch.uint8, device=param.device).view(dtype) for _ in range(2))
+    return AdamWState(m, v, *(torch.ones(blocks, dtype=torch.float32, device=param.device) for _ in range(2)))
+
+
+class AdamWPlan:
+    """The tensors of a step, checked and laid out once (adamw_plan). It keeps
+    the storages that the tensors had then: a parameter or gradient that is given
+    another storage needs another plan."""
+
+    def __init__(self, device, table, count, keep):
+        self.device, self.table, self.count, self.keep = device, table, count, keep
+
+
+def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[AdamWState],
+               copies: Optional[Sequence[Optional[torch.Tensor]]] = None) -> AdamWPlan:
+    """A plan for adamw_step: parameters bf16 or fp32, gradients bf16 or fp32 of
+    the same shapes (kept in place from step to step, as accumulators are),
+    states from adamw_state, copies None or bf16 tensors that take the rounded
+    parameters. All contiguous, on one GPU, and none sharing memory with another."""
+    copies = [None] * len(params) if copies is None else list(copies)
+    if not len(params) == len(grads) == len(states) == len(copies):
+        raise ValueError("params, grads, states and copies must be of one length")
+    if len(params) == 0:
+        raise ValueError("a plan needs a parameter")
+    table = (lmhead_adamw_tensor * len(params))()
+    dev, keep, spans = None, [], []
+    for i, (p, g, s, c) in enumerate(zip(params, grads, states, copies)):
+        _check_gpu(f"params[{i}]", p, _BF16_F32, p.shape if isinstance(p, torch.Tensor) else (), dev)
+        dev = p.device
+        shape = p.shape
+        _check_gpu(f"grads[{i}]", g, _BF16_F32, shape, dev)
+        m, v, ms, vs = s
+        _check_gpu(f"states[{i}].exp_avg", m, (torch.float32, torch.float8_e4m3fn), shape, dev)
+        _check_gpu(f"states[{i}].exp_avg_sq", v, (m.dtype,), shape, dev)
+        e8 = m.dtype == torch.float8_e4m3fn
+        if (ms is not None) != e8 or (vs is not None) != e8:
+            raise ValueError(f"states[{i}]: scales go with e4m3 states")
+        if e8:
+            blocks = -(-p.numel() // FP8_BLOCK)
+            for name, t in (("exp_avg_scale", ms), ("exp_avg_sq_scale", vs)):
+                _check_gpu(f"states[{i}].{name}", t, (torch.float32,), (blocks,), dev)
+        if c is not None:
+            _check_gpu(f"copies[{i}]", c, (torch.bfloat16,), shape, dev)
+        tensors = [t.detach() for t in (p, g, m, v, ms, vs, c) if t is not None]
+        keep += tensors
+        spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel() > 0]
+        table[i] = lmhead_adamw_tensor(_p(p), _p(g), _p(m), _p(v), _p(ms), _p(vs), _p(c), p.numel(),
+                                       _DTYPES[p.dtype], _DTYPES[g.dtype], _WEIGHT_DTYPES[m.dtype], 0)
+    spans.sort()
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("two tensors of the plan share memory")
+    return AdamWPlan(dev, table, len(params), keep)
+
+
+def adamw_step(plan: AdamWPlan, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.0, grad_scale: Optional[torch.Tensor] = None,
+               seed: Optional[int] = None) -> None:
+    """One AdamW step of the plan's tensors, in place; see lmhead_adamw_step.
+    step: 1 for the first, or an int32 device tensor of one element (read at
+    each replay of a captured step); lr: a number or an fp32 device tensor of one;
+    grad_scale: an fp32 device tensor of one that multiplies the gradients. seed:
+    8-bit states round at random by it, the step and the element's place, and so
+    follow slow changes on average; without, to nearest."""
+    p = lmhead_adamw(0.0, beta1, beta2, eps, weight_decay, 1, None, None, None, int(seed is not None),
+                     (seed or 0) & 0xffffffff)
+    if isinstance(step, torch.Tensor):
+        _check_scalar("step", step, torch.int32, plan.device)
+        p.device_step = step.data_ptr()
+    else:
+        p.step = int(step)
+    if isinstance(lr, torch.Tensor):
+        _check_scalar("lr", lr, torch.float32, plan.device)
+        p.device_lr = lr.data_ptr()
+    else:
+        p.lr = lr
+    if grad_scale is not None:
+        _check_scalar("grad_scale", grad_scale, torch.float32, plan.device)
+        p.grad_scale = grad_scale.data_ptr()
+    if plan.device.index == torch.cuda.current_device():
+        _ok(lmhead_adamw_step(p, plan.table, plan.count), "lmhead_adamw_step")
+        return
+    with torch.cuda.device(plan.device):
+        _ok(lmhead_adamw_step(p, plan.table, plan.count), "lmhead_adamw_step")

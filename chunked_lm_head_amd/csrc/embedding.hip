@@ -9,12 +9,12 @@
 //      of one bucket (id mod B, so that common ids spread over the buckets) and
 //      reads all n ids, twice: once to count, once to place. It needs nothing
 //      from the others: its first place is the number of ids of lower buckets,
-//      which it counts along. Where the whole gradient is written, the
-//      workgroup also writes the zeros of its ids without a token.
-//   2. sum: a workgroup adds kSumRows tokens of that order over 2048 columns.
-//      A run of one id within them is finished there; a run that passes a
-//      border leaves fp32 partial sums.
-//   3. join: partial sums of such runs, in order.
+//      which it counts along. Where the whole gradient is written, further
+//      workgroups of this launch write its zeros meanwhile, 16 KB each.
+//   2. sum: a run of tokens of one id is cut into pieces of R (16, or 64 above
+//      16,384 tokens); 16 .. 64 lanes add a piece over up to 1024 columns. A run
+//      of one piece is finished there, longer ones leave fp32 partial sums.
+//   3. join: the pieces of the longer runs, in order.
 #include "host_util.h"
 #include "train_kernels.h"
 #include "vec8.h"
@@ -74,10 +74,18 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int log_lan
 
 // ----------------------------------------------------------------- backward
 
-constexpr int kLocals = 512;   // ids of one bucket
-constexpr int kWaves = 16;     // of a grouping workgroup
-constexpr int kSumCols = 2048; // columns of a summing workgroup
+constexpr int kLocals = 512;       // ids of one bucket
+constexpr int kWaves = 16;         // of a grouping workgroup
+constexpr int kLogPiece = 4, kLogPieceMany = 6;
+constexpr int64_t kManyTokens = 16384;
+constexpr int64_t kMaxFill = int64_t(1) << 21;   // workgroups that write zeros
+constexpr int kHeld = 8;          // ids per lane of a grouping wave in registers
+constexpr int kJoinWaves = 4;
 constexpr int kJoinCols = 256;
+
+// An item is a piece's first token in the order: .x its length and flags, .y the
+// whole run's length. Other tokens have .x 0.
+constexpr int kItemLength = 0xff, kItemFirst = 0x100, kItemLong = 0x200;
 
 int buckets_log(int64_t vocab) {
     int b = 8;
@@ -89,34 +97,53 @@ struct GroupArgs {
     const int32_t* ids;
     int64_t n, vocab;
     int log_buckets;
+    int log_piece;
     int32_t *hdr, *order, *keys;
-    uint4* zero_into;     // dweight where untouched rows are written, else null
-    int64_t row_vectors;  // 16-byte vectors of its rows
+    int2* items;
+    uint4* zeros;     // dweight where all of it is written, else null
+    int64_t vectors;  // 16-byte vectors of it
 };
 
-__global__ __launch_bounds__(1024) void group_tokens_kernel(GroupArgs a) {
+__global__ __launch_bounds__(1024, 8) void group_tokens_kernel(GroupArgs a) {
     // places of (id, wave): an id's tokens stand in the order of the waves' segments
     __shared__ int place[kLocals * kWaves];
-    __shared__ int total[kLocals];
+    __shared__ int total[kLocals], start[kLocals];
     __shared__ int wave_sum[kWaves], wave_low[kWaves], wave_bad[kWaves];
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    if ((int)blockIdx.x >> a.log_buckets != 0) {
+        const unsigned first = 1u << a.log_buckets;
+        for (int64_t v = (int64_t)(blockIdx.x - first) * 1024 + t; v < a.vectors; v += (int64_t)(gridDim.x - first) * 1024)
+            a.zeros[v] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
     const int bucket = blockIdx.x, mask = (1 << a.log_buckets) - 1;
     for (int i = t; i < kLocals * kWaves; i += 1024) place[i] = 0;
     __syncthreads();
     const int64_t segment = (a.n + kWaves * 64 - 1) / (kWaves * 64) * 64;
     const int64_t from = wave * segment, to = from + segment < a.n ? from + segment : a.n;
     int low = 0, bad = 0x7fffffff;
-#pragma unroll 8
-    for (int64_t i = from + lane; i < to; i += 64) {
-        const int id = a.ids[i];
-        if (id < 0) continue;
-        if (id >= a.vocab) {
-            bad = bad < (int)i ? bad : (int)i;
-            continue;
+    int ids[kHeld];
+    const auto fetch = [&](int64_t i0) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int64_t i = i0 + k * 64 + lane;
+            ids[k] = i < to ? a.ids[i] : -1;
         }
-        const int b = id & mask;
-        low += b < bucket;
-        if (b == bucket) atomicAdd(&place[(id >> a.log_buckets) * kWaves + wave], 1);
+    };
+    for (int64_t i0 = from; i0 < to; i0 += 64 * kHeld) {
+        fetch(i0);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int id = ids[k], i = (int)(i0 + k * 64 + lane);
+            if (id < 0) continue;
+            if (id >= a.vocab) {
+                bad = bad < i ? bad : i;
+                continue;
+            }
+            const int b = id & mask;
+            low += b < bucket;
+            if (b == bucket) atomicAdd(&place[(id >> a.log_buckets) * kWaves + wave], 1);
+        }
     }
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
@@ -153,6 +180,7 @@ __global__ __launch_bounds__(1024) void group_tokens_kernel(GroupArgs a) {
         all += wave_sum[w];
     }
     run += base - sum;
+    if ((t & 1) == 0) start[t >> 1] = run;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         place[t * 8 + k] = run;
@@ -170,150 +198,170 @@ __global__ __launch_bounds__(1024) void group_tokens_kernel(GroupArgs a) {
     __syncthreads();
     if (all > 0) {
         volatile int* at = place + wave;   // this wave's column
-        for (int64_t i0 = from; i0 < to; i0 += 64) {
-            const int64_t i = i0 + lane;
-            const int id = i < to ? a.ids[i] : -1;
-            const bool mine = id >= 0 && id < a.vocab && (id & mask) == bucket;
-            unsigned long long left = __ballot(mine);
-            while (left != 0) {   // one id a turn, its lanes in order
-                const int lead = __ffsll((long long)left) - 1;
-                const int one = __shfl(id, lead);
-                const unsigned long long same = __ballot(mine && id == one);
-                const int slot = (one >> a.log_buckets) * kWaves;
-                const int first = at[slot];
-                if (mine && id == one) {
-                    const int p = first + __popcll(same & ((1ull << lane) - 1));
-                    a.order[p] = (int)i;
-                    a.keys[p] = id;
+        for (int64_t i0 = from; i0 < to; i0 += 64 * kHeld) {
+            if (to - from > 64 * kHeld) fetch(i0);   // else they are still held
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) {
+                const int id = ids[k];
+                const bool mine = id >= 0 && id < a.vocab && (id & mask) == bucket;
+                unsigned long long left = __ballot(mine);
+                while (left != 0) {   // one id a turn, its lanes in order
+                    const int lead = __ffsll((long long)left) - 1;
+                    const int one = __shfl(id, lead);
+                    const unsigned long long same = __ballot(mine && id == one);
+                    const int slot = (one >> a.log_buckets) * kWaves;
+                    const int first = at[slot];
+                    if (mine && id == one) {
+                        const int p = first + __popcll(same & ((1ull << lane) - 1));
+                        const int l = one >> a.log_buckets, q = p - start[l], c = total[l], piece = 1 << a.log_piece;
+                        int2 item = make_int2(0, c);
+                        if ((q & (piece - 1)) == 0)
+                            item.x = (c - q < piece ? c - q : piece) | (q == 0 ? kItemFirst : 0) |
+                                     (c > piece ? kItemLong : 0);
+                        a.order[p] = (int)(i0 + k * 64 + lane);
+                        a.keys[p] = id;
+                        a.items[p] = item;
+                    }
+                    if (lane == lead) at[slot] = first + __popcll(same);
+                    left &= ~same;
                 }
-                if (lane == lead) at[slot] = first + __popcll(same);
-                left &= ~same;
             }
         }
-    }
-    if (a.zero_into == nullptr) return;
-    for (int l = wave; l < kLocals; l += kWaves) {
-        const int64_t id = ((int64_t)l << a.log_buckets) + bucket;
-        if (id >= a.vocab) break;
-        if (total[l] != 0) continue;
-        uint4* row = a.zero_into + id * a.row_vectors;
-        for (int64_t v = lane; v < a.row_vectors; v += 64) row[v] = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
 struct SumArgs {
     EmbedBwdArgs e;
     const int32_t *hdr, *order, *keys;
-    float* partial;   // [blocks][2][hidden]: a block's first run, if it began before; its last, if it goes on
-    int slices;
+    const int2* items;
+    float* partial;    // [2 windows][hidden], see partial_row
+    int log_piece, log_lanes;
+    unsigned parts;
 };
 
-// dweight's vector i of a row from the id's finished sum
-template <bool W32>
-__device__ __forceinline__ void finish(const EmbedBwdArgs& e, int64_t id, int vec, const V8& sum) {
-    const int64_t at = id * (e.hidden >> 3) + vec;
-    V8 f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) f.v[c] = sum.v[c] * e.scale;
-    if (e.accumulate) {
-        const V8 old = load8<W32>(e.dweight, at);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) f.v[c] += old.v[c];
-    }
-    store8<W32>(e.dweight, at, f);
+// A window is as many places of the order as a piece is long. A run's pieces
+// begin a window apart, so a window holds at most one later piece of a long run
+// and, behind it, at most one first piece of another.
+__device__ __forceinline__ int64_t partial_row(int64_t place, int log_piece, bool first) {
+    return 2 * (place >> log_piece) + (first ? 1 : 0);
 }
 
-template <bool D32, bool W32>
+// A workgroup takes the items among 16 places of the order, over 64 VPL vectors of
+// 8 columns (a part of the row). All that says where its operands stand is
+// loaded at once; then 16 .. 64 lanes each take every 4th .. 16th item.
+template <bool D32, bool W32, int VPL>
 __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs a) {
-    __shared__ int token[kSumRows], key[kSumRows + 2];
-    const int64_t block = blockIdx.x / a.slices;
-    const int slice = (int)(blockIdx.x - block * a.slices);
-    const int64_t count = a.hdr[kHdrCount], i0 = block * kSumRows;
-    if (i0 >= count) return;
-    const int rows = (int)(count - i0 < kSumRows ? count - i0 : kSumRows);
-    const int t = threadIdx.x;
-    if (t < kSumRows + 2) {   // key[1 + j]: row j's; -1 before the first and behind the last row of all
-        const int64_t i = i0 + t - 1;
-        key[t] = i >= 0 && i < count ? a.keys[i] : -1;
-    }
-    if (t < rows) token[t] = a.order[i0 + t];
-    __syncthreads();
-    const int nv = a.e.hidden >> 3, vec = slice * (kSumCols / 8) + t;
-    if (vec >= nv) return;
-    V8 sum = zeros8();
-    bool first = true;
-    for (int j0 = 0; j0 < rows; j0 += 8) {
-        V8 f[8];
+    const int lanes = 1 << a.log_lanes, sub = threadIdx.x & (lanes - 1), near = threadIdx.x & 15;
+    const unsigned group = blockIdx.x / a.parts, part = blockIdx.x - group * a.parts;
+    const int64_t place0 = (int64_t)group * 16, place = place0 + near, end = a.e.n - 1;
+    const int64_t at = place < end ? place : end, at16 = place + 16 < end ? place + 16 : end;
+    int2 item = a.items[at];
+    const int key = a.keys[at], token_lo = a.order[at], token_hi = a.order[at16];
+    if (place >= a.hdr[kHdrCount]) item.x = 0;
+    // of these 16 lanes (every 16 of the wave hold the same)
+    unsigned live = (unsigned)(__ballot(item.x != 0) >> (threadIdx.x & 48)) & 0xffffu;
+    for (int skip = threadIdx.x >> a.log_lanes; skip > 0 && live != 0; --skip) live &= live - 1;
+    const int nv = a.e.hidden >> 3, v0 = (int)part * 64 * VPL + sub;
+    while (live != 0) {
+        const int o = __ffs((int)live) - 1;
+        const int flags = __shfl(item.x, o, 16), length = flags & kItemLength;
+        const bool whole = (flags & kItemLong) == 0, add = whole && a.e.accumulate;
+        const int64_t row = (int64_t)__shfl(key, o, 16) * nv;
+        V8 sum[VPL];
+        Raw8<W32> old[VPL];
+        if (add)   // under way while the tokens are summed
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (j0 + u < rows) f[u] = load8<D32>(a.e.dout, (int64_t)token[j0 + u] * nv + vec);
+            for (int k = 0; k < VPL; ++k)
+                if (v0 + k * lanes < nv) old[k] = load_raw8<W32>(a.e.dweight, row + v0 + k * lanes);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int j = j0 + u;
-            if (j >= rows) break;
+        for (int k = 0; k < VPL; ++k) sum[k] = zeros8();
+        constexpr int U = 4;   // tokens in flight
+        for (int j0 = 0; j0 < length; j0 += 16) {
+            const int stop = length - j0 < 16 ? length - j0 : 16;
+            const int later = j0 > 0 && near < stop ? a.order[place0 + o + j0 + near] : 0;
+            for (int j = 0; j < stop; j += U) {
+                Raw8<D32> f[U][VPL];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) sum.v[c] += f[u].v[c];
-            const int k = key[1 + j];
-            const bool last = j == rows - 1;
-            if (!last && key[2 + j] == k) continue;
-            const bool before = first && key[0] == k, after = last && key[2 + j] == k;
-            if (before || after) {
-                float* out = a.partial + (block * 2 + (before ? 0 : 1)) * a.e.hidden;
-                store8<true>(out, vec, sum);
-            } else {
-                finish<W32>(a.e, k, vec, sum);
+                for (int u = 0; u < U; ++u) {
+                    const int i = o + j + u;
+                    const int lo = __shfl(token_lo, i, 16), hi = __shfl(token_hi, i, 16), on = __shfl(later, j + u, 16);
+                    const int64_t from = (int64_t)(j0 > 0 ? on : i < 16 ? lo : hi) * nv;
+                    if (j + u < stop)
+#pragma unroll
+                        for (int k = 0; k < VPL; ++k)
+                            if (v0 + k * lanes < nv) f[u][k] = load_raw8<D32>(a.e.dout, from + v0 + k * lanes);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (j + u < stop)
+#pragma unroll
+                        for (int k = 0; k < VPL; ++k) {
+                            const V8 x = to8<D32>(f[u][k]);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) sum[k].v[c] += x.v[c];
+                        }
             }
-            sum = zeros8();
-            first = false;
         }
+        float* out = a.partial + partial_row(place0 + o, a.log_piece, (flags & kItemFirst) != 0) * a.e.hidden;
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            const int v = v0 + k * lanes;
+            if (v >= nv) continue;
+            if (!whole) {
+                store8<true>(out, v, sum[k]);
+                continue;
+            }
+            const V8 before = add ? to8<W32>(old[k]) : zeros8();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sum[k].v[c] = sum[k].v[c] * a.e.scale + before.v[c];
+            store8<W32>(a.e.dweight, row + v, sum[k]);
+        }
+        for (int skip = 256 >> a.log_lanes; skip > 0 && live != 0; --skip) live &= live - 1;
     }
 }
 
-// The runs that begin in a block and pass its end: that block's last partial
-// sum and the following blocks' first ones. Sixteen waves take every 16th of
-// the latter and are added in order. Four columns per lane.
+// The long run whose first piece lies in this workgroup's window, if there is
+// one. Four columns per lane; each wave takes every fourth piece, then their
+// sums are added in order.
 template <bool W32>
-__global__ __launch_bounds__(1024) void embedding_join_kernel(SumArgs a) {
-    __shared__ float4 part[16][64];
-    const int64_t block = blockIdx.x;
-    const int64_t count = a.hdr[kHdrCount], next = (block + 1) * kSumRows;
-    if (next >= count) return;
-    const int k = a.keys[next - 1];
-    if (a.keys[next] != k) return;
-    if (block > 0 && a.keys[block * kSumRows] == k && a.keys[block * kSumRows - 1] == k) return;   // began before
-    int64_t lo = block + 1, hi = (count - 1) / kSumRows;   // the last block that begins with k
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
-        if (a.keys[mid * kSumRows] == k) lo = mid;
-        else hi = mid - 1;
-    }
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+__global__ __launch_bounds__(64 * kJoinWaves) void embedding_join_kernel(SumArgs a) {
+    __shared__ float4 part_sum[kJoinWaves][64];
+    const int64_t count = a.hdr[kHdrCount], window = blockIdx.x, from = window << a.log_piece;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t place = from + lane;
+    const bool in = lane < 1 << a.log_piece && place < count;
+    const int2 item = in ? a.items[place] : make_int2(0, 0);
+    const unsigned long long heads = __ballot((item.x & kItemFirst) != 0 && (item.x & kItemLong) != 0);
+    if (heads == 0) return;
+    const int lead = __ffsll((long long)heads) - 1;
+    const int length = __shfl(item.y, lead);
+    const int64_t pieces = ((int64_t)length + (1 << a.log_piece) - 1) >> a.log_piece;
+    const int64_t id = a.keys[from + lead];
     const int col = (int)blockIdx.y * kJoinCols + lane * 4;
-    const bool in = col < a.e.hidden;
+    const bool live = col < a.e.hidden;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (in) {
+    if (live) {
 #pragma unroll 8
-        for (int64_t b = block + 1 + wave; b <= lo; b += 16) {
-            const float4 v = *reinterpret_cast<const float4*>(a.partial + b * 2 * a.e.hidden + col);
+        for (int64_t j = wave; j < pieces; j += kJoinWaves) {
+            const float4 v = *reinterpret_cast<const float4*>(a.partial + (2 * (window + j) + (j == 0)) * a.e.hidden + col);
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
             s.w += v.w;
         }
     }
-    part[wave][lane] = s;
+    part_sum[wave][lane] = s;
     __syncthreads();
-    if (wave != 0 || !in) return;
-    s = *reinterpret_cast<const float4*>(a.partial + (block * 2 + 1) * a.e.hidden + col);
+    if (wave != 0 || !live) return;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) {
-        const float4 v = part[w][lane];
+    for (int w = 1; w < kJoinWaves; ++w) {
+        const float4 v = part_sum[w][lane];
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
         s.w += v.w;
     }
-    const int64_t at = (int64_t)k * a.e.hidden + col;
+    const int64_t at = id * a.e.hidden + col;
     float f[4] = {s.x * a.e.scale, s.y * a.e.scale, s.z * a.e.scale, s.w * a.e.scale};
     if (W32) {
         float4* out = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.e.dweight) + at);
@@ -339,12 +387,16 @@ __global__ __launch_bounds__(1024) void embedding_join_kernel(SumArgs a) {
 }
 
 template <bool D32, bool W32>
-void sum_and_join(const SumArgs& a, hipStream_t s) {
-    const int64_t blocks = cdiv(a.e.n, kSumRows);
-    embedding_sum_kernel<D32, W32><<<(unsigned)(blocks * a.slices), 256, 0, s>>>(a);
-    if (blocks > 1)
-        embedding_join_kernel<W32>
-            <<<dim3((unsigned)blocks, (unsigned)cdiv(a.e.hidden, kJoinCols)), 1024, 0, s>>>(a);
+void sum_and_join(SumArgs a, hipStream_t s) {
+    const int nv = a.e.hidden >> 3;
+    a.log_lanes = nv <= 16 ? 4 : nv <= 32 ? 5 : 6;
+    a.parts = nv <= 64 ? 1u : (unsigned)cdiv(nv, 128);
+    const unsigned x = (unsigned)cdiv(a.e.n, 16) * a.parts;
+    if (nv <= 64) embedding_sum_kernel<D32, W32, 1><<<x, 256, 0, s>>>(a);
+    else embedding_sum_kernel<D32, W32, 2><<<x, 256, 0, s>>>(a);
+    if (a.e.n > 1 << a.log_piece)
+        embedding_join_kernel<W32><<<dim3((unsigned)cdiv(a.e.n, 1 << a.log_piece), (unsigned)cdiv(a.e.hidden, kJoinCols)),
+                                     64 * kJoinWaves, 0, s>>>(a);
 }
 
 }  // namespace
@@ -369,43 +421,53 @@ void launch_embedding(const EmbedArgs& a, hipStream_t s) {
 
 namespace {
 struct EmbedPlan {
-    int64_t order, keys, partial, bytes;
+    int log_buckets, log_piece;
+    int64_t order, keys, items, partial, bytes;
 };
-EmbedPlan plan_bwd(int64_t n, int hidden) {
+EmbedPlan plan_bwd(int64_t n, int64_t vocab, int hidden) {
     EmbedPlan p;
+    p.log_buckets = buckets_log(vocab);
+    p.log_piece = n > kManyTokens ? kLogPieceMany : kLogPiece;
     p.order = 256;
     p.keys = p.order + round_up(4 * n, 256);
-    p.partial = p.keys + round_up(4 * n, 256);
-    const int64_t blocks = cdiv(n, kSumRows);
-    p.bytes = p.partial + (blocks > 1 ? round_up(blocks * 2 * hidden * 4, 256) : 0);
+    p.items = p.keys + round_up(4 * n, 256);
+    p.partial = p.items + round_up(8 * n, 256);
+    const int64_t piece = 1 << p.log_piece;
+    p.bytes = p.partial + (n > piece ? round_up(cdiv(n, piece) * 2 * hidden * 4, 256) : 0);
     return p;
 }
 }  // namespace
 
-size_t embedding_bwd_workspace(int64_t n, int hidden) { return (size_t)plan_bwd(n, hidden).bytes; }
+size_t embedding_bwd_workspace(int64_t n, int64_t vocab, int hidden) {
+    return (size_t)plan_bwd(n, vocab, hidden).bytes;
+}
 
 void launch_embedding_bwd(const EmbedBwdArgs& a, void* workspace, hipStream_t s) {
-    const EmbedPlan p = plan_bwd(a.n, a.hidden);
+    const EmbedPlan p = plan_bwd(a.n, a.vocab, a.hidden);
     char* w = (char*)workspace;
     GroupArgs g;
     g.ids = a.ids;
     g.n = a.n;
     g.vocab = a.vocab;
-    g.log_buckets = buckets_log(a.vocab);
+    g.log_buckets = p.log_buckets;
+    g.log_piece = p.log_piece;
     g.hdr = (int32_t*)w;
     g.order = (int32_t*)(w + p.order);
     g.keys = (int32_t*)(w + p.keys);
-    g.zero_into = a.accumulate ? nullptr : (uint4*)a.dweight;
-    g.row_vectors = (int64_t)a.hidden * (a.dweight_f32 ? 4 : 2) / 16;
-    group_tokens_kernel<<<1u << g.log_buckets, 1024, 0, s>>>(g);
+    g.items = (int2*)(w + p.items);
+    g.zeros = (uint4*)a.dweight;
+    g.vectors = a.accumulate ? 0 : a.vocab * (a.hidden * (a.dweight_f32 ? 4 : 2) / 16);
+    const int64_t fills = cdiv(g.vectors, 1024);
+    group_tokens_kernel<<<(1u << g.log_buckets) + (unsigned)(fills < kMaxFill ? fills : kMaxFill), 1024, 0, s>>>(g);
     if (a.n == 0) return;
     SumArgs u;
     u.e = a;
     u.hdr = g.hdr;
     u.order = g.order;
     u.keys = g.keys;
+    u.items = g.items;
     u.partial = (float*)(w + p.partial);
-    u.slices = (int)cdiv(a.hidden, kSumCols);
+    u.log_piece = p.log_piece;
     if (a.dout_f32) {
         if (a.dweight_f32) sum_and_join<true, true>(u, s);
         else sum_and_join<true, false>(u, s);

@@ -17,7 +17,8 @@ constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int64_t kMaxVocab = int64_t(1) << 30;
 constexpr int64_t kMaxHidden = 65536;
 constexpr int64_t kMaxGroups = 16777215;   // 256-thread workgroups of one launch: 2^32 - 1 work-items
-constexpr int64_t kMaxJoins = 4194303;     // 1024-thread workgroups
+constexpr int64_t kMaxGathered = int64_t(1) << 26;    // tokens of an embedding gradient
+constexpr int64_t kMaxGradVocab = int64_t(1) << 28;   // 1024 threads for each 512 ids
 constexpr int64_t kMaxSequences = int64_t(1) << 24;
 constexpr float kMaxFloat = 3.402823466e38f;
 
@@ -32,7 +33,7 @@ int validate(const lmhead_embedding* p, bool backward) {
     if (p->n < 0 || p->n > kMaxRows || p->vocab < 1 || p->vocab > kMaxVocab) return LMHEAD_ERR_SHAPE;
     if (p->hidden < 64 || p->hidden > kMaxHidden || p->hidden % 64 != 0) return LMHEAD_ERR_SHAPE;
     if (p->weight_dtype == LMHEAD_DTYPE_E4M3 && p->hidden % kQBlock != 0) return LMHEAD_ERR_SHAPE;
-    if (backward && (cdiv(p->n, kSumRows) * cdiv(p->hidden, 2048) > kMaxGroups || cdiv(p->n, kSumRows) > kMaxJoins))
+    if (backward && (p->n > kMaxGathered || p->vocab > kMaxGradVocab || cdiv(p->n, 16) * cdiv(p->hidden, 1024) > kMaxGroups))
         return LMHEAD_ERR_SHAPE;
     return LMHEAD_OK;
 }
@@ -170,7 +171,7 @@ int lmhead_embedding_fwd(const lmhead_embedding* p, const int32_t* ids, const vo
 }
 
 size_t lmhead_embedding_bwd_workspace_size(const lmhead_embedding* p) {
-    return validate(p, true) == LMHEAD_OK ? embedding_bwd_workspace(p->n, (int)p->hidden) : 0;
+    return validate(p, true) == LMHEAD_OK ? embedding_bwd_workspace(p->n, p->vocab, (int)p->hidden) : 0;
 }
 
 int lmhead_embedding_bwd(const lmhead_embedding* p, const int32_t* ids, const void* dout, void* dweight,

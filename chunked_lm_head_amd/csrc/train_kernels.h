@@ -37,8 +37,7 @@ struct EmbedBwdArgs {
     float scale;
     int dout_f32, dweight_f32, accumulate;
 };
-constexpr int kSumRows = 32;   // tokens, in the order of their ids, that one workgroup sums
-size_t embedding_bwd_workspace(int64_t n, int hidden);
+size_t embedding_bwd_workspace(int64_t n, int64_t vocab, int hidden);
 void launch_embedding_bwd(const EmbedBwdArgs& a, void* workspace, hipStream_t s);
 
 // -------------------------------------------------------- token_losses.hip

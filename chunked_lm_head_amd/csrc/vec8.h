@@ -53,6 +53,29 @@ __device__ __forceinline__ V8 load8(const void* p, int64_t i) {
     }
     return bf16_to8(reinterpret_cast<const uint4*>(p)[i]);
 }
+// as it stands in memory, to be turned into fp32 when it is used
+template <bool F32>
+struct Raw8 {
+    uint4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_raw8(const void* p, int64_t i) {
+    Raw8<F32> r;
+#pragma unroll
+    for (int k = 0; k < (F32 ? 2 : 1); ++k) r.w[k] = reinterpret_cast<const uint4*>(p)[(F32 ? 2 : 1) * i + k];
+    return r;
+}
+template <bool F32>
+__device__ __forceinline__ V8 to8(const Raw8<F32>& r) {
+    if (!F32) return bf16_to8(r.w[0]);
+    const uint4 a = r.w[0], b = r.w[F32 ? 1 : 0];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    V8 f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f.v[c] = __builtin_bit_cast(float, w[c]);
+    return f;
+}
+
 template <bool F32>
 __device__ __forceinline__ void store8(void* p, int64_t i, const V8& f) {
     if (F32) {

@@ -51,8 +51,8 @@ enum lmhead_train_device_error {
  *                 of dweight (enum lmhead_dtype).
  *   out_dtype     type of out and dout (enum lmhead_dtype).
  *   accumulate    0 or 1, lmhead_embedding_bwd: 1 adds to dweight.
- *   Launch sizes of the backward: ceil(n / 32) * ceil(hidden / 2048) <=
- *   16,777,215 and ceil(n / 32) <= 4,194,303.
+ *   The backward (launch sizes): n <= 2^26, vocab <= 2^28,
+ *   ceil(n / 16) * ceil(hidden / 1024) <= 16,777,215.
  */
 typedef struct lmhead_embedding {
     int64_t n;
@@ -82,8 +82,8 @@ int lmhead_embedding_fwd(const lmhead_embedding* p, const int32_t* ids, const vo
                          void* stream);
 
 /* Bytes of workspace lmhead_embedding_bwd needs (0 for an invalid problem):
- * the tokens in the order of their ids, and fp32 sums of ids that pass a border
- * of 32 such tokens. */
+ * the tokens in the order of their ids, and fp32 sums of pieces of 16 tokens
+ * (64 above 16,384) of one id. */
 size_t lmhead_embedding_bwd_workspace_size(const lmhead_embedding* p);
 
 /*

@@ -69,16 +69,17 @@ def test_embedding_backward_refusals():
         return lm.lmhead_embedding_bwd(p, *{**ok, **kw}.values())
     for bad in (dict(weight_dtype=2), dict(out_dtype=2), dict(accumulate=-1), dict(scale=INF)):
         assert call(emb(**bad)) == A and size(emb(**bad)) == 0, bad
-    for bad in (dict(n=-1), dict(hidden=100), dict(vocab=0), dict(n=1 << 30, hidden=64), dict(n=1 << 26, hidden=65536)):
+    for bad in (dict(n=-1), dict(hidden=100), dict(vocab=0), dict(n=(1 << 26) + 1), dict(vocab=(1 << 28) + 1),
+                dict(n=1 << 26, hidden=8192)):
         assert call(emb(**bad)) == S and size(emb(**bad)) == 0, bad
     for name in ("ids", "dout", "dweight", "ws"):
         assert call(emb(), **{name: None}) == A, name
         assert call(emb(), **{name: F + 2}) == AL, name
     assert call(emb(n=0), ids=None, dout=None, dweight=None) == A   # an empty call still writes zeros
     assert call(emb(), bytes=size(emb()) - 1) == W
-    # tokens of one block need no partial sums; two blocks have two rows each
-    assert size(emb(n=32)) == 256 + 2 * 256 and size(emb(n=0)) == 256
-    assert size(emb(n=33)) == 256 + 2 * 256 + 2 * 2 * 256 * 4
+    # four regions by tokens, and two rows of partial sums for each window of 16
+    assert size(emb(n=16)) == 4 * 256 and size(emb(n=0)) == 256
+    assert size(emb(n=17)) == 4 * 256 + 2 * 2 * 256 * 4
 
 
 def pol(**kw):

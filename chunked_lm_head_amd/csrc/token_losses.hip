@@ -8,9 +8,12 @@
 // = beta (s_chosen - s_rejected) - margin; dlogp_t = g coef_q.
 //
 // 12 to 24 bytes per token and direction and few operations: small batches are
-// bound by launches, large ones by memory. So up to 8192 tokens are one launch
-// of one workgroup; above, tiles of 2048 tokens leave 64-bit partial sums and a
-// second launch (a third for the sequence mean) adds them in order.
+// bound by launches and by the latency of loads that wait for one another,
+// large ones by memory. So up to 8192 tokens are one launch of one workgroup;
+// above, tiles of 1024 tokens leave 64-bit partial sums and a second launch (a
+// third for the sequence mean) adds them in order. A tile's tokens are loaded
+// before its sequences are looked up, and all its sums cross the workgroup
+// behind one barrier.
 //
 // Sequences and tiles. A tile's partial of sequence s stands at slot tile + s:
 // along the packed tokens either the tile or the sequence moves on, so no two
@@ -22,10 +25,10 @@ namespace lmhead {
 
 namespace {
 
-constexpr int kTileThreads = 256, kWholeThreads = 1024;
-constexpr int kEach = 8;   // tokens per thread
-constexpr int64_t kWholeTokens = kWholeThreads * kEach;
-constexpr int64_t kTileTokens = kTileThreads * kEach;
+constexpr int kTileThreads = 256, kTileEach = 4;     // tokens per thread
+constexpr int64_t kTileTokens = kTileThreads * kTileEach;
+constexpr int kFewThreads = 256, kWholeThreads = 1024, kWholeEach = 8;
+constexpr int64_t kFewTokens = kFewThreads * kWholeEach, kWholeTokens = kWholeThreads * kWholeEach;
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -33,17 +36,24 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
-// Sum over the workgroup, for every thread, in the order of lanes and waves. red: a
-// double per wave.
-template <int THREADS>
-__device__ __forceinline__ double group_sum(double v, double* red) {
-    v = wave_sum(v);
+// Sums over the workgroup of N values per thread, for every thread: lanes, then
+// waves, each in a fixed tree. red: N doubles per wave, used once.
+template <int N, int THREADS>
+__device__ __forceinline__ void group_sums(double (&v)[N], double* red) {
+    constexpr int WAVES = THREADS / 64;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = wave_sum(v[k]);
+    if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < N; ++k) red[k * WAVES + (threadIdx.x >> 6)] = v[k];
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = 0.0;
-    for (int w = 0; w < THREADS / 64; ++w) s += red[w];
-    return s;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        v[k] = red[k * WAVES + (lane & (WAVES - 1))];
+#pragma unroll
+        for (int m = 1; m < WAVES; m <<= 1) v[k] += __shfl_xor(v[k], m);
+    }
 }
 
 __device__ __forceinline__ int64_t border(const Tokens& t, int64_t s) {
@@ -52,21 +62,37 @@ __device__ __forceinline__ int64_t border(const Tokens& t, int64_t s) {
     return v < 0 ? 0 : v < t.n ? v : t.n;
 }
 
-// The last sequence whose first token is at or before i (-1: none), searched by
-// a wave: 64 places at once, so two steps find one of 4096 borders.
-__device__ __forceinline__ int64_t sequence_at(const Tokens& t, int64_t i) {
-    if (t.cu == nullptr) return 0;
-    int64_t lo = 0, hi = t.sequences + 1;   // number of borders <= i
-    const int lane = threadIdx.x & 63;
-    while (lo < hi) {
-        const int64_t step = (hi - lo + 63) >> 6, at = lo + lane * step;
-        const int c = __popcll(__ballot(at < hi && border(t, at) <= i));
-        if (c == 0) break;
-        const int64_t end = lo + c * step;
-        lo = lo + (c - 1) * step + 1;
-        hi = end < hi ? end : hi;
+// The last sequences whose first tokens are at or before i and j >= i (-1: none),
+// searched by a wave: 64 borders at once, the first look for both, so that two
+// looks find any of 4096.
+struct Span {
+    int64_t first, last;
+};
+__device__ __forceinline__ void narrow(int64_t& lo, int64_t& hi, int64_t step, int c) {
+    if (c == 0) {
+        hi = lo;
+        return;
     }
-    return lo - 1;
+    const int64_t end = lo + c * step;
+    lo = lo + (c - 1) * step + 1;
+    hi = end < hi ? end : hi;
+}
+__device__ __forceinline__ Span sequences_at(const Tokens& t, int64_t i, int64_t j) {
+    if (t.cu == nullptr) return Span{0, 0};
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, hi = t.sequences + 1, lo2 = 0, hi2 = hi;   // the number of borders <= i, <= j
+    const int64_t step0 = (hi + 63) >> 6, at0 = lane * step0;
+    const int64_t b0 = at0 < hi ? border(t, at0) : t.n + 1;
+    narrow(lo, hi, step0, __popcll(__ballot(b0 <= i)));
+    narrow(lo2, hi2, step0, __popcll(__ballot(b0 <= j)));
+    while (lo < hi || lo2 < hi2) {
+        const int64_t step = (hi - lo + 63) >> 6, at = lo + lane * step;
+        const int64_t step2 = (hi2 - lo2 + 63) >> 6, at2 = lo2 + lane * step2;
+        const int64_t b = at < hi ? border(t, at) : t.n + 1, b2 = at2 < hi2 ? border(t, at2) : t.n + 1;
+        if (lo < hi) narrow(lo, hi, step, __popcll(__ballot(b <= i)));
+        if (lo2 < hi2) narrow(lo2, hi2, step2, __popcll(__ballot(b2 <= j)));
+    }
+    return Span{lo - 1, lo2 - 1};
 }
 // The same for one token between two known answers.
 __device__ __forceinline__ int64_t sequence_between(const Tokens& t, int64_t lo, int64_t hi, int64_t i) {
@@ -141,70 +167,85 @@ __device__ __forceinline__ Term policy_term(const PolicyArgs& a, float logp, flo
 
 // ------------------------------------------------------------------- policy
 
-struct Sums {
-    double loss, count, kl, clipped, ratio, back;
-};
+enum { kLoss, kCount, kKl, kClipped, kRatio, kBack };   // a tile's six sums
 struct Part {
     double sum, count;
 };
 
 struct Tile {
-    int64_t t0, t1, first, last;   // tokens; sequences at the first and last one
+    int64_t t0, t1;
+    Span at;   // sequences at its first and last token
 };
-template <int THREADS>
-__device__ __forceinline__ Tile tile_at(const Tokens& t, int64_t index) {
+template <int TOKENS>
+__device__ __forceinline__ Tile tile_of(const Tokens& t) {
     Tile o;
-    o.t0 = index * THREADS * kEach;
-    o.t1 = o.t0 + THREADS * kEach < t.n ? o.t0 + THREADS * kEach : t.n;
-    o.first = sequence_at(t, o.t0);
-    o.last = o.t1 - o.t0 > 1 ? sequence_at(t, o.t1 - 1) : o.first;
+    o.t0 = (int64_t)blockIdx.x * TOKENS;
+    o.t1 = o.t0 + TOKENS < t.n ? o.t0 + TOKENS : t.n;
     return o;
 }
+__device__ __forceinline__ void look_up(Tile& o, const Tokens& t) {
+    o.at = sequences_at(t, o.t0, o.t1 > o.t0 ? o.t1 - 1 : o.t0);
+}
 
-// A tile's terms, summed; per token kept in LDS where sequences are summed apart.
-template <int THREADS, bool SEQ>
-__device__ __forceinline__ Sums policy_tile(const PolicyArgs& a, const Tile& tile, float* kept, uint8_t* counts,
-                                            double* red) {
-    Sums s = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
-    float logp[kEach], old[kEach], ref[kEach], adv[kEach];
-    bool valid[kEach];
+// A thread's tokens t0 + thread, + THREADS, ...: loaded at once; then their terms.
+template <int THREADS, int EACH>
+struct PolicyTokens {
+    float logp[EACH], old[EACH], ref[EACH], adv[EACH];
+    int32_t target[EACH];
+
+    __device__ __forceinline__ void load(const PolicyArgs& a, const Tile& tile) {
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-        const int64_t i = tile.t0 + k * THREADS + threadIdx.x;
-        valid[k] = false;
-        logp[k] = old[k] = ref[k] = adv[k] = 0.0f;
-        if (i >= tile.t1) continue;
-        const int64_t q = sequence_between(a.t, tile.first, tile.last, i);
-        valid[k] = q >= 0 && q < a.t.sequences && (a.t.targets == nullptr || a.t.targets[i] >= 0);
-        logp[k] = a.logp[i];
-        old[k] = a.old_logp != nullptr ? a.old_logp[i] : logp[k];
-        if (a.ref_logp != nullptr) ref[k] = a.ref_logp[i];
-        if (!a.per_sequence) adv[k] = a.advantage[i];
-        else if (valid[k]) adv[k] = a.advantage[q];
+        for (int k = 0; k < EACH; ++k) {
+            const int64_t i = tile.t0 + k * THREADS + threadIdx.x;
+            logp[k] = old[k] = ref[k] = adv[k] = 0.0f;
+            target[k] = -1;
+            if (i >= tile.t1) continue;
+            logp[k] = a.logp[i];
+            if (a.old_logp != nullptr) old[k] = a.old_logp[i];
+            if (a.ref_logp != nullptr) ref[k] = a.ref_logp[i];
+            if (!a.per_sequence) adv[k] = a.advantage[i];
+            target[k] = a.t.targets != nullptr ? a.t.targets[i] : 0;
+        }
     }
+    // the token's sequence where it counts, else -1
+    __device__ __forceinline__ int64_t place(const PolicyArgs& a, const Tile& tile, int k) const {
+        const int64_t i = tile.t0 + k * THREADS + threadIdx.x;
+        if (i >= tile.t1 || target[k] < 0) return -1;
+        const int64_t q = sequence_between(a.t, tile.at.first, tile.at.last, i);
+        return q < a.t.sequences ? q : -1;
+    }
+    __device__ __forceinline__ Term term(const PolicyArgs& a, int k, int64_t q) const {
+        return policy_term(a, logp[k], a.old_logp != nullptr ? old[k] : logp[k], ref[k],
+                           a.per_sequence ? a.advantage[q >= 0 ? q : 0] : adv[k]);
+    }
+};
+
+// A tile's terms, summed per thread; per token kept in LDS where sequences are
+// summed apart.
+template <int THREADS, int EACH, bool SEQ>
+__device__ __forceinline__ void policy_tile(const PolicyArgs& a, Tile& tile, double (&s)[6], float* kept, uint8_t* counts) {
+    PolicyTokens<THREADS, EACH> tokens;
+    tokens.load(a, tile);
+    look_up(tile, a.t);
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-        const Term o = policy_term(a, logp[k], old[k], ref[k], adv[k]);
-        if (valid[k]) {   // whatever stands in the other places takes no part
-            s.loss += (double)o.loss;
-            s.count += 1.0;
-            s.kl += (double)o.kl;
-            s.clipped += o.clipped ? 1.0 : 0.0;
-            s.ratio += (double)o.ratio;
-            s.back += (double)o.back;
+    for (int k = 0; k < 6; ++k) s[k] = 0.0;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+        const int64_t q = tokens.place(a, tile, k);
+        const Term o = tokens.term(a, k, q);
+        if (q >= 0) {   // whatever stands in the other places takes no part
+            if (!SEQ) s[kLoss] += (double)o.loss;
+            s[kCount] += 1.0;
+            s[kKl] += (double)o.kl;
+            s[kClipped] += o.clipped ? 1.0 : 0.0;
+            s[kRatio] += (double)o.ratio;
+            s[kBack] += (double)o.back;
         }
         if (SEQ) {
             kept[k * THREADS + threadIdx.x] = o.loss;
-            counts[k * THREADS + threadIdx.x] = valid[k];
+            counts[k * THREADS + threadIdx.x] = q >= 0;
         }
     }
-    if (!SEQ) s.loss = group_sum<THREADS>(s.loss, red);
-    s.count = group_sum<THREADS>(s.count, red);
-    s.kl = group_sum<THREADS>(s.kl, red);
-    s.clipped = group_sum<THREADS>(s.clipped, red);
-    s.ratio = group_sum<THREADS>(s.ratio, red);
-    s.back = group_sum<THREADS>(s.back, red);   // also: kept and counts are written
-    return s;
 }
 
 // One sequence's part of a tile, from LDS, by one wave.
@@ -252,47 +293,54 @@ __device__ __forceinline__ double weigh(const PolicyArgs& a, int64_t q, const Pa
 }
 
 // What is left once the totals are known: called by every thread of the last workgroup.
-__device__ __forceinline__ void policy_end(const PolicyArgs& a, const Sums& s, double sequence_means, int threads) {
+__device__ __forceinline__ void policy_end(const PolicyArgs& a, const double (&s)[6], int threads) {
     const bool seq = a.reduction == 2;
-    const double w = a.reduction == 0 ? share(a.num_valid, s.count) : 1.0;
+    const double w = a.reduction == 0 ? share(a.num_valid, s[kCount]) : 1.0;
     if (!seq)   // one weight for all
         for (int64_t q = threadIdx.x; q < a.t.sequences; q += threads) a.weights[q] = (float)w;
     if (threadIdx.x != 0) return;
-    a.loss[0] = (float)(seq ? sequence_means : w > 0.0 ? w * s.loss : 0.0);
+    a.loss[0] = (float)(seq ? s[kLoss] : w > 0.0 ? w * s[kLoss] : 0.0);
     if (a.stats == nullptr) return;
-    const double each = s.count > 0.0 ? 1.0 / s.count : 0.0;
-    a.stats[0] = (float)(s.kl * each);
-    a.stats[1] = (float)(s.clipped * each);
-    a.stats[2] = (float)(s.ratio * each);
-    a.stats[3] = (float)(s.back * each);
+    const double each = s[kCount] > 0.0 ? 1.0 / s[kCount] : 0.0;
+    a.stats[0] = (float)(s[kKl] * each);
+    a.stats[1] = (float)(s[kClipped] * each);
+    a.stats[2] = (float)(s[kRatio] * each);
+    a.stats[3] = (float)(s[kBack] * each);
 }
 
-template <bool SEQ>
-__global__ __launch_bounds__(kWholeThreads) void policy_whole_kernel(PolicyArgs a) {
-    __shared__ double red[kWholeThreads / 64];
-    __shared__ float kept[SEQ ? kWholeTokens : 1];
-    __shared__ uint8_t counts[SEQ ? kWholeTokens : 1];
-    const Tile tile = tile_at<kWholeThreads>(a.t, 0);
-    const Sums s = policy_tile<kWholeThreads, SEQ>(a, tile, kept, counts, red);
-    double means = 0.0;
-    if (SEQ) {
-        for (int64_t q = threadIdx.x >> 6; q < a.t.sequences; q += kWholeThreads / 64)
+template <int THREADS, bool SEQ>
+__global__ __launch_bounds__(THREADS) void policy_whole_kernel(PolicyArgs a) {
+    __shared__ double red[6 * THREADS / 64];
+    __shared__ float kept[SEQ ? THREADS * kWholeEach : 1];
+    __shared__ uint8_t counts[SEQ ? THREADS * kWholeEach : 1];
+    Tile tile = tile_of<THREADS * kWholeEach>(a.t);
+    double s[6];
+    policy_tile<THREADS, kWholeEach, SEQ>(a, tile, s, kept, counts);
+    if (SEQ) {   // every sequence by a wave; a lane's share of the loss is its mean
+        __syncthreads();
+        double means = 0.0;
+        for (int64_t q = threadIdx.x >> 6; q < a.t.sequences; q += THREADS / 64)
             means += weigh(a, q, part_of(a.t, tile, q, kept, counts));
-        means = group_sum<kWholeThreads>((threadIdx.x & 63) == 0 ? means : 0.0, red);
+        s[kLoss] = (threadIdx.x & 63) == 0 ? means : 0.0;
     }
-    policy_end(a, s, means, kWholeThreads);
+    group_sums<6, THREADS>(s, red);
+    policy_end(a, s, THREADS);
 }
 
 template <bool SEQ>
-__global__ __launch_bounds__(kTileThreads) void policy_tiles_kernel(PolicyArgs a, Sums* tiles, Part* slots) {
-    __shared__ double red[kTileThreads / 64];
+__global__ __launch_bounds__(kTileThreads) void policy_tiles_kernel(PolicyArgs a, double* tiles, Part* slots) {
+    __shared__ double red[6 * kTileThreads / 64];
     __shared__ float kept[SEQ ? kTileTokens : 1];
     __shared__ uint8_t counts[SEQ ? kTileTokens : 1];
-    const Tile tile = tile_at<kTileThreads>(a.t, blockIdx.x);
-    const Sums s = policy_tile<kTileThreads, SEQ>(a, tile, kept, counts, red);
-    if (threadIdx.x == 0) tiles[blockIdx.x] = s;
+    Tile tile = tile_of<kTileTokens>(a.t);
+    double s[6];
+    policy_tile<kTileThreads, kTileEach, SEQ>(a, tile, s, kept, counts);
+    group_sums<6, kTileThreads>(s, red);   // its barrier: kept and counts are written
+    if (threadIdx.x == 0)
+#pragma unroll
+        for (int k = 0; k < 6; ++k) tiles[k * (int64_t)gridDim.x + blockIdx.x] = s[k];
     if (!SEQ) return;
-    for (int64_t q = (tile.first > 0 ? tile.first : 0) + (threadIdx.x >> 6); q <= tile.last && q < a.t.sequences;
+    for (int64_t q = (tile.at.first > 0 ? tile.at.first : 0) + (threadIdx.x >> 6); q <= tile.at.last && q < a.t.sequences;
          q += kTileThreads / 64) {
         const Part p = part_of(a.t, tile, q, kept, counts);
         if ((threadIdx.x & 63) == 0) slots[blockIdx.x + q] = p;
@@ -306,72 +354,44 @@ __global__ __launch_bounds__(kTileThreads) void policy_sequences_kernel(PolicyAr
     if ((threadIdx.x & 63) == 0) means[q] = m;
 }
 
-__global__ __launch_bounds__(kWholeThreads) void policy_join_kernel(PolicyArgs a, const Sums* tiles, int64_t count,
+__global__ __launch_bounds__(kWholeThreads) void policy_join_kernel(PolicyArgs a, const double* tiles, int64_t count,
                                                                     const double* means) {
-    __shared__ double red[kWholeThreads / 64];
-    Sums s = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+    __shared__ double red[6 * kWholeThreads / 64];
+    double s[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+    for (int64_t i = threadIdx.x; i < count; i += kWholeThreads)
+#pragma unroll
+        for (int k = 0; k < 6; ++k) s[k] += tiles[k * count + i];
+    if (a.reduction == 2) {
+        s[kLoss] = 0.0;
 #pragma unroll 4
-    for (int64_t i = threadIdx.x; i < count; i += kWholeThreads) {
-        const Sums o = tiles[i];
-        s.loss += o.loss;
-        s.count += o.count;
-        s.kl += o.kl;
-        s.clipped += o.clipped;
-        s.ratio += o.ratio;
-        s.back += o.back;
+        for (int64_t q = threadIdx.x; q < a.t.sequences; q += kWholeThreads) s[kLoss] += means[q];
     }
-    double m = 0.0;
-    if (a.reduction == 2)
-#pragma unroll 4
-        for (int64_t q = threadIdx.x; q < a.t.sequences; q += kWholeThreads) m += means[q];
-    s.loss = group_sum<kWholeThreads>(a.reduction == 2 ? m : s.loss, red);
-    s.count = group_sum<kWholeThreads>(s.count, red);
-    s.kl = group_sum<kWholeThreads>(s.kl, red);
-    s.clipped = group_sum<kWholeThreads>(s.clipped, red);
-    s.ratio = group_sum<kWholeThreads>(s.ratio, red);
-    s.back = group_sum<kWholeThreads>(s.back, red);
-    policy_end(a, s, s.loss, kWholeThreads);
-}
-
-constexpr int kBackEach = 4;
-constexpr int64_t kBackTile = kTileThreads * kBackEach;
-
-// The tile of a backward workgroup: kBackEach tokens per thread.
-__device__ __forceinline__ Tile back_tile(const Tokens& t) {
-    Tile o;
-    o.t0 = (int64_t)blockIdx.x * kBackTile;
-    o.t1 = o.t0 + kBackTile < t.n ? o.t0 + kBackTile : t.n;
-    o.first = sequence_at(t, o.t0);
-    o.last = sequence_at(t, o.t1 - 1);
-    return o;
+    group_sums<6, kWholeThreads>(s, red);
+    policy_end(a, s, kWholeThreads);
 }
 
 __global__ __launch_bounds__(kTileThreads) void policy_bwd_kernel(PolicyArgs a, const float* grad, float* dlogp) {
-    const Tile tile = back_tile(a.t);
+    Tile tile = tile_of<kTileTokens>(a.t);
+    PolicyTokens<kTileThreads, kTileEach> tokens;
+    tokens.load(a, tile);
     const float g = grad[0];
+    look_up(tile, a.t);
 #pragma unroll
-    for (int k = 0; k < kBackEach; ++k) {
+    for (int k = 0; k < kTileEach; ++k) {
         const int64_t i = tile.t0 + k * kTileThreads + threadIdx.x;
         if (i >= tile.t1) continue;
-        const int64_t q = sequence_between(a.t, tile.first, tile.last, i);
-        float d = 0.0f;
-        if (q >= 0 && q < a.t.sequences && (a.t.targets == nullptr || a.t.targets[i] >= 0)) {
-            const float logp = a.logp[i];
-            const Term o = policy_term(a, logp, a.old_logp != nullptr ? a.old_logp[i] : logp,
-                                       a.ref_logp != nullptr ? a.ref_logp[i] : 0.0f,
-                                       a.advantage[a.per_sequence ? q : i]);
-            d = g * (a.weights[q] * o.slope);
-        }
-        dlogp[i] = d;
+        const int64_t q = tokens.place(a, tile, k);
+        const Term o = tokens.term(a, k, q);
+        dlogp[i] = q >= 0 ? g * (a.weights[q] * o.slope) : 0.0f;
     }
 }
 
 // --------------------------------------------------------------- preference
 
-template <int THREADS>
+template <int THREADS, int EACH>
 __device__ __forceinline__ void preference_tile(const PreferenceArgs& a, const Tile& tile, float* kept, uint8_t* counts) {
 #pragma unroll
-    for (int k = 0; k < kEach; ++k) {
+    for (int k = 0; k < EACH; ++k) {
         const int64_t i = tile.t0 + k * THREADS + threadIdx.x;
         float gain = 0.0f;
         bool valid = false;
@@ -382,7 +402,6 @@ __device__ __forceinline__ void preference_tile(const PreferenceArgs& a, const T
         kept[k * THREADS + threadIdx.x] = gain;
         counts[k * THREADS + threadIdx.x] = valid;
     }
-    __syncthreads();
 }
 
 // One pair from its sequences' sums: writes the rewards and coefficients, returns its share of the loss.
@@ -421,26 +440,31 @@ __device__ __forceinline__ double pair_loss(const PreferenceArgs& a, int64_t pai
     return one > 0.0 ? loss * one : 0.0;
 }
 
-__global__ __launch_bounds__(kWholeThreads) void preference_whole_kernel(PreferenceArgs a) {
-    __shared__ double red[kWholeThreads / 64];
-    __shared__ float kept[kWholeTokens];
-    __shared__ uint8_t counts[kWholeTokens];
-    Tile tile = {0, a.t.n, 0, 0};
-    preference_tile<kWholeThreads>(a, tile, kept, counts);
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void preference_whole_kernel(PreferenceArgs a) {
+    __shared__ double red[THREADS / 64];
+    __shared__ float kept[THREADS * kWholeEach];
+    __shared__ uint8_t counts[THREADS * kWholeEach];
+    const Tile tile = tile_of<THREADS * kWholeEach>(a.t);
+    preference_tile<THREADS, kWholeEach>(a, tile, kept, counts);
+    __syncthreads();
     const int64_t pairs = a.t.sequences / 2;
-    double loss = 0.0;
-    for (int64_t j = threadIdx.x >> 6; j < pairs; j += kWholeThreads / 64)
-        loss += pair_loss(a, j, part_of(a.t, tile, j, kept, counts), part_of(a.t, tile, pairs + j, kept, counts));
-    loss = group_sum<kWholeThreads>((threadIdx.x & 63) == 0 ? loss : 0.0, red);
-    if (threadIdx.x == 0) a.loss[0] = (float)loss;
+    double loss[1] = {0.0};
+    for (int64_t j = threadIdx.x >> 6; j < pairs; j += THREADS / 64)
+        loss[0] += pair_loss(a, j, part_of(a.t, tile, j, kept, counts), part_of(a.t, tile, pairs + j, kept, counts));
+    if ((threadIdx.x & 63) != 0) loss[0] = 0.0;
+    group_sums<1, THREADS>(loss, red);
+    if (threadIdx.x == 0) a.loss[0] = (float)loss[0];
 }
 
 __global__ __launch_bounds__(kTileThreads) void preference_tiles_kernel(PreferenceArgs a, Part* slots) {
     __shared__ float kept[kTileTokens];
     __shared__ uint8_t counts[kTileTokens];
-    const Tile tile = tile_at<kTileThreads>(a.t, blockIdx.x);
-    preference_tile<kTileThreads>(a, tile, kept, counts);
-    for (int64_t q = (tile.first > 0 ? tile.first : 0) + (threadIdx.x >> 6); q <= tile.last && q < a.t.sequences;
+    Tile tile = tile_of<kTileTokens>(a.t);
+    preference_tile<kTileThreads, kTileEach>(a, tile, kept, counts);
+    look_up(tile, a.t);
+    __syncthreads();
+    for (int64_t q = (tile.at.first > 0 ? tile.at.first : 0) + (threadIdx.x >> 6); q <= tile.at.last && q < a.t.sequences;
          q += kTileThreads / 64) {
         const Part p = part_of(a.t, tile, q, kept, counts);
         if ((threadIdx.x & 63) == 0) slots[blockIdx.x + q] = p;
@@ -456,24 +480,30 @@ __global__ __launch_bounds__(kTileThreads) void preference_pairs_kernel(Preferen
 
 __global__ __launch_bounds__(kWholeThreads) void preference_join_kernel(const double* each, int64_t count, float* loss) {
     __shared__ double red[kWholeThreads / 64];
-    double s = 0.0;
+    double s[1] = {0.0};
 #pragma unroll 4
-    for (int64_t i = threadIdx.x; i < count; i += kWholeThreads) s += each[i];
-    s = group_sum<kWholeThreads>(s, red);
-    if (threadIdx.x == 0) loss[0] = (float)s;
+    for (int64_t i = threadIdx.x; i < count; i += kWholeThreads) s[0] += each[i];
+    group_sums<1, kWholeThreads>(s, red);
+    if (threadIdx.x == 0) loss[0] = (float)s[0];
 }
 
 __global__ __launch_bounds__(kTileThreads) void preference_bwd_kernel(Tokens t, const float* grad, const float* coef,
                                                                       float* dlogp) {
-    const Tile tile = back_tile(t);
-    const float g = grad[0];
+    Tile tile = tile_of<kTileTokens>(t);
+    int32_t target[kTileEach];
 #pragma unroll
-    for (int k = 0; k < kBackEach; ++k) {
+    for (int k = 0; k < kTileEach; ++k) {
+        const int64_t i = tile.t0 + k * kTileThreads + threadIdx.x;
+        target[k] = t.targets != nullptr && i < tile.t1 ? t.targets[i] : 0;
+    }
+    const float g = grad[0];
+    look_up(tile, t);
+#pragma unroll
+    for (int k = 0; k < kTileEach; ++k) {
         const int64_t i = tile.t0 + k * kTileThreads + threadIdx.x;
         if (i >= tile.t1) continue;
-        const int64_t q = sequence_between(t, tile.first, tile.last, i);
-        const bool valid = q >= 0 && q < t.sequences && (t.targets == nullptr || t.targets[i] >= 0);
-        dlogp[i] = valid ? g * coef[q] : 0.0f;
+        const int64_t q = sequence_between(t, tile.at.first, tile.at.last, i);
+        dlogp[i] = q >= 0 && q < t.sequences && target[k] >= 0 ? g * coef[q] : 0.0f;
     }
 }
 
@@ -482,7 +512,7 @@ __global__ __launch_bounds__(kTileThreads) void preference_bwd_kernel(Tokens t, 
 size_t policy_workspace(int64_t n, int64_t sequences, int reduction) {
     if (n <= kWholeTokens) return 256;
     const int64_t tiles = cdiv(n, kTileTokens);
-    int64_t bytes = round_up(tiles * (int64_t)sizeof(Sums), 256);
+    int64_t bytes = round_up(tiles * 6 * 8, 256);
     if (reduction == 2)
         bytes += round_up((tiles + sequences) * (int64_t)sizeof(Part), 256) + round_up(sequences * 8, 256);
     return (size_t)bytes;
@@ -491,14 +521,19 @@ size_t policy_workspace(int64_t n, int64_t sequences, int reduction) {
 void launch_policy(const PolicyArgs& a, void* workspace, hipStream_t s) {
     const bool seq = a.reduction == 2;
     if (a.t.n <= kWholeTokens) {
-        if (seq) policy_whole_kernel<true><<<1, kWholeThreads, 0, s>>>(a);
-        else policy_whole_kernel<false><<<1, kWholeThreads, 0, s>>>(a);
+        if (a.t.n <= kFewTokens) {
+            if (seq) policy_whole_kernel<kFewThreads, true><<<1, kFewThreads, 0, s>>>(a);
+            else policy_whole_kernel<kFewThreads, false><<<1, kFewThreads, 0, s>>>(a);
+        } else {
+            if (seq) policy_whole_kernel<kWholeThreads, true><<<1, kWholeThreads, 0, s>>>(a);
+            else policy_whole_kernel<kWholeThreads, false><<<1, kWholeThreads, 0, s>>>(a);
+        }
         return;
     }
     const int64_t tiles = cdiv(a.t.n, kTileTokens);
     char* w = (char*)workspace;
-    Sums* sums = (Sums*)w;
-    Part* slots = (Part*)(w + round_up(tiles * (int64_t)sizeof(Sums), 256));
+    double* sums = (double*)w;
+    Part* slots = (Part*)(w + round_up(tiles * 6 * 8, 256));
     double* means = (double*)((char*)slots + round_up((tiles + a.t.sequences) * (int64_t)sizeof(Part), 256));
     if (seq) {
         policy_tiles_kernel<true><<<(unsigned)tiles, kTileThreads, 0, s>>>(a, sums, slots);
@@ -510,7 +545,7 @@ void launch_policy(const PolicyArgs& a, void* workspace, hipStream_t s) {
 }
 
 void launch_policy_bwd(const PolicyArgs& a, const float* grad, float* dlogp, hipStream_t s) {
-    policy_bwd_kernel<<<(unsigned)cdiv(a.t.n, kBackTile), kTileThreads, 0, s>>>(a, grad, dlogp);
+    policy_bwd_kernel<<<(unsigned)cdiv(a.t.n, kTileTokens), kTileThreads, 0, s>>>(a, grad, dlogp);
 }
 
 size_t preference_workspace(int64_t n, int64_t pairs) {
@@ -520,7 +555,8 @@ size_t preference_workspace(int64_t n, int64_t pairs) {
 
 void launch_preference(const PreferenceArgs& a, void* workspace, hipStream_t s) {
     if (a.t.n <= kWholeTokens) {
-        preference_whole_kernel<<<1, kWholeThreads, 0, s>>>(a);
+        if (a.t.n <= kFewTokens) preference_whole_kernel<kFewThreads><<<1, kFewThreads, 0, s>>>(a);
+        else preference_whole_kernel<kWholeThreads><<<1, kWholeThreads, 0, s>>>(a);
         return;
     }
     const int64_t tiles = cdiv(a.t.n, kTileTokens), pairs = a.t.sequences / 2;
@@ -532,7 +568,7 @@ void launch_preference(const PreferenceArgs& a, void* workspace, hipStream_t s) 
 }
 
 void launch_preference_bwd(const Tokens& t, const float* grad, const float* coef, float* dlogp, hipStream_t s) {
-    preference_bwd_kernel<<<(unsigned)cdiv(t.n, kBackTile), kTileThreads, 0, s>>>(t, grad, coef, dlogp);
+    preference_bwd_kernel<<<(unsigned)cdiv(t.n, kTileTokens), kTileThreads, 0, s>>>(t, grad, coef, dlogp);
 }
 
 }  // namespace lmhead

@@ -668,7 +668,8 @@ from .train import (  # noqa: E402
     DEVERR_TOKEN, DTYPE_E4M3, KL_K1, KL_K2, KL_K3, PREFERENCE_HINGE, PREFERENCE_SIGMOID, PREFERENCE_SQUARED,
     REDUCE_MEAN, REDUCE_SEQUENCE_MEAN, REDUCE_SUM, AdamWPlan, AdamWState, Embedding, PolicyLoss, PolicyOutputs,
     PreferenceLoss, PreferenceOutputs, adamw_plan, adamw_state, adamw_step, embedding, embedding_backward,
-    embedding_forward, lmhead_adamw, lmhead_adamw_step, lmhead_adamw_tensor, lmhead_embedding, lmhead_embedding_bwd,
+    embedding_forward, lmhead_adamw, lmhead_adamw_step, lmhead_adamw_table,
+    lmhead_adamw_table_size, lmhead_adamw_tensor, lmhead_embedding, lmhead_embedding_bwd,
     lmhead_embedding_bwd_workspace_size, lmhead_embedding_fwd, lmhead_policy_loss_bwd, lmhead_policy_loss_fwd,
     lmhead_policy_loss_workspace_size, lmhead_policy_problem, lmhead_preference_loss_bwd, lmhead_preference_loss_fwd,
     lmhead_preference_loss_workspace_size, lmhead_preference_problem, policy_loss, policy_loss_backward,

@@ -11,8 +11,8 @@
 // Bound by memory: 10 to 28 bytes per element and about 40 operations. Each
 // element is read and written once; eight consecutive ones per lane, so that 16
 // lanes hold a block of 128 and its maximum is four shuffles. Tensors share a
-// launch: the table of up to 48 travels as a kernel argument (no copy to the
-// device, nothing to keep), a workgroup finds its tensor by its chunk's number.
+// launch; a workgroup finds its tensor by its chunk's number, in a table of up to
+// 48 that travels as a kernel argument, or in the caller's table on the device.
 #include "host_util.h"
 #include "train_kernels.h"
 #include "vec8.h"
@@ -21,12 +21,21 @@ namespace lmhead {
 
 namespace {
 
-constexpr int kTrips = kAdamWChunk / 2048;
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
 
-// lane's eight values at element e; zeros past the end
-template <bool F32>
+// lane's eight values at element e; zeros past the end. STREAM: past the caches
+template <bool F32, bool STREAM>
 __device__ __forceinline__ V8 fetch(const void* p, int64_t e, int64_t numel, bool wide) {
-    if (wide && e + 8 <= numel) return load8<F32>(p, e >> 3);
+    if (wide && e + 8 <= numel) {
+        if (!STREAM) return load8<F32>(p, e >> 3);
+        Raw8<F32> r;
+#pragma unroll
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) {
+            const words4 w = __builtin_nontemporal_load(reinterpret_cast<const words4*>(p) + (F32 ? 2 : 1) * (e >> 3) + k);
+            r.w[k] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return to8<F32>(r);
+    }
     V8 f = zeros8();
 #pragma unroll
     for (int c = 0; c < 8; ++c)
@@ -35,10 +44,23 @@ __device__ __forceinline__ V8 fetch(const void* p, int64_t e, int64_t numel, boo
                          : __builtin_bit_cast(float, (uint32_t)reinterpret_cast<const bf16_bits*>(p)[e + c] << 16);
     return f;
 }
-template <bool F32>
+template <bool F32, bool STREAM>
 __device__ __forceinline__ void put(void* p, int64_t e, int64_t numel, bool wide, const V8& f) {
     if (wide && e + 8 <= numel) {
-        store8<F32>(p, e >> 3, f);
+        if (!STREAM) {
+            store8<F32>(p, e >> 3, f);
+        } else if (F32) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                words4 w;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c] = __builtin_bit_cast(uint32_t, f.v[4 * k + c]);
+                __builtin_nontemporal_store(w, reinterpret_cast<words4*>(p) + 2 * (e >> 3) + k);
+            }
+        } else {
+            const uint4 w = to_bf16x8(f);
+            __builtin_nontemporal_store(words4{w.x, w.y, w.z, w.w}, reinterpret_cast<words4*>(p) + (e >> 3));
+        }
         return;
     }
 #pragma unroll
@@ -58,7 +80,7 @@ __device__ __forceinline__ uint2 fetch_codes(const void* p, int64_t e, int64_t n
 }
 __device__ __forceinline__ void put_codes(void* p, int64_t e, int64_t numel, bool wide, const uint2& q) {
     if (wide && e + 8 <= numel) {
-        reinterpret_cast<uint2*>(p)[e >> 3] = q;
+        __builtin_nontemporal_store((uint64_t)q.y << 32 | q.x, reinterpret_cast<uint64_t*>(p) + (e >> 3));
         return;
     }
     const uint32_t w[2] = {q.x, q.y};
@@ -97,10 +119,14 @@ __device__ __forceinline__ float cut_at_random(float y, uint32_t random20) {
 // least the least code. RANDOM: noise of the eight, in bits 4 .. 19.
 template <bool ROOT, bool RANDOM>
 __device__ __forceinline__ uint2 codes(const V8& f, float scale, const uint32_t* noise) {
+    // the quotient of x inv and one step with its remainder: as the division
+    // rounds, but where it lies within 2^-22 of a step from the middle of two values
+    const float inv = 1.0f / scale;
     V8 y;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-        y.v[c] = f.v[c] / scale;
+        const float q = f.v[c] * inv;
+        y.v[c] = __builtin_fmaf(__builtin_fmaf(-q, scale, f.v[c]), inv, q);
         if (ROOT && f.v[c] > 0.0f) y.v[c] = y.v[c] < 0x1p-9f ? 0x1p-9f : y.v[c];
         if (RANDOM) y.v[c] = cut_at_random(y.v[c], ROOT ? noise[c] >> 16 << 4 : (noise[c] & 0xffffu) << 4);
     }
@@ -121,8 +147,13 @@ struct Step {
 
 template <bool P32, bool G32, bool S8, bool RANDOM>
 __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int64_t chunk) {
+    // 8-bit states leave few bytes per element: two trips in flight, past the
+    // caches (622 M bf16 parameters: 1050 us; one trip 1139, two through the
+    // caches 1093). fp32 states: one trip through them (525 M: 2296 us; two 2323,
+    // past the caches 2390).
+    constexpr int kTrips = (S8 ? kAdamWChunk8 : kAdamWChunk) / 2048;
     const bool wide = (t.kind & kAdamWWide) != 0;
-    const int64_t e0 = chunk * kAdamWChunk + threadIdx.x * 8;
+    const int64_t e0 = chunk * (2048 * kTrips) + threadIdx.x * 8;
     V8 p[kTrips], g[kTrips], m[kTrips], v[kTrips];
     uint2 mq[S8 ? kTrips : 1], vq[S8 ? kTrips : 1];
     float ms[S8 ? kTrips : 1], vs[S8 ? kTrips : 1];
@@ -130,16 +161,16 @@ __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int6
 #pragma unroll
     for (int j = 0; j < kTrips; ++j) {
         const int64_t e = e0 + j * 2048;
-        p[j] = fetch<P32>(t.param, e, t.numel, wide);
-        g[j] = fetch<G32>(t.grad, e, t.numel, wide);
+        p[j] = fetch<P32, S8>(t.param, e, t.numel, wide);
+        g[j] = fetch<G32, S8>(t.grad, e, t.numel, wide);
         if (S8) {
             mq[S8 ? j : 0] = fetch_codes(t.m, e, t.numel, wide);
             vq[S8 ? j : 0] = fetch_codes(t.v, e, t.numel, wide);
             ms[S8 ? j : 0] = e < t.numel ? t.m_scale[e >> 7] : 0.0f;
             vs[S8 ? j : 0] = e < t.numel ? t.v_scale[e >> 7] : 0.0f;
         } else {
-            m[j] = fetch<true>(t.m, e, t.numel, wide);
-            v[j] = fetch<true>(t.v, e, t.numel, wide);
+            m[j] = fetch<true, false>(t.m, e, t.numel, wide);
+            v[j] = fetch<true, false>(t.v, e, t.numel, wide);
         }
     }
 #pragma unroll
@@ -162,8 +193,11 @@ __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int6
             const float gc = g[j].v[c] * k.grad_scale;
             const float mc = __builtin_fmaf(k.rest1, gc, k.beta1 * m[j].v[c]);
             const float vc = __builtin_fmaf(k.rest2 * gc, gc, k.beta2 * v[j].v[c]);
-            const float rc = sqrtf(vc);
-            p[j].v[c] = __builtin_fmaf(-k.step_size, mc / __builtin_fmaf(rc, k.root_scale, k.eps), p[j].v[c] * k.keep);
+            // the instructions' own root and reciprocal, each within 2^-23: the
+            // library's correctly rounded ones would double the arithmetic
+            const float rc = __builtin_amdgcn_sqrtf(vc);
+            const float step = mc * __builtin_amdgcn_rcpf(__builtin_fmaf(rc, k.root_scale, k.eps));
+            p[j].v[c] = __builtin_fmaf(-k.step_size, step, p[j].v[c] * k.keep);
             m[j].v[c] = mc;
             v[j].v[c] = vc;
             root.v[c] = rc;
@@ -172,8 +206,8 @@ __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int6
                 v_max = fmaxf(v_max, rc);
             }
         }
-        put<P32>(t.param, e, t.numel, wide, p[j]);
-        if (t.copy != nullptr) put<false>(t.copy, e, t.numel, wide, p[j]);
+        put<P32, S8>(t.param, e, t.numel, wide, p[j]);
+        if (t.copy != nullptr) put<false, S8>(t.copy, e, t.numel, wide, p[j]);
         if (S8) {
             uint32_t noise[RANDOM ? 8 : 1];
             if (RANDOM)
@@ -188,15 +222,14 @@ __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int6
                 t.v_scale[e >> 7] = sv;
             }
         } else {
-            put<true>(t.m, e, t.numel, wide, m[j]);
-            put<true>(t.v, e, t.numel, wide, v[j]);
+            put<true, false>(t.m, e, t.numel, wide, m[j]);
+            put<true, false>(t.v, e, t.numel, wide, v[j]);
         }
     }
 }
 
-__global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
-    __shared__ float now[3];
-    const AdamWScalars& k = a.k;
+// The step's numbers, from the device where they stand there.
+__device__ __forceinline__ Step step_of(const AdamWScalars& k, float* now) {
     Step s = {k.beta1, k.rest1, k.beta2, k.rest2, k.eps, k.keep, k.step_size, k.root_scale, 1.0f, 0u};
     if (k.grad_scale != nullptr) s.grad_scale = k.grad_scale[0];
     if (k.step != nullptr || k.device_lr != nullptr) {
@@ -213,14 +246,10 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
         s.step_size = now[1];
         s.root_scale = now[2];
     }
-    int lo = 0, hi = a.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.tensor[mid].first <= blockIdx.x) lo = mid;
-        else hi = mid - 1;
-    }
-    const AdamWTensor t = a.tensor[lo];
-    const int64_t chunk = blockIdx.x - t.first;
+    return s;
+}
+
+__device__ __forceinline__ void update_any(const AdamWScalars& k, const AdamWTensor& t, Step& s, int64_t chunk) {
     if (k.stochastic) {
         const int64_t step = k.step != nullptr ? (k.step[0] < 1 ? 1 : k.step[0]) : k.host_step;
         s.mix = scramble(k.seed + scramble((uint32_t)step + scramble(t.kind >> kAdamWPlace)));
@@ -233,19 +262,53 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
         }
     }
     switch (t.kind & 7) {
-        case 0: update<false, false, false, false>(t, s, chunk); break;
-        case 1: update<true, false, false, false>(t, s, chunk); break;
-        case 2: update<false, true, false, false>(t, s, chunk); break;
-        case 3: update<true, true, false, false>(t, s, chunk); break;
-        case 4: update<false, false, true, false>(t, s, chunk); break;
-        case 5: update<true, false, true, false>(t, s, chunk); break;
-        case 6: update<false, true, true, false>(t, s, chunk); break;
-        default: update<true, true, true, false>(t, s, chunk); break;
+        case 0: return update<false, false, false, false>(t, s, chunk);
+        case 1: return update<true, false, false, false>(t, s, chunk);
+        case 2: return update<false, true, false, false>(t, s, chunk);
+        case 3: return update<true, true, false, false>(t, s, chunk);
+        case 4: return update<false, false, true, false>(t, s, chunk);
+        case 5: return update<true, false, true, false>(t, s, chunk);
+        case 6: return update<false, true, true, false>(t, s, chunk);
+        default: return update<true, true, true, false>(t, s, chunk);
     }
+}
+
+__global__ __launch_bounds__(256) void adamw_kernel(AdamWArgs a) {
+    __shared__ float now[3];
+    Step s = step_of(a.k, now);
+    int lo = 0, hi = a.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.tensor[mid].first <= blockIdx.x) lo = mid;
+        else hi = mid - 1;
+    }
+    const AdamWTensor t = a.tensor[lo];
+    update_any(a.k, t, s, blockIdx.x - t.first);
+}
+
+// The tensor is the last one whose first chunk is at or before the workgroup's:
+// 64 of them are looked at at once.
+__global__ __launch_bounds__(256) void adamw_table_kernel(AdamWScalars k, AdamWTable table) {
+    __shared__ float now[3];
+    int64_t lo = 0, hi = table.count;   // the number of first chunks <= blockIdx.x
+    while (lo < hi) {
+        const int64_t step = (hi - lo + 63) >> 6, at = lo + (threadIdx.x & 63) * step;
+        const int c = __popcll(__ballot(at < hi && table.first[at] <= blockIdx.x));
+        if (c == 0) break;
+        const int64_t end = lo + c * step;
+        lo = lo + (c - 1) * step + 1;
+        hi = end < hi ? end : hi;
+    }
+    Step s = step_of(k, now);
+    const AdamWTensor t = table.tensor[lo - 1];
+    update_any(k, t, s, blockIdx.x - t.first);
 }
 
 }  // namespace
 
 void launch_adamw(const AdamWArgs& a, hipStream_t s) { adamw_kernel<<<a.chunks, 256, 0, s>>>(a); }
+void launch_adamw_table(const AdamWScalars& k, const AdamWTable& t, uint32_t chunks, hipStream_t s) {
+    adamw_table_kernel<<<chunks, 256, 0, s>>>(k, t);
+}
 
 }  // namespace lmhead

@@ -20,6 +20,8 @@ constexpr int64_t kMaxGroups = 16777215;   // 256-thread workgroups of one launc
 constexpr int64_t kMaxGathered = int64_t(1) << 26;    // tokens of an embedding gradient
 constexpr int64_t kMaxGradVocab = int64_t(1) << 28;   // 1024 threads for each 512 ids
 constexpr int64_t kMaxSequences = int64_t(1) << 24;
+constexpr int64_t kMaxTensors = int64_t(1) << 20;
+constexpr int64_t kMaxNumel = (int64_t(1) << 35) - (int64_t(1) << 24);
 constexpr float kMaxFloat = 3.402823466e38f;
 
 // as the fp32 number that the kernels get
@@ -75,7 +77,7 @@ int check(const lmhead_adamw_tensor& t) {
     if (!dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype) || t.reserved != 0) return LMHEAD_ERR_ARG;
     const bool e8 = t.state_dtype == LMHEAD_DTYPE_E4M3;
     if (!e8 && t.state_dtype != LMHEAD_DTYPE_F32) return LMHEAD_ERR_ARG;
-    if (t.numel < 0 || t.numel > (int64_t(1) << 35)) return LMHEAD_ERR_SHAPE;
+    if (t.numel < 0 || t.numel > kMaxNumel) return LMHEAD_ERR_SHAPE;
     if (t.numel == 0) return LMHEAD_OK;
     if (t.param == nullptr || t.grad == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr) return LMHEAD_ERR_ARG;
     if ((t.exp_avg_scale != nullptr) != e8 || (t.exp_avg_sq_scale != nullptr) != e8) return LMHEAD_ERR_ARG;
@@ -85,6 +87,33 @@ int check(const lmhead_adamw_tensor& t) {
         !aligned(t.copy, 2))
         return LMHEAD_ERR_ALIGN;
     return LMHEAD_OK;
+}
+
+int64_t chunks_of(const lmhead_adamw_tensor& t) {   // at most 2^24 - 2^13, of fp32 states
+    return cdiv(t.numel, t.state_dtype == LMHEAD_DTYPE_E4M3 ? kAdamWChunk8 : kAdamWChunk);
+}
+
+size_t table_tensors(int64_t count) { return (size_t)round_up(4 * count, 64); }   // where a table's tensors begin
+
+AdamWTensor packed(const lmhead_adamw_tensor& t, int64_t place, uint32_t first) {
+    AdamWTensor o;
+    const bool e8 = t.state_dtype == LMHEAD_DTYPE_E4M3;
+    o.param = t.param;
+    o.grad = t.grad;
+    o.m = t.exp_avg;
+    o.v = t.exp_avg_sq;
+    o.m_scale = t.exp_avg_scale;
+    o.v_scale = t.exp_avg_sq_scale;
+    o.copy = (bf16_bits*)t.copy;
+    o.numel = t.numel;
+    o.first = first;
+    o.kind = (t.param_dtype == LMHEAD_DTYPE_F32 ? kAdamWParamF32 : 0) |
+             (t.grad_dtype == LMHEAD_DTYPE_F32 ? kAdamWGradF32 : 0) | (e8 ? kAdamWState8 : 0) |
+             (uint32_t)place << kAdamWPlace;
+    if (aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.exp_avg, e8 ? 8 : 16) &&
+        aligned(t.exp_avg_sq, e8 ? 8 : 16) && aligned(t.copy, 16))
+        o.kind |= kAdamWWide;
+    return o;
 }
 
 Tokens tokens(int64_t n, int64_t sequences, const int32_t* targets, const int32_t* cu) {
@@ -295,15 +324,44 @@ int lmhead_preference_loss_bwd(const lmhead_preference_problem* p, const float* 
     return launched();
 }
 
-int lmhead_adamw_step(const lmhead_adamw* p, const lmhead_adamw_tensor* tensors, int64_t count, void* stream) {
+size_t lmhead_adamw_table_size(int64_t count) {
+    return count < 0 || count > kMaxTensors ? 0 : table_tensors(count) + (size_t)count * sizeof(AdamWTensor);
+}
+
+int lmhead_adamw_table(const lmhead_adamw_tensor* tensors, int64_t count, void* table, size_t table_bytes) {
+    if (count < 0 || count > kMaxTensors) return LMHEAD_ERR_SHAPE;
+    if (count > 0 && (tensors == nullptr || table == nullptr)) return LMHEAD_ERR_ARG;
+    if (!aligned(table, 8)) return LMHEAD_ERR_ALIGN;
+    if (table_bytes < lmhead_adamw_table_size(count)) return LMHEAD_ERR_WORKSPACE;
+    for (int64_t i = 0; i < count; ++i) {
+        const int st = check(tensors[i]);
+        if (st != LMHEAD_OK) return st;
+    }
+    uint32_t* first = (uint32_t*)table;
+    AdamWTensor* out = (AdamWTensor*)((char*)table + table_tensors(count));
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (chunks > kMaxGroups) return LMHEAD_ERR_SHAPE;
+        first[i] = (uint32_t)chunks;
+        out[i] = packed(tensors[i], i, (uint32_t)chunks);
+        chunks += chunks_of(tensors[i]);
+    }
+    return chunks > kMaxGroups ? LMHEAD_ERR_SHAPE : LMHEAD_OK;
+}
+
+int lmhead_adamw_step(const lmhead_adamw* p, const lmhead_adamw_tensor* tensors, int64_t count, const void* table,
+                      void* stream) {
     int st = validate(p);
     if (st != LMHEAD_OK) return st;
-    if (count < 0 || count > (int64_t(1) << 20)) return LMHEAD_ERR_SHAPE;
+    if (count < 0 || count > kMaxTensors) return LMHEAD_ERR_SHAPE;
     if (count > 0 && tensors == nullptr) return LMHEAD_ERR_ARG;
-    if (!aligned(p->device_step, 4) || !aligned(p->device_lr, 4) || !aligned(p->grad_scale, 4)) return LMHEAD_ERR_ALIGN;
+    if (!aligned(p->device_step, 4) || !aligned(p->device_lr, 4) || !aligned(p->grad_scale, 4) || !aligned(table, 8))
+        return LMHEAD_ERR_ALIGN;
+    int64_t chunks = 0;
     for (int64_t i = 0; i < count; ++i) {
         st = check(tensors[i]);
         if (st != LMHEAD_OK) return st;
+        chunks += chunks_of(tensors[i]);
     }
     st = check_device();
     if (st != LMHEAD_OK) return st;
@@ -327,6 +385,14 @@ int lmhead_adamw_step(const lmhead_adamw* p, const lmhead_adamw_tensor* tensors,
     k.keep = (float)(1.0 - p->lr * p->weight_decay);
     k.step_size = (float)(p->lr / -expm1((double)p->step * k.log_beta1));
     k.root_scale = (float)(1.0 / sqrt(-expm1((double)p->step * k.log_beta2)));
+    if (table != nullptr && count > kAdamWTensors && chunks > 0 && chunks <= kMaxGroups) {
+        AdamWTable t;
+        t.first = (const uint32_t*)table;
+        t.tensor = (const AdamWTensor*)((const char*)table + table_tensors(count));
+        t.count = count;
+        launch_adamw_table(k, t, (uint32_t)chunks, (hipStream_t)stream);
+        return launched();
+    }
     a.count = 0;
     a.chunks = 0;
     const auto flush = [&]() {
@@ -335,28 +401,11 @@ int lmhead_adamw_step(const lmhead_adamw* p, const lmhead_adamw_tensor* tensors,
         a.chunks = 0;
     };
     for (int64_t i = 0; i < count; ++i) {
-        const lmhead_adamw_tensor& t = tensors[i];
-        if (t.numel == 0) continue;
-        const int64_t chunks = cdiv(t.numel, kAdamWChunk);   // at most 2^23 of a tensor
-        if (a.count == kAdamWTensors || a.chunks + chunks > kMaxGroups) flush();
-        AdamWTensor& o = a.tensor[a.count++];
-        const bool e8 = t.state_dtype == LMHEAD_DTYPE_E4M3;
-        o.param = t.param;
-        o.grad = t.grad;
-        o.m = t.exp_avg;
-        o.v = t.exp_avg_sq;
-        o.m_scale = t.exp_avg_scale;
-        o.v_scale = t.exp_avg_sq_scale;
-        o.copy = (bf16_bits*)t.copy;
-        o.numel = t.numel;
-        o.first = a.chunks;
-        o.kind = (t.param_dtype == LMHEAD_DTYPE_F32 ? kAdamWParamF32 : 0) |
-                 (t.grad_dtype == LMHEAD_DTYPE_F32 ? kAdamWGradF32 : 0) | (e8 ? kAdamWState8 : 0) |
-                 (uint32_t)i << kAdamWPlace;
-        if (aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.exp_avg, e8 ? 8 : 16) &&
-            aligned(t.exp_avg_sq, e8 ? 8 : 16) && aligned(t.copy, 16))
-            o.kind |= kAdamWWide;
-        a.chunks += (uint32_t)chunks;
+        if (tensors[i].numel == 0) continue;
+        const int64_t more = chunks_of(tensors[i]);
+        if (a.count == kAdamWTensors || a.chunks + more > kMaxGroups) flush();
+        a.tensor[a.count++] = packed(tensors[i], i, a.chunks);
+        a.chunks += (uint32_t)more;
     }
     flush();
     return launched();

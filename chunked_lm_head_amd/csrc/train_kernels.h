@@ -88,7 +88,7 @@ struct AdamWTensor {
 };
 constexpr uint32_t kAdamWParamF32 = 1, kAdamWGradF32 = 2, kAdamWState8 = 4, kAdamWWide = 8;
 constexpr int kAdamWPlace = 4;
-constexpr int kAdamWTensors = 48;   // per launch: the table travels as a kernel argument
+constexpr int kAdamWTensors = 48;   // per launch where the table travels as a kernel argument
 struct AdamWScalars {
     float beta1, rest1, beta2, rest2, eps, decay;   // decay: weight_decay (lr is applied on the device)
     float lr, step_size, root_scale, keep;          // of the host's step and lr
@@ -107,7 +107,15 @@ struct AdamWArgs {
     uint32_t chunks;
     AdamWTensor tensor[kAdamWTensors];
 };
-constexpr int kAdamWChunk = 4096;   // elements, a multiple of 2048
+// On the device: each tensor's first chunk, then the tensors.
+struct AdamWTable {
+    const uint32_t* first;
+    const AdamWTensor* tensor;
+    int64_t count;
+};
+// elements of a workgroup: 2048 with fp32 states, twice as many with 8-bit ones
+constexpr int kAdamWChunk = 2048, kAdamWChunk8 = 4096;
 void launch_adamw(const AdamWArgs& a, hipStream_t s);
+void launch_adamw_table(const AdamWScalars& k, const AdamWTable& t, uint32_t chunks, hipStream_t s);
 
 }  // namespace lmhead

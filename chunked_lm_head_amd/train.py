@@ -11,12 +11,13 @@ that check their arguments, allocate outputs and workspace and raise
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional, Sequence
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import LMHEAD_ERR_SHAPE, LMHeadError, _check_f32, _ok, _on_device_of, _p, _stream, lib
+from . import LMHEAD_ERR_SHAPE, LMHeadError, _ok, _on_device_of, _p, _stream, lib
 from .decode import _DTYPES, FP8_BLOCK, _check_gpu, _workspace
 
 DTYPE_E4M3 = 2
@@ -30,7 +31,9 @@ _KL = {"k1": KL_K1, "k2": KL_K2, "k3": KL_K3}
 _REDUCE = {"mean": REDUCE_MEAN, "sum": REDUCE_SUM, "sequence_mean": REDUCE_SEQUENCE_MEAN}
 _PREFERENCE = {"sigmoid": PREFERENCE_SIGMOID, "hinge": PREFERENCE_HINGE, "squared": PREFERENCE_SQUARED}
 _WEIGHT_DTYPES = {**_DTYPES, torch.float8_e4m3fn: DTYPE_E4M3}
+_WEIGHTS = tuple(_WEIGHT_DTYPES)
 _I32 = (torch.int32,)
+_F32 = (torch.float32,)
 _BF16_F32 = (torch.bfloat16, torch.float32)
 
 
@@ -128,12 +131,15 @@ def _lib() -> ctypes.CDLL:
         L.lmhead_preference_loss_workspace_size.argtypes = [F]
         L.lmhead_preference_loss_fwd.argtypes = [F] + [vp] * 8 + [sz, vp]
         L.lmhead_preference_loss_bwd.argtypes = [F] + [vp] * 6
-        L.lmhead_adamw_step.argtypes = [A, T, i64, vp]
+        L.lmhead_adamw_step.argtypes = [A, T, i64, vp, vp]
+        L.lmhead_adamw_table_size.argtypes = [i64]
+        L.lmhead_adamw_table.argtypes = [T, i64, vp, sz]
         for f in (L.lmhead_embedding_bwd_workspace_size, L.lmhead_policy_loss_workspace_size,
-                  L.lmhead_preference_loss_workspace_size):
+                  L.lmhead_preference_loss_workspace_size, L.lmhead_adamw_table_size):
             f.restype = sz
         for f in (L.lmhead_embedding_fwd, L.lmhead_embedding_bwd, L.lmhead_policy_loss_fwd, L.lmhead_policy_loss_bwd,
-                  L.lmhead_preference_loss_fwd, L.lmhead_preference_loss_bwd, L.lmhead_adamw_step):
+                  L.lmhead_preference_loss_fwd, L.lmhead_preference_loss_bwd, L.lmhead_adamw_step,
+                  L.lmhead_adamw_table):
             f.restype = ctypes.c_int
         _ready = True
     return L
@@ -188,9 +194,18 @@ def lmhead_preference_loss_bwd(p, grad, coef, targets, cu_seqlens, dlogp, stream
                                              _p(dlogp), _stream(stream))
 
 
-def lmhead_adamw_step(p, tensors, count, stream=None) -> int:
+def lmhead_adamw_step(p, tensors, count, table, stream=None) -> int:
     """tensors: a ctypes array of lmhead_adamw_tensor (host), or None."""
-    return _lib().lmhead_adamw_step(ctypes.byref(p), tensors, count, _stream(stream))
+    return _lib().lmhead_adamw_step(ctypes.byref(p), tensors, count, _p(table), _stream(stream))
+
+
+def lmhead_adamw_table_size(count) -> int:
+    return int(_lib().lmhead_adamw_table_size(count))
+
+
+def lmhead_adamw_table(tensors, count, table, table_bytes) -> int:
+    """table: a tensor in host memory, or its address."""
+    return _lib().lmhead_adamw_table(tensors, count, _p(table), table_bytes)
 
 
 # --------------------------------------------------------------- embedding
@@ -203,7 +218,7 @@ def embedding_forward(ids, weight, scale: float = 1.0, weight_scale=None, out_dt
     weight_scale (quantize_fp8 with block_rows 128). out_dtype: the weight's
     (bf16 for e4m3) unless given. ws: 256 bytes, to read the error word."""
     _check_gpu("ids", ids, _I32, (None,))
-    _check_gpu("weight", weight, tuple(_WEIGHT_DTYPES), (None, None), ids.device)
+    _check_gpu("weight", weight, _WEIGHTS, (None, None), ids.device)
     n = ids.shape[0]
     vocab, hidden = weight.shape
     if (weight_scale is not None) != (weight.dtype == torch.float8_e4m3fn):
@@ -281,22 +296,56 @@ class PolicyOutputs(NamedTuple):
     weights: torch.Tensor   # fp32 [max(sequences, 1)], for the backward
 
 
-def _check_tokens(logp, targets, cu_seqlens, n=None):
-    _check_gpu("logp", logp, (torch.float32,), (n,))
+def _check_vector(name, t, dtypes, n, like):
+    """A contiguous [n] of one dtype on the device of `like`; n None: any size."""
+    # half the time of the general check, which says what is wrong
+    if isinstance(t, torch.Tensor) and t.dtype is dtypes[0] and t.get_device() == like.get_device() and t.is_cuda and \
+            t.dim() == 1 and (n is None or t.shape[0] == n) and t.is_contiguous():
+        return
+    _check_gpu(name, t, dtypes, (n,), like.device)
+
+
+def _check_tokens(logp, targets, cu_seqlens):
+    """(tokens, sequences or 0)."""
+    _check_gpu("logp", logp, _F32, (None,))
+    n = logp.shape[0]
     if targets is not None:
-        _check_gpu("targets", targets, _I32, (logp.shape[0],), logp.device)
-    if cu_seqlens is not None:
-        _check_gpu("cu_seqlens", cu_seqlens, _I32, (None,), logp.device)
-        if cu_seqlens.shape[0] < 2:
-            raise ValueError("cu_seqlens must be int32 [sequences + 1], at least one sequence")
+        _check_vector("targets", targets, _I32, n, logp)
+    if cu_seqlens is None:
+        return n, 0
+    _check_vector("cu_seqlens", cu_seqlens, _I32, None, logp)
+    if cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be int32 [sequences + 1], at least one sequence")
+    return n, cu_seqlens.shape[0] - 1
+
+
+def _outputs(entry, p, nbytes, pointers, ws, floats, like):
+    """(workspace, fp32 [floats] of outputs). A workspace of no more than a tile's
+    size stands in the outputs' own allocation."""
+    if ws is None and 0 < nbytes <= 4096:
+        both = torch.empty(nbytes // 4 + floats, dtype=torch.float32, device=like.device)
+        return both, both[nbytes // 4:]
+    ws = _workspace(ws, nbytes, like.device, entry, p, pointers)
+    return ws, torch.empty(floats, dtype=torch.float32, device=like.device)
+
+
+# a problem and its workspace's size, by its numbers alone
+@functools.lru_cache(maxsize=64)
+def _policy_sizes(*numbers):
+    p = lmhead_policy_problem(*numbers, 0)
+    return p, lmhead_policy_loss_workspace_size(p)
+
+
+@functools.lru_cache(maxsize=64)
+def _preference_sizes(*numbers):
+    p = lmhead_preference_problem(*numbers)
+    return p, lmhead_preference_loss_workspace_size(p)
 
 
 def _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
                     kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence):
-    _check_tokens(logp, targets, cu_seqlens)
-    n = logp.shape[0]
-    sequences = cu_seqlens.shape[0] - 1 if cu_seqlens is not None else 0
-    _check_gpu("advantage", advantage, (torch.float32,), (None,), logp.device)
+    n, sequences = _check_tokens(logp, targets, cu_seqlens)
+    _check_vector("advantage", advantage, _F32, None, logp)
     per_sequence = advantage_per_sequence
     if per_sequence is None:
         if sequences == n and n > 1:
@@ -304,14 +353,16 @@ def _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, cl
         per_sequence = advantage.shape[0] != n
     if (per_sequence and sequences == 0) or advantage.shape[0] != (sequences if per_sequence else n):
         raise ValueError("advantage must be float32 [n], or [sequences] with cu_seqlens")
-    for name, t in (("old_logp", old_logp), ("ref_logp", ref_logp)):
-        _check_f32(name, t, (n,), logp.device)
+    if old_logp is not None:
+        _check_vector("old_logp", old_logp, _F32, n, logp)
+    if ref_logp is not None:
+        _check_vector("ref_logp", ref_logp, _F32, n, logp)
     if kl_kind not in _KL:
         raise ValueError("kl_kind must be 'k1', 'k2' or 'k3'")
     if reduction not in _REDUCE:
         raise ValueError("reduction must be 'mean', 'sum' or 'sequence_mean'")
-    return lmhead_policy_problem(n, sequences, num_valid, clip_low, clip_high, dual_clip, kl_weight, _KL[kl_kind],
-                                 _REDUCE[reduction], int(per_sequence), 0)
+    return _policy_sizes(n, sequences, num_valid, clip_low, clip_high, dual_clip, kl_weight, _KL[kl_kind],
+                         _REDUCE[reduction], int(per_sequence))
 
 
 @_on_device_of(0)
@@ -323,13 +374,12 @@ def policy_loss_forward(logp, advantage, old_logp=None, ref_logp=None, targets=N
     [n] (logprob's); advantage fp32 [n], or [sequences] with cu_seqlens (int32
     [sequences + 1]), told apart by its length unless advantage_per_sequence says
     which; targets int32 [n], negative: the token does not count."""
-    p = _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
-                        kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence)
-    ws = _workspace(ws, lmhead_policy_loss_workspace_size(p), logp.device, lmhead_policy_loss_fwd, p, 10)
-    out = torch.empty(5 + max(p.sequences, 1), dtype=torch.float32, device=logp.device)
+    p, nbytes = _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
+                                kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence)
+    ws, out = _outputs(lmhead_policy_loss_fwd, p, nbytes, 10, ws, 5 + max(p.sequences, 1), logp)
     loss, stats, weights = out[0], out[1:5], out[5:]
     _ok(lmhead_policy_loss_fwd(p, logp, old_logp, ref_logp, advantage, targets, cu_seqlens, loss, stats, weights, ws,
-                               ws.numel()), "lmhead_policy_loss_fwd")
+                               ws.numel() * ws.element_size()), "lmhead_policy_loss_fwd")
     return PolicyOutputs(loss, stats, weights)
 
 
@@ -340,10 +390,10 @@ def policy_loss_backward(grad, weights, logp, advantage, old_logp=None, ref_logp
                          advantage_per_sequence: Optional[bool] = None):
     """dlogp fp32 [n]. grad: fp32 [1] or []; weights: the forward's; the rest as
     given to the forward."""
-    p = _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
-                        kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence)
+    p, _ = _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
+                           kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence)
     _check_scalar("grad", grad, torch.float32, logp.device)
-    _check_f32("weights", weights, (max(p.sequences, 1),), logp.device, required=True)
+    _check_vector("weights", weights, _F32, max(p.sequences, 1), logp)
     dlogp = torch.empty_like(logp)
     _ok(lmhead_policy_loss_bwd(p, grad, weights, logp, old_logp, ref_logp, advantage, targets, cu_seqlens, dlogp),
         "lmhead_policy_loss_bwd")
@@ -398,18 +448,18 @@ def preference_loss_forward(logp, cu_seqlens, ref_logp=None, targets=None, kind:
                             num_pairs: int = -1, ws: Optional[torch.Tensor] = None) -> PreferenceOutputs:
     """Loss of pairs of packed answers, the chosen ones first; see
     lmhead_preference_loss_fwd. cu_seqlens int32 [2 pairs + 1]."""
-    _check_tokens(logp, targets, cu_seqlens)
-    n = logp.shape[0]
-    _check_f32("ref_logp", ref_logp, (n,), logp.device)
+    n, _ = _check_tokens(logp, targets, cu_seqlens)
+    if ref_logp is not None:
+        _check_vector("ref_logp", ref_logp, _F32, n, logp)
     pairs = _pairs(cu_seqlens)
     if kind not in _PREFERENCE:
         raise ValueError("kind must be 'sigmoid', 'hinge' or 'squared'")
-    p = lmhead_preference_problem(n, pairs, num_pairs, beta, margin, label_smoothing, _PREFERENCE[kind], int(bool(average)))
-    ws = _workspace(ws, lmhead_preference_loss_workspace_size(p), logp.device, lmhead_preference_loss_fwd, p, 8)
-    out = torch.empty(1 + 4 * pairs, dtype=torch.float32, device=logp.device)
+    p, nbytes = _preference_sizes(n, pairs, num_pairs, beta, margin, label_smoothing, _PREFERENCE[kind],
+                                  int(bool(average)))
+    ws, out = _outputs(lmhead_preference_loss_fwd, p, nbytes, 8, ws, 1 + 4 * pairs, logp)
     loss, rewards, coef = out[0], out[1:1 + 2 * pairs], out[1 + 2 * pairs:]
-    _ok(lmhead_preference_loss_fwd(p, logp, ref_logp, targets, cu_seqlens, loss, rewards, coef, ws, ws.numel()),
-        "lmhead_preference_loss_fwd")
+    _ok(lmhead_preference_loss_fwd(p, logp, ref_logp, targets, cu_seqlens, loss, rewards, coef, ws,
+                                   ws.numel() * ws.element_size()), "lmhead_preference_loss_fwd")
     return PreferenceOutputs(loss, rewards, coef)
 
 
@@ -425,11 +475,11 @@ def preference_loss_backward(grad, coef, n: int, cu_seqlens, targets=None):
     """dlogp fp32 [n]. grad: fp32 [1] or []; coef: the forward's."""
     _check_scalar("grad", grad, torch.float32)
     pairs = _pairs(cu_seqlens)
-    _check_gpu("cu_seqlens", cu_seqlens, _I32, (None,), grad.device)
-    _check_f32("coef", coef, (2 * pairs,), grad.device, required=True)
+    _check_vector("cu_seqlens", cu_seqlens, _I32, None, grad)
+    _check_vector("coef", coef, _F32, 2 * pairs, grad)
     if targets is not None:
-        _check_gpu("targets", targets, _I32, (n,), grad.device)
-    p = lmhead_preference_problem(n, pairs, -1, 1.0, 0.0, 0.0, PREFERENCE_SIGMOID, 0)
+        _check_vector("targets", targets, _I32, n, grad)
+    p, _ = _preference_sizes(n, pairs, -1, 1.0, 0.0, 0.0, PREFERENCE_SIGMOID, 0)
     dlogp = torch.empty(n, dtype=torch.float32, device=grad.device)
     _ok(lmhead_preference_loss_bwd(p, grad, coef, targets, cu_seqlens, dlogp), "lmhead_preference_loss_bwd")
     return dlogp
@@ -490,8 +540,17 @@ class AdamWPlan:
     the storages that the tensors had then: a parameter or gradient that is given
     another storage needs another plan."""
 
-    def __init__(self, device, table, count, keep):
-        self.device, self.table, self.count, self.keep = device, table, count, keep
+    def __init__(self, device, tensors, keep):
+        self.device, self.tensors, self.count, self.keep = device, tensors, len(tensors), keep
+        self.table = None
+        if self.count > 48:   # more than a launch takes as an argument
+            table = torch.empty(lmhead_adamw_table_size(self.count), dtype=torch.uint8)
+            st = lmhead_adamw_table(tensors, self.count, table, table.numel())
+            if st == LMHEAD_ERR_SHAPE:   # too large for one launch: without
+                return
+            _ok(st, "lmhead_adamw_table")
+            self.table = table.to(device)
+            torch.cuda.synchronize(device)   # steps may run on any stream
 
 
 def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[AdamWState],
@@ -532,7 +591,7 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     spans.sort()
     if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
         raise ValueError("two tensors of the plan share memory")
-    return AdamWPlan(dev, table, len(params), keep)
+    return AdamWPlan(dev, table, keep)
 
 
 def adamw_step(plan: AdamWPlan, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -560,7 +619,7 @@ def adamw_step(plan: AdamWPlan, step, lr, beta1: float = 0.9, beta2: float = 0.9
         _check_scalar("grad_scale", grad_scale, torch.float32, plan.device)
         p.grad_scale = grad_scale.data_ptr()
     if plan.device.index == torch.cuda.current_device():
-        _ok(lmhead_adamw_step(p, plan.table, plan.count), "lmhead_adamw_step")
+        _ok(lmhead_adamw_step(p, plan.tensors, plan.count, plan.table), "lmhead_adamw_step")
         return
     with torch.cuda.device(plan.device):
-        _ok(lmhead_adamw_step(p, plan.table, plan.count), "lmhead_adamw_step")
+        _ok(lmhead_adamw_step(p, plan.tensors, plan.count, plan.table), "lmhead_adamw_step")

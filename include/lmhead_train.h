@@ -317,14 +317,26 @@ typedef struct lmhead_adamw {
  * rounded after that, over blocks of 128 consecutive elements of a tensor as
  * lmhead_quantize_fp8 rounds, except that a sqrt(v') > 0 becomes no zero
  * (at least 2^-9 of its scale): a vanishing denominator would let m' loose.
+ * The root of a v' below 2^-126 is zero.
  * States of zeros start (any finite scales).
  * Stochastic: with y = value / scale and u the upper 16 of 20 random bits, as a
  * fraction, |y| + u step(y) is cut to the code below, step(y) being the distance
  * of the codes around y.
- *   tensors  host, [count]; count 0 .. 2^20. numel 0 .. 2^35.
- * At most 48 tensors share a launch.
+ *   tensors  host, [count]; count 0 .. 2^20. numel 0 .. 2^35 - 2^24.
+ *   table    device, 8-byte aligned, or NULL: what lmhead_adamw_table wrote for
+ *            these tensors, copied there. With it any number of tensors shares one
+ *            launch (up to 16,777,215 workgroups of 2048 elements, or 4096 in 8
+ *            bits), without it 48 do; 48 or fewer need none. Bits do not differ.
  */
-int lmhead_adamw_step(const lmhead_adamw* p, const lmhead_adamw_tensor* tensors, int64_t count, void* stream);
+int lmhead_adamw_step(const lmhead_adamw* p, const lmhead_adamw_tensor* tensors, int64_t count, const void* table,
+                      void* stream);
+
+/* Bytes of a table of count tensors (0 for a count out of range), and the table
+ * itself, written to host memory (8-byte aligned). Pure host functions. A table
+ * holds the tensors' addresses: other addresses need another table. A shape
+ * error where the tensors are too large for one launch. */
+size_t lmhead_adamw_table_size(int64_t count);
+int lmhead_adamw_table(const lmhead_adamw_tensor* tensors, int64_t count, void* table, size_t table_bytes);
 
 #ifdef __cplusplus
 }

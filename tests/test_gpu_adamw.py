@@ -155,6 +155,26 @@ def test_mixed_tensors_over_several_launches():
     run(items, 7, HYPER)
 
 
+def test_a_table_gives_the_same_bits():
+    """49 to 200 tensors: one launch from the table, or several without; at random rounding too."""
+    rng = np.random.default_rng(12)
+    for count in (49, 64, 65, 200):
+        sizes = [int(rng.integers(0, 7000)) if i % 7 else 0 for i in range(count)]
+        outs = []
+        for table in (True, False):
+            g = torch.Generator(device="cuda")
+            g.manual_seed(count)
+            items = [make(g, (n,), BF, BF, E8 if i % 3 else F32, False) for i, n in enumerate(sizes)]
+            plan = lm.adamw_plan(*[[i[k] for i in items] for k in range(3)])
+            assert plan.table is not None
+            if not table:
+                plan.table = None
+            lm.adamw_step(plan, 3, 0.01)
+            lm.adamw_step(plan, 4, 0.01, seed=5)
+            outs.append([t.float() for i in items for t in (i[0], *i[2]) if t is not None])
+        assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 def test_one_tensor_of_many_chunks():
     g = torch.Generator(device="cuda")
     g.manual_seed(5)

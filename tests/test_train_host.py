@@ -25,7 +25,7 @@ NAN, INF = float("nan"), float("inf")
 def test_library_exports_the_header():
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "lmhead_train.h")).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(lmhead_[a-z_0-9]+)\s*\(", text)))
-    assert names == ["lmhead_adamw_step", "lmhead_embedding_bwd", "lmhead_embedding_bwd_workspace_size",
+    assert names == ["lmhead_adamw_step", "lmhead_adamw_table", "lmhead_adamw_table_size", "lmhead_embedding_bwd", "lmhead_embedding_bwd_workspace_size",
                      "lmhead_embedding_fwd", "lmhead_policy_loss_bwd", "lmhead_policy_loss_fwd",
                      "lmhead_policy_loss_workspace_size", "lmhead_preference_loss_bwd",
                      "lmhead_preference_loss_fwd", "lmhead_preference_loss_workspace_size"]
@@ -179,7 +179,7 @@ def test_adamw_refusals():
     f, F = lm.lmhead_adamw_step, FAKE
 
     def call(p, *tensors):
-        return f(p, (lm.lmhead_adamw_tensor * len(tensors))(*tensors), len(tensors), 0)
+        return f(p, (lm.lmhead_adamw_tensor * len(tensors))(*tensors), len(tensors), None, 0)
     for bad in (dict(lr=NAN), dict(lr=INF), dict(weight_decay=-0.1), dict(weight_decay=NAN), dict(beta1=1.0),
                 dict(beta1=-0.1), dict(beta1=NAN), dict(beta2=1.0), dict(beta2=1 - 1e-12), dict(beta2=NAN), dict(eps=0.0),
                 dict(eps=1e-45), dict(eps=NAN), dict(eps=INF), dict(step=0), dict(step=-1),
@@ -187,19 +187,37 @@ def test_adamw_refusals():
         assert call(adam(**bad), tensor()) == A, bad
     for name in ("device_step", "device_lr", "grad_scale"):
         assert call(adam(**{name: F + 2}), tensor()) == AL, name
-    assert f(adam(), None, 1, 0) == A and f(adam(), None, -1, 0) == S and f(adam(), None, (1 << 20) + 1, 0) == S
+    assert f(adam(), None, 1, None, 0) == A and f(adam(), None, -1, None, 0) == S and \
+        f(adam(), None, (1 << 20) + 1, None, 0) == S
+    assert f(adam(), (lm.lmhead_adamw_tensor * 1)(tensor()), 1, F + 4, 0) == AL
     e8 = dict(state_dtype=2, exp_avg_scale=F, exp_avg_sq_scale=F)
     good = tensor()
     for bad in (dict(param=None), dict(grad=None), dict(exp_avg=None), dict(exp_avg_sq=None), dict(param_dtype=2),
                 dict(grad_dtype=2), dict(state_dtype=0), dict(state_dtype=3), dict(reserved=1), dict(exp_avg_scale=F),
                 dict(exp_avg_sq_scale=F), dict(e8, exp_avg_scale=None), dict(e8, exp_avg_sq_scale=None)):
         assert call(adam(), good, tensor(**bad)) == A, bad
-    for bad in (dict(numel=-1), dict(numel=(1 << 35) + 1)):
+    for bad in (dict(numel=-1), dict(numel=1 << 35)):
         assert call(adam(), good, tensor(**bad)) == S, bad
     for bad in (dict(param=F + 1), dict(grad=F + 1), dict(param=F + 2, param_dtype=1), dict(grad=F + 2, grad_dtype=1),
                 dict(exp_avg=F + 2), dict(exp_avg_sq=F + 2), dict(copy=F + 1), dict(e8, exp_avg_scale=F + 2),
                 dict(e8, exp_avg_sq_scale=F + 2)):
         assert call(adam(), good, tensor(**bad)) == AL, bad
+
+
+def test_adamw_table():
+    f, size = lm.lmhead_adamw_table, lm.lmhead_adamw_table_size
+    assert size(0) == 0 and size(-1) == 0 and size((1 << 20) + 1) == 0
+    assert size(1) == 64 + 72 and size(16) == 64 + 16 * 72 and size(17) == 128 + 17 * 72
+    e8 = dict(state_dtype=2, exp_avg_scale=FAKE, exp_avg_sq_scale=FAKE)
+    tensors = (lm.lmhead_adamw_tensor * 4)(tensor(numel=2049), tensor(numel=0), tensor(numel=4097, **e8), tensor())
+    buf = torch.zeros(size(4), dtype=torch.uint8)
+    assert f(tensors, 4, buf, size(4)) == lm.LMHEAD_OK
+    assert buf[:16].view(torch.int32).tolist() == [0, 2, 2, 4]   # chunks of 2048, or of 4096 in 8 bits
+    assert f(tensors, 4, buf, size(4) - 1) == W and f(tensors, 4, None, BIG) == A and f(None, 4, buf, BIG) == A
+    assert f(tensors, 4, buf.data_ptr() + 4, BIG) == AL and f(None, -1, None, 0) == S
+    assert f((lm.lmhead_adamw_tensor * 1)(tensor(param=None)), 1, buf, BIG) == A
+    big = (lm.lmhead_adamw_tensor * 2)(*[tensor(numel=(1 << 35) - (1 << 24))] * 2)
+    assert f(big, 2, buf, BIG) == S and f(big, 1, buf, BIG) == lm.LMHEAD_OK
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-device path")
@@ -214,8 +232,8 @@ def test_no_device():
     assert lm.lmhead_preference_loss_fwd(pref(), F, None, None, F, F, None, F, F, BIG, 0) == D
     assert lm.lmhead_preference_loss_bwd(pref(), F, F, F, F, F, 0) == D
     one = (lm.lmhead_adamw_tensor * 1)(tensor(exp_avg=F + 4, param=F + 2))
-    assert lm.lmhead_adamw_step(adam(), one, 1, 0) == D
-    assert lm.lmhead_adamw_step(adam(), None, 0, 0) == D
+    assert lm.lmhead_adamw_step(adam(), one, 1, None, 0) == D
+    assert lm.lmhead_adamw_step(adam(), None, 0, FAKE, 0) == D
 
 
 def test_helpers_refuse():

@@ -21,17 +21,14 @@ namespace lmhead {
 
 namespace {
 
-typedef uint32_t words4 __attribute__((ext_vector_type(4)));
-
 // lane's eight values at element e; zeros past the end. STREAM: past the caches
 template <bool F32, bool STREAM>
 __device__ __forceinline__ V8 fetch(const void* p, int64_t e, int64_t numel, bool wide) {
     if (wide && e + 8 <= numel) {
-        if (!STREAM) return load8<F32>(p, e >> 3);
         Raw8<F32> r;
 #pragma unroll
         for (int k = 0; k < (F32 ? 2 : 1); ++k) {
-            const words4 w = __builtin_nontemporal_load(reinterpret_cast<const words4*>(p) + (F32 ? 2 : 1) * (e >> 3) + k);
+            const Words4 w = load_words<STREAM>(p, (F32 ? 2 : 1) * (e >> 3) + k);
             r.w[k] = make_uint4(w[0], w[1], w[2], w[3]);
         }
         return to8<F32>(r);
@@ -47,20 +44,7 @@ __device__ __forceinline__ V8 fetch(const void* p, int64_t e, int64_t numel, boo
 template <bool F32, bool STREAM>
 __device__ __forceinline__ void put(void* p, int64_t e, int64_t numel, bool wide, const V8& f) {
     if (wide && e + 8 <= numel) {
-        if (!STREAM) {
-            store8<F32>(p, e >> 3, f);
-        } else if (F32) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                words4 w;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) w[c] = __builtin_bit_cast(uint32_t, f.v[4 * k + c]);
-                __builtin_nontemporal_store(w, reinterpret_cast<words4*>(p) + 2 * (e >> 3) + k);
-            }
-        } else {
-            const uint4 w = to_bf16x8(f);
-            __builtin_nontemporal_store(words4{w.x, w.y, w.z, w.w}, reinterpret_cast<words4*>(p) + (e >> 3));
-        }
+        store8<F32, STREAM>(p, e >> 3, f);
         return;
     }
 #pragma unroll

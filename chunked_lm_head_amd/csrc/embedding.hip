@@ -10,7 +10,7 @@
 //      reads all n ids, twice: once to count, once to place. It needs nothing
 //      from the others: its first place is the number of ids of lower buckets,
 //      which it counts along. Where the whole gradient is written, further
-//      workgroups of this launch write its zeros meanwhile, 16 KB each.
+//      workgroups of this launch write its zeros meanwhile, 8 KB each.
 //   2. sum: a run of tokens of one id is cut into pieces of R (16, or 64 above
 //      16,384 tokens); 16 .. 64 lanes add a piece over up to 1024 columns. A run
 //      of one piece is finished there, longer ones leave fp32 partial sums.
@@ -26,8 +26,15 @@ namespace {
 // ------------------------------------------------------------------ forward
 
 // A row is taken by 8 .. 64 lanes of a wave (all that its vectors of 8 can
-// use), eight vectors per lane in flight; wider rows in segments (grid y).
-template <int TYPE, bool OUT32>
+// use), four vectors per lane in flight; wider rows in segments (grid y). 16,384
+// rows of 4096 bf16: 37.7 us, eight vectors 41.5, two 45.2. STREAM: the output
+// past the caches, for outputs that they would not hold until the next
+// operator: 28.5 us there, the same 82 us with the norm behind it; 12,288 rows
+// with the norm 63 us, through the caches 60; 4096 rows 25.4 and 24.4.
+constexpr int kVectors = 4;
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+
+template <int TYPE, bool OUT32, bool STREAM>
 __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int log_lanes) {
     const int lanes = 1 << log_lanes, lane = threadIdx.x & 63;
     const int sub = lane & (lanes - 1);
@@ -44,10 +51,10 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int log_lan
             atomicMin(&a.hdr[kHdrErrRow], (int)row);
         }
         const int64_t from = (live ? id : 0) * nv, to = row * nv;
-        V8 f[8];
+        V8 f[kVectors];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int v = sub + (((int)blockIdx.y * 8 + k) << log_lanes);
+        for (int k = 0; k < kVectors; ++k) {
+            const int v = sub + (((int)blockIdx.y * kVectors + k) << log_lanes);
             f[k] = V8{{fill, fill, fill, fill, fill, fill, fill, fill}};
             if (live && v < nv) {
                 if (TYPE == kEmbedE4m3) {
@@ -61,13 +68,13 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int log_lan
             }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int v = sub + (((int)blockIdx.y * 8 + k) << log_lanes);
+        for (int k = 0; k < kVectors; ++k) {
+            const int v = sub + (((int)blockIdx.y * kVectors + k) << log_lanes);
             if (v >= nv) continue;
             if (live)
 #pragma unroll
                 for (int c = 0; c < 8; ++c) f[k].v[c] *= a.scale;
-            store8<OUT32>(a.out, to + v, f[k]);
+            store8<OUT32, STREAM>(a.out, to + v, f[k]);
         }
     }
 }
@@ -75,11 +82,9 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int log_lan
 // ----------------------------------------------------------------- backward
 
 constexpr int kLocals = 512;       // ids of one bucket
-constexpr int kWaves = 16;         // of a grouping workgroup
 constexpr int kLogPiece = 4, kLogPieceMany = 6;
 constexpr int64_t kManyTokens = 16384;
 constexpr int64_t kMaxFill = int64_t(1) << 21;   // workgroups that write zeros
-constexpr int kHeld = 8;          // ids per lane of a grouping wave in registers
 constexpr int kJoinWaves = 4;
 constexpr int kJoinCols = 256;
 
@@ -104,7 +109,13 @@ struct GroupArgs {
     int64_t vectors;  // 16-byte vectors of it
 };
 
-__global__ __launch_bounds__(1024, 8) void group_tokens_kernel(GroupArgs a) {
+// 16 waves with 8 ids per lane in registers; 8 waves with 16 where zeros are
+// written too, whose workgroups do best at 512 threads (16,384 tokens, 152 k x 4096
+// bf16: 258 us for all three launches, with 1024 threads 270; added to fp32
+// instead 101 and 94).
+template <int kWaves, int kHeld>
+__global__ __launch_bounds__(64 * kWaves, kWaves / 2) void group_tokens_kernel(GroupArgs a) {
+    constexpr int kGroupThreads = 64 * kWaves;
     // places of (id, wave): an id's tokens stand in the order of the waves' segments
     __shared__ int place[kLocals * kWaves];
     __shared__ int total[kLocals], start[kLocals];
@@ -112,12 +123,13 @@ __global__ __launch_bounds__(1024, 8) void group_tokens_kernel(GroupArgs a) {
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
     if ((int)blockIdx.x >> a.log_buckets != 0) {
         const unsigned first = 1u << a.log_buckets;
-        for (int64_t v = (int64_t)(blockIdx.x - first) * 1024 + t; v < a.vectors; v += (int64_t)(gridDim.x - first) * 1024)
+        for (int64_t v = (int64_t)(blockIdx.x - first) * kGroupThreads + t; v < a.vectors;
+             v += (int64_t)(gridDim.x - first) * kGroupThreads)
             a.zeros[v] = make_uint4(0u, 0u, 0u, 0u);
         return;
     }
     const int bucket = blockIdx.x, mask = (1 << a.log_buckets) - 1;
-    for (int i = t; i < kLocals * kWaves; i += 1024) place[i] = 0;
+    for (int i = t; i < kLocals * kWaves; i += kGroupThreads) place[i] = 0;
     __syncthreads();
     const int64_t segment = (a.n + kWaves * 64 - 1) / (kWaves * 64) * 64;
     const int64_t from = wave * segment, to = from + segment < a.n ? from + segment : a.n;
@@ -156,15 +168,17 @@ __global__ __launch_bounds__(1024, 8) void group_tokens_kernel(GroupArgs a) {
         wave_bad[wave] = bad;
     }
     __syncthreads();
-    // exclusive sums over (id, wave): eight entries per thread, two threads per id
+    // exclusive sums over (id, wave): eight entries per thread, kWaves / 8 threads per id
     int own[8], sum = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         own[k] = place[t * 8 + k];
         sum += own[k];
     }
-    const int both = sum + __shfl_xor(sum, 1);
-    if ((t & 1) == 0) total[t >> 1] = both;
+    const int whole = kWaves == 16 ? sum + __shfl_xor(sum, 1) : sum;
+    const bool leads = kWaves == 8 || (t & 1) == 0;
+    const int local = kWaves == 16 ? t >> 1 : t;
+    if (leads) total[local] = whole;
     int run = sum;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
@@ -180,7 +194,7 @@ __global__ __launch_bounds__(1024, 8) void group_tokens_kernel(GroupArgs a) {
         all += wave_sum[w];
     }
     run += base - sum;
-    if ((t & 1) == 0) start[t >> 1] = run;
+    if (leads) start[local] = run;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         place[t * 8 + k] = run;
@@ -401,21 +415,29 @@ void sum_and_join(SumArgs a, hipStream_t s) {
 
 }  // namespace
 
-void launch_embedding(const EmbedArgs& a, hipStream_t s) {
+namespace {
+template <int TYPE, bool OUT32>
+void embedding(const EmbedArgs& a, hipStream_t s) {
     const int nv = a.hidden >> 3;
     int log_lanes = 3;
     while (log_lanes < 6 && (1 << log_lanes) < nv) ++log_lanes;
-    const dim3 grid((unsigned)grid_1d(a.n, 256 >> log_lanes, 1 << 20), (unsigned)cdiv(nv, 8 << log_lanes));
+    const dim3 grid((unsigned)grid_1d(a.n, 256 >> log_lanes, 1 << 20), (unsigned)cdiv(nv, kVectors << log_lanes));
+    if (a.n * a.hidden * (OUT32 ? 4 : 2) >= kStreamBytes) embedding_kernel<TYPE, OUT32, true><<<grid, 256, 0, s>>>(a, log_lanes);
+    else embedding_kernel<TYPE, OUT32, false><<<grid, 256, 0, s>>>(a, log_lanes);
+}
+}  // namespace
+
+void launch_embedding(const EmbedArgs& a, hipStream_t s) {
     if (a.hdr != nullptr) init_header_kernel<<<1, 64, 0, s>>>(a.hdr);
     if (a.weight_type == kEmbedE4m3) {
-        if (a.out_f32) embedding_kernel<kEmbedE4m3, true><<<grid, 256, 0, s>>>(a, log_lanes);
-        else embedding_kernel<kEmbedE4m3, false><<<grid, 256, 0, s>>>(a, log_lanes);
+        if (a.out_f32) embedding<kEmbedE4m3, true>(a, s);
+        else embedding<kEmbedE4m3, false>(a, s);
     } else if (a.weight_type == kEmbedF32) {
-        if (a.out_f32) embedding_kernel<kEmbedF32, true><<<grid, 256, 0, s>>>(a, log_lanes);
-        else embedding_kernel<kEmbedF32, false><<<grid, 256, 0, s>>>(a, log_lanes);
+        if (a.out_f32) embedding<kEmbedF32, true>(a, s);
+        else embedding<kEmbedF32, false>(a, s);
     } else {
-        if (a.out_f32) embedding_kernel<kEmbedBf16, true><<<grid, 256, 0, s>>>(a, log_lanes);
-        else embedding_kernel<kEmbedBf16, false><<<grid, 256, 0, s>>>(a, log_lanes);
+        if (a.out_f32) embedding<kEmbedBf16, true>(a, s);
+        else embedding<kEmbedBf16, false>(a, s);
     }
 }
 
@@ -457,8 +479,10 @@ void launch_embedding_bwd(const EmbedBwdArgs& a, void* workspace, hipStream_t s)
     g.items = (int2*)(w + p.items);
     g.zeros = (uint4*)a.dweight;
     g.vectors = a.accumulate ? 0 : a.vocab * (a.hidden * (a.dweight_f32 ? 4 : 2) / 16);
-    const int64_t fills = cdiv(g.vectors, 1024);
-    group_tokens_kernel<<<(1u << g.log_buckets) + (unsigned)(fills < kMaxFill ? fills : kMaxFill), 1024, 0, s>>>(g);
+    const unsigned buckets = 1u << g.log_buckets;
+    const int64_t fills = cdiv(g.vectors, 512);
+    if (a.accumulate) group_tokens_kernel<16, 8><<<buckets, 1024, 0, s>>>(g);
+    else group_tokens_kernel<8, 16><<<buckets + (unsigned)(fills < kMaxFill ? fills : kMaxFill), 512, 0, s>>>(g);
     if (a.n == 0) return;
     SumArgs u;
     u.e = a;

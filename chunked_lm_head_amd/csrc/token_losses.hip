@@ -10,8 +10,9 @@
 // 12 to 24 bytes per token and direction and few operations: small batches are
 // bound by launches and by the latency of loads that wait for one another,
 // large ones by memory. So up to 8192 tokens are one launch of one workgroup;
-// above, tiles of 1024 tokens leave 64-bit partial sums and a second launch (a
-// third for the sequence mean) adds them in order. A tile's tokens are loaded
+// above, tiles of 1024 tokens leave 64-bit partial sums and a second launch adds
+// them in order (over more sequences or tiles than a workgroup can take at once, a
+// third). A tile's tokens are loaded
 // before its sequences are looked up, and all its sums cross the workgroup
 // behind one barrier.
 //
@@ -265,18 +266,21 @@ __device__ __forceinline__ Part part_of(const Tokens& t, const Tile& tile, int64
     return p;
 }
 
-// The same over the tiles that a sequence touches, from their slots.
-__device__ __forceinline__ Part part_of(const Tokens& t, int64_t q, const Part* slots) {
+// The same over the tiles that a sequence touches, from their slots, by `lanes`
+// (a power of two) neighbours of a wave.
+__device__ __forceinline__ Part part_of(const Tokens& t, int64_t q, const Part* slots, int lanes) {
     const int64_t from = border(t, q), to = border(t, q + 1);
     Part p = {0.0, 0.0};
     if (from < to)
-        for (int64_t tile = from / kTileTokens + (threadIdx.x & 63); tile <= (to - 1) / kTileTokens; tile += 64) {
+        for (int64_t tile = from / kTileTokens + (threadIdx.x & (lanes - 1)); tile <= (to - 1) / kTileTokens; tile += lanes) {
             const Part o = slots[tile + q];
             p.sum += o.sum;
             p.count += o.count;
         }
-    p.sum = wave_sum(p.sum);
-    p.count = wave_sum(p.count);
+    for (int m = 1; m < lanes; m <<= 1) {
+        p.sum += __shfl_xor(p.sum, m);
+        p.count += __shfl_xor(p.count, m);
+    }
     return p;
 }
 
@@ -286,9 +290,9 @@ __device__ __forceinline__ double share(int64_t given, double counted) {
 }
 
 // A sequence's weight in the sequence mean; returns its mean times its share.
-__device__ __forceinline__ double weigh(const PolicyArgs& a, int64_t q, const Part& p) {
+__device__ __forceinline__ double weigh(const PolicyArgs& a, int64_t q, const Part& p, bool writes) {
     const double w = p.count > 0.0 ? share(a.num_valid, (double)a.t.sequences) / p.count : 0.0;
-    if ((threadIdx.x & 63) == 0) a.weights[q] = (float)w;
+    if (writes) a.weights[q] = (float)w;
     return w > 0.0 ? w * p.sum : 0.0;
 }
 
@@ -320,7 +324,7 @@ __global__ __launch_bounds__(THREADS) void policy_whole_kernel(PolicyArgs a) {
         __syncthreads();
         double means = 0.0;
         for (int64_t q = threadIdx.x >> 6; q < a.t.sequences; q += THREADS / 64)
-            means += weigh(a, q, part_of(a.t, tile, q, kept, counts));
+            means += weigh(a, q, part_of(a.t, tile, q, kept, counts), (threadIdx.x & 63) == 0);
         s[kLoss] = (threadIdx.x & 63) == 0 ? means : 0.0;
     }
     group_sums<6, THREADS>(s, red);
@@ -350,18 +354,25 @@ __global__ __launch_bounds__(kTileThreads) void policy_tiles_kernel(PolicyArgs a
 __global__ __launch_bounds__(kTileThreads) void policy_sequences_kernel(PolicyArgs a, const Part* slots, double* means) {
     const int64_t q = (int64_t)blockIdx.x * (kTileThreads / 64) + (threadIdx.x >> 6);
     if (q >= a.t.sequences) return;
-    const double m = weigh(a, q, part_of(a.t, q, slots));
-    if ((threadIdx.x & 63) == 0) means[q] = m;
+    const bool writes = (threadIdx.x & 63) == 0;
+    const double m = weigh(a, q, part_of(a.t, q, slots, 64), writes);
+    if (writes) means[q] = m;
 }
 
+// lanes: of the sequences' means, where their parts are added here (a thread each, or more)
 __global__ __launch_bounds__(kWholeThreads) void policy_join_kernel(PolicyArgs a, const double* tiles, int64_t count,
-                                                                    const double* means) {
+                                                                    const double* means, const Part* slots, int lanes) {
     __shared__ double red[6 * kWholeThreads / 64];
     double s[6] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
     for (int64_t i = threadIdx.x; i < count; i += kWholeThreads)
 #pragma unroll
         for (int k = 0; k < 6; ++k) s[k] += tiles[k * count + i];
-    if (a.reduction == 2) {
+    if (lanes > 0) {
+        const int64_t q = threadIdx.x / (unsigned)lanes;
+        const bool in = q < a.t.sequences, writes = in && (threadIdx.x & (lanes - 1)) == 0;
+        const double m = weigh(a, in ? q : 0, part_of(a.t, in ? q : 0, slots, lanes), writes);
+        s[kLoss] = writes ? m : 0.0;
+    } else if (a.reduction == 2) {
         s[kLoss] = 0.0;
 #pragma unroll 4
         for (int64_t q = threadIdx.x; q < a.t.sequences; q += kWholeThreads) s[kLoss] += means[q];
@@ -405,7 +416,7 @@ __device__ __forceinline__ void preference_tile(const PreferenceArgs& a, const T
 }
 
 // One pair from its sequences' sums: writes the rewards and coefficients, returns its share of the loss.
-__device__ __forceinline__ double pair_loss(const PreferenceArgs& a, int64_t pair, Part c, Part r) {
+__device__ __forceinline__ double pair_loss(const PreferenceArgs& a, int64_t pair, Part c, Part r, bool writes) {
     const int64_t pairs = a.t.sequences / 2;
     const double one = share(a.num_pairs, (double)pairs);
     const double fc = a.average && c.count > 0.0 ? 1.0 / c.count : 1.0;
@@ -428,7 +439,7 @@ __device__ __forceinline__ double pair_loss(const PreferenceArgs& a, int64_t pai
         loss = d * d;
         slope = 2.0 * d / a.beta;
     }
-    if ((threadIdx.x & 63) == 0) {
+    if (writes) {
         const double k = one > 0.0 ? a.beta * slope * one : 0.0;
         a.coef[pair] = (float)(k * fc);
         a.coef[pairs + pair] = (float)(-k * fr);
@@ -451,7 +462,8 @@ __global__ __launch_bounds__(THREADS) void preference_whole_kernel(PreferenceArg
     const int64_t pairs = a.t.sequences / 2;
     double loss[1] = {0.0};
     for (int64_t j = threadIdx.x >> 6; j < pairs; j += THREADS / 64)
-        loss[0] += pair_loss(a, j, part_of(a.t, tile, j, kept, counts), part_of(a.t, tile, pairs + j, kept, counts));
+        loss[0] += pair_loss(a, j, part_of(a.t, tile, j, kept, counts), part_of(a.t, tile, pairs + j, kept, counts),
+                             (threadIdx.x & 63) == 0);
     if ((threadIdx.x & 63) != 0) loss[0] = 0.0;
     group_sums<1, THREADS>(loss, red);
     if (threadIdx.x == 0) a.loss[0] = (float)loss[0];
@@ -474,8 +486,22 @@ __global__ __launch_bounds__(kTileThreads) void preference_tiles_kernel(Preferen
 __global__ __launch_bounds__(kTileThreads) void preference_pairs_kernel(PreferenceArgs a, const Part* slots, double* each) {
     const int64_t j = (int64_t)blockIdx.x * (kTileThreads / 64) + (threadIdx.x >> 6), pairs = a.t.sequences / 2;
     if (j >= pairs) return;
-    const double l = pair_loss(a, j, part_of(a.t, j, slots), part_of(a.t, pairs + j, slots));
-    if ((threadIdx.x & 63) == 0) each[j] = l;
+    const bool writes = (threadIdx.x & 63) == 0;
+    const double l = pair_loss(a, j, part_of(a.t, j, slots, 64), part_of(a.t, pairs + j, slots, 64), writes);
+    if (writes) each[j] = l;
+}
+
+// Both, where a workgroup has `lanes` threads for each pair.
+__global__ __launch_bounds__(kWholeThreads) void preference_end_kernel(PreferenceArgs a, const Part* slots, int lanes) {
+    __shared__ double red[kWholeThreads / 64];
+    const int64_t j = threadIdx.x / (unsigned)lanes, pairs = a.t.sequences / 2;
+    const bool in = j < pairs, writes = in && (threadIdx.x & (lanes - 1)) == 0;
+    const int64_t pair = in ? j : 0;
+    double loss[1];
+    loss[0] = pair_loss(a, pair, part_of(a.t, pair, slots, lanes), part_of(a.t, pairs + pair, slots, lanes), writes);
+    if (!writes) loss[0] = 0.0;
+    group_sums<1, kWholeThreads>(loss, red);
+    if (threadIdx.x == 0) a.loss[0] = (float)loss[0];
 }
 
 __global__ __launch_bounds__(kWholeThreads) void preference_join_kernel(const double* each, int64_t count, float* loss) {
@@ -509,6 +535,16 @@ __global__ __launch_bounds__(kTileThreads) void preference_bwd_kernel(Tokens t, 
 
 }  // namespace
 
+// Threads that one workgroup has for each of `count` sequences or pairs: a power
+// of two up to 64, or 0 for more than it has threads or for parts that would
+// keep them long (many more tiles than threads).
+static int lanes_for(int64_t count, int64_t tiles) {
+    if (count > kWholeThreads || tiles > 8 * kWholeThreads) return 0;
+    int lanes = 64;
+    while (count * lanes > kWholeThreads) lanes >>= 1;
+    return lanes;
+}
+
 size_t policy_workspace(int64_t n, int64_t sequences, int reduction) {
     if (n <= kWholeTokens) return 256;
     const int64_t tiles = cdiv(n, kTileTokens);
@@ -535,13 +571,12 @@ void launch_policy(const PolicyArgs& a, void* workspace, hipStream_t s) {
     double* sums = (double*)w;
     Part* slots = (Part*)(w + round_up(tiles * 6 * 8, 256));
     double* means = (double*)((char*)slots + round_up((tiles + a.t.sequences) * (int64_t)sizeof(Part), 256));
-    if (seq) {
-        policy_tiles_kernel<true><<<(unsigned)tiles, kTileThreads, 0, s>>>(a, sums, slots);
+    const int lanes = seq ? lanes_for(a.t.sequences, tiles) : 0;
+    if (seq) policy_tiles_kernel<true><<<(unsigned)tiles, kTileThreads, 0, s>>>(a, sums, slots);
+    else policy_tiles_kernel<false><<<(unsigned)tiles, kTileThreads, 0, s>>>(a, sums, nullptr);
+    if (seq && lanes == 0)
         policy_sequences_kernel<<<(unsigned)cdiv(a.t.sequences, kTileThreads / 64), kTileThreads, 0, s>>>(a, slots, means);
-    } else {
-        policy_tiles_kernel<false><<<(unsigned)tiles, kTileThreads, 0, s>>>(a, sums, nullptr);
-    }
-    policy_join_kernel<<<1, kWholeThreads, 0, s>>>(a, sums, tiles, means);
+    policy_join_kernel<<<1, kWholeThreads, 0, s>>>(a, sums, tiles, means, slots, lanes);
 }
 
 void launch_policy_bwd(const PolicyArgs& a, const float* grad, float* dlogp, hipStream_t s) {
@@ -563,6 +598,11 @@ void launch_preference(const PreferenceArgs& a, void* workspace, hipStream_t s) 
     Part* slots = (Part*)workspace;
     double* each = (double*)((char*)workspace + round_up((tiles + a.t.sequences) * (int64_t)sizeof(Part), 256));
     preference_tiles_kernel<<<(unsigned)tiles, kTileThreads, 0, s>>>(a, slots);
+    const int lanes = lanes_for(pairs, tiles);
+    if (lanes > 0) {
+        preference_end_kernel<<<1, kWholeThreads, 0, s>>>(a, slots, lanes);
+        return;
+    }
     preference_pairs_kernel<<<(unsigned)cdiv(pairs, kTileThreads / 64), kTileThreads, 0, s>>>(a, slots, each);
     preference_join_kernel<<<1, kWholeThreads, 0, s>>>(each, pairs, a.loss);
 }

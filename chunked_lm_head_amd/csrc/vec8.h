@@ -76,13 +76,33 @@ __device__ __forceinline__ V8 to8(const Raw8<F32>& r) {
     return f;
 }
 
-template <bool F32>
+typedef uint32_t Words4 __attribute__((ext_vector_type(4)));
+
+// STREAM: past the caches
+template <bool STREAM>
+__device__ __forceinline__ Words4 load_words(const void* p, int64_t i) {
+    const Words4* at = reinterpret_cast<const Words4*>(p) + i;
+    return STREAM ? __builtin_nontemporal_load(at) : *at;
+}
+template <bool STREAM>
+__device__ __forceinline__ void store_words(void* p, int64_t i, const Words4& w) {
+    Words4* at = reinterpret_cast<Words4*>(p) + i;
+    if (STREAM) __builtin_nontemporal_store(w, at);
+    else *at = w;
+}
+template <bool F32, bool STREAM = false>
 __device__ __forceinline__ void store8(void* p, int64_t i, const V8& f) {
     if (F32) {
-        reinterpret_cast<float4*>(p)[2 * i] = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
-        reinterpret_cast<float4*>(p)[2 * i + 1] = make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            Words4 w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[c] = __builtin_bit_cast(uint32_t, f.v[4 * k + c]);
+            store_words<STREAM>(p, 2 * i + k, w);
+        }
     } else {
-        reinterpret_cast<uint4*>(p)[i] = to_bf16x8(f);
+        const uint4 w = to_bf16x8(f);
+        store_words<STREAM>(p, i, Words4{w.x, w.y, w.z, w.w});
     }
 }
 

@@ -12,7 +12,7 @@
 //      which it counts along. Where the whole gradient is written, further
 //      workgroups of this launch write its zeros meanwhile, 8 KB each.
 //   2. sum: a run of tokens of one id is cut into pieces of R (16, or 64 above
-//      16,384 tokens); 16 .. 64 lanes add a piece over up to 1024 columns. A run
+//      8192 tokens); 16 .. 64 lanes add a piece over up to 1024 columns. A run
 //      of one piece is finished there, longer ones leave fp32 partial sums.
 //   3. join: the pieces of the longer runs, in order.
 #include "host_util.h"
@@ -82,10 +82,16 @@ __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int log_lan
 // ----------------------------------------------------------------- backward
 
 constexpr int kLocals = 512;       // ids of one bucket
+// Tokens of a piece: short ones spread few tokens over the chip, long ones leave
+// fewer partial sums. Zipf ids, 100 k x 4096, added to fp32, pieces of 16 and 64:
+// 1024 tokens 18.4 and 26.3 us, 4096 28.9 and 37.0, 16,384 91.9 and 89.1, 65,536
+// 295 and 266.
 constexpr int kLogPiece = 4, kLogPieceMany = 6;
-constexpr int64_t kManyTokens = 16384;
+constexpr int64_t kManyTokens = 8192;
 constexpr int64_t kMaxFill = int64_t(1) << 21;   // workgroups that write zeros
-constexpr int kJoinWaves = 4;
+// 4096 tokens, 90 % of them one id: 30.5 us for the whole gradient, with 4 waves
+// 38.4, with one 60; Zipf ids 31.1 and 30.5 us
+constexpr int kJoinWaves = 8;
 constexpr int kJoinCols = 256;
 
 // An item is a piece's first token in the order: .x its length and flags, .y the
@@ -133,6 +139,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 2) void group_tokens_kernel(G
     __syncthreads();
     const int64_t segment = (a.n + kWaves * 64 - 1) / (kWaves * 64) * 64;
     const int64_t from = wave * segment, to = from + segment < a.n ? from + segment : a.n;
+    volatile int* at = place + wave;   // this wave's column
     int low = 0, bad = 0x7fffffff;
     int ids[kHeld];
     const auto fetch = [&](int64_t i0) {
@@ -147,14 +154,18 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 2) void group_tokens_kernel(G
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             const int id = ids[k], i = (int)(i0 + k * 64 + lane);
-            if (id < 0) continue;
-            if (id >= a.vocab) {
-                bad = bad < i ? bad : i;
-                continue;
+            const bool valid = id >= 0 && id < a.vocab;
+            if (id >= a.vocab) bad = bad < i ? bad : i;
+            low += valid && (id & mask) < bucket;
+            const bool mine = valid && (id & mask) == bucket;
+            unsigned long long left = __ballot(mine);
+            while (left != 0) {   // as below: atomics of 64 lanes on one common id would wait for one another
+                const int lead = __ffsll((long long)left) - 1;
+                const int one = __shfl(id, lead);
+                const unsigned long long same = __ballot(mine && id == one);
+                if (lane == lead) at[(one >> a.log_buckets) * kWaves] += __popcll(same);
+                left &= ~same;
             }
-            const int b = id & mask;
-            low += b < bucket;
-            if (b == bucket) atomicAdd(&place[(id >> a.log_buckets) * kWaves + wave], 1);
         }
     }
 #pragma unroll
@@ -211,7 +222,6 @@ __global__ __launch_bounds__(64 * kWaves, kWaves / 2) void group_tokens_kernel(G
     }
     __syncthreads();
     if (all > 0) {
-        volatile int* at = place + wave;   // this wave's column
         for (int64_t i0 = from; i0 < to; i0 += 64 * kHeld) {
             if (to - from > 64 * kHeld) fetch(i0);   // else they are still held
 #pragma unroll
@@ -335,7 +345,7 @@ __global__ __launch_bounds__(256) void embedding_sum_kernel(SumArgs a) {
 }
 
 // The long run whose first piece lies in this workgroup's window, if there is
-// one. Four columns per lane; each wave takes every fourth piece, then their
+// one. Four columns per lane; each wave takes every eighth piece, then their
 // sums are added in order.
 template <bool W32>
 __global__ __launch_bounds__(64 * kJoinWaves) void embedding_join_kernel(SumArgs a) {

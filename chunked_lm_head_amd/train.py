@@ -553,6 +553,13 @@ class AdamWPlan:
             torch.cuda.synchronize(device)   # steps may run on any stream
 
 
+def _check_of(i, name, t, dtypes, shape, device):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous() and \
+            (device is None or t.device == device):
+        return
+    _check_gpu(f"{name} of tensor {i}", t, dtypes, shape, device)
+
+
 def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[AdamWState],
                copies: Optional[Sequence[Optional[torch.Tensor]]] = None) -> AdamWPlan:
     """A plan for adamw_step: parameters bf16 or fp32, gradients bf16 or fp32 of
@@ -567,27 +574,34 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     table = (lmhead_adamw_tensor * len(params))()
     dev, keep, spans = None, [], []
     for i, (p, g, s, c) in enumerate(zip(params, grads, states, copies)):
-        _check_gpu(f"params[{i}]", p, _BF16_F32, p.shape if isinstance(p, torch.Tensor) else (), dev)
-        dev = p.device
-        shape = p.shape
-        _check_gpu(f"grads[{i}]", g, _BF16_F32, shape, dev)
         m, v, ms, vs = s
-        _check_gpu(f"states[{i}].exp_avg", m, (torch.float32, torch.float8_e4m3fn), shape, dev)
-        _check_gpu(f"states[{i}].exp_avg_sq", v, (m.dtype,), shape, dev)
+        shape = p.shape if isinstance(p, torch.Tensor) else ()
+        _check_of(i, "params", p, _BF16_F32, shape, dev)
+        dev = p.device
+        _check_of(i, "grads", g, _BF16_F32, shape, dev)
+        _check_of(i, "states.exp_avg", m, (torch.float32, torch.float8_e4m3fn), shape, dev)
+        _check_of(i, "states.exp_avg_sq", v, (m.dtype,), shape, dev)
         e8 = m.dtype == torch.float8_e4m3fn
         if (ms is not None) != e8 or (vs is not None) != e8:
             raise ValueError(f"states[{i}]: scales go with e4m3 states")
+        numel = p.numel()
         if e8:
-            blocks = -(-p.numel() // FP8_BLOCK)
-            for name, t in (("exp_avg_scale", ms), ("exp_avg_sq_scale", vs)):
-                _check_gpu(f"states[{i}].{name}", t, (torch.float32,), (blocks,), dev)
+            blocks = (-(-numel // FP8_BLOCK),)
+            _check_of(i, "states.exp_avg_scale", ms, _F32, blocks, dev)
+            _check_of(i, "states.exp_avg_sq_scale", vs, _F32, blocks, dev)
         if c is not None:
-            _check_gpu(f"copies[{i}]", c, (torch.bfloat16,), shape, dev)
-        tensors = [t.detach() for t in (p, g, m, v, ms, vs, c) if t is not None]
-        keep += tensors
-        spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel() > 0]
-        table[i] = lmhead_adamw_tensor(_p(p), _p(g), _p(m), _p(v), _p(ms), _p(vs), _p(c), p.numel(),
-                                       _DTYPES[p.dtype], _DTYPES[g.dtype], _WEIGHT_DTYPES[m.dtype], 0)
+            _check_of(i, "copies", c, (torch.bfloat16,), shape, dev)
+        at = []
+        for t in (p, g, m, v, ms, vs, c):
+            if t is None:
+                at.append(None)
+                continue
+            start = t.data_ptr()
+            at.append(start)
+            keep.append(t.detach())
+            if t.numel() > 0:
+                spans.append((start, start + t.numel() * t.element_size()))
+        table[i] = (*at, numel, _DTYPES[p.dtype], _DTYPES[g.dtype], _WEIGHT_DTYPES[m.dtype], 0)
     spans.sort()
     if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
         raise ValueError("two tensors of the plan share memory")

@@ -83,7 +83,7 @@ int lmhead_embedding_fwd(const lmhead_embedding* p, const int32_t* ids, const vo
 
 /* Bytes of workspace lmhead_embedding_bwd needs (0 for an invalid problem):
  * the tokens in the order of their ids, and fp32 sums of pieces of 16 tokens
- * (64 above 16,384) of one id. */
+ * (64 above 8192) of one id. */
 size_t lmhead_embedding_bwd_workspace_size(const lmhead_embedding* p);
 
 /*

@@ -29,6 +29,7 @@ namespace {
 constexpr int kTileThreads = 256, kTileEach = 4;     // tokens per thread
 constexpr int64_t kTileTokens = kTileThreads * kTileEach;
 constexpr int kFewThreads = 256, kWholeThreads = 1024, kWholeEach = 8;
+constexpr int64_t kWholeSequences = 8192;   // more of them go over several workgroups
 constexpr int64_t kFewTokens = kFewThreads * kWholeEach, kWholeTokens = kWholeThreads * kWholeEach;
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -545,9 +546,12 @@ static int lanes_for(int64_t count, int64_t tiles) {
     return lanes;
 }
 
+static int64_t tiles_of(int64_t n) { return n > 0 ? cdiv(n, kTileTokens) : 1; }
+static bool one_launch(int64_t n, int64_t sequences) { return n <= kWholeTokens && sequences <= kWholeSequences; }
+
 size_t policy_workspace(int64_t n, int64_t sequences, int reduction) {
-    if (n <= kWholeTokens) return 256;
-    const int64_t tiles = cdiv(n, kTileTokens);
+    if (one_launch(n, sequences)) return 256;
+    const int64_t tiles = tiles_of(n);
     int64_t bytes = round_up(tiles * 6 * 8, 256);
     if (reduction == 2)
         bytes += round_up((tiles + sequences) * (int64_t)sizeof(Part), 256) + round_up(sequences * 8, 256);
@@ -556,7 +560,7 @@ size_t policy_workspace(int64_t n, int64_t sequences, int reduction) {
 
 void launch_policy(const PolicyArgs& a, void* workspace, hipStream_t s) {
     const bool seq = a.reduction == 2;
-    if (a.t.n <= kWholeTokens) {
+    if (one_launch(a.t.n, a.t.sequences)) {
         if (a.t.n <= kFewTokens) {
             if (seq) policy_whole_kernel<kFewThreads, true><<<1, kFewThreads, 0, s>>>(a);
             else policy_whole_kernel<kFewThreads, false><<<1, kFewThreads, 0, s>>>(a);
@@ -566,7 +570,7 @@ void launch_policy(const PolicyArgs& a, void* workspace, hipStream_t s) {
         }
         return;
     }
-    const int64_t tiles = cdiv(a.t.n, kTileTokens);
+    const int64_t tiles = tiles_of(a.t.n);
     char* w = (char*)workspace;
     double* sums = (double*)w;
     Part* slots = (Part*)(w + round_up(tiles * 6 * 8, 256));
@@ -584,17 +588,17 @@ void launch_policy_bwd(const PolicyArgs& a, const float* grad, float* dlogp, hip
 }
 
 size_t preference_workspace(int64_t n, int64_t pairs) {
-    if (n <= kWholeTokens) return 256;
-    return (size_t)(round_up((cdiv(n, kTileTokens) + 2 * pairs) * (int64_t)sizeof(Part), 256) + round_up(pairs * 8, 256));
+    if (one_launch(n, 2 * pairs)) return 256;
+    return (size_t)(round_up((tiles_of(n) + 2 * pairs) * (int64_t)sizeof(Part), 256) + round_up(pairs * 8, 256));
 }
 
 void launch_preference(const PreferenceArgs& a, void* workspace, hipStream_t s) {
-    if (a.t.n <= kWholeTokens) {
+    if (one_launch(a.t.n, a.t.sequences)) {
         if (a.t.n <= kFewTokens) preference_whole_kernel<kFewThreads><<<1, kFewThreads, 0, s>>>(a);
         else preference_whole_kernel<kWholeThreads><<<1, kWholeThreads, 0, s>>>(a);
         return;
     }
-    const int64_t tiles = cdiv(a.t.n, kTileTokens), pairs = a.t.sequences / 2;
+    const int64_t tiles = tiles_of(a.t.n), pairs = a.t.sequences / 2;
     Part* slots = (Part*)workspace;
     double* each = (double*)((char*)workspace + round_up((tiles + a.t.sequences) * (int64_t)sizeof(Part), 256));
     preference_tiles_kernel<<<(unsigned)tiles, kTileThreads, 0, s>>>(a, slots);

@@ -282,7 +282,8 @@ class Embedding(torch.autograd.Function):
 def embedding(ids, weight, scale: float = 1.0, weight_scale=None, out_dtype=None):
     """embedding_forward with the gradient of a bf16 or fp32 weight (whole, as
     autograd adds it up; embedding_backward adds to an accumulator in place). An
-    e4m3 weight has none. Differentiable once."""
+    e4m3 weight has none. Differentiable once; for a backward captured into a graph
+    see rms_norm."""
     if weight_scale is not None or not isinstance(weight, torch.Tensor) or weight.dtype not in _DTYPES:
         return embedding_forward(ids, weight, scale, weight_scale, out_dtype)
     return Embedding.apply(ids, weight, scale, out_dtype)
@@ -431,7 +432,8 @@ def policy_loss(logp, advantage, old_logp=None, ref_logp=None, targets=None, cu_
                 clip_high: float = 0.2, dual_clip: float = 0.0, kl_weight: float = 0.0, kl_kind: str = "k3",
                 reduction: str = "mean", num_valid: int = -1, advantage_per_sequence: Optional[bool] = None):
     """(loss, stats) with the gradient of logp alone (old_logp, ref_logp and the
-    advantages are constants); see policy_loss_forward. Differentiable once."""
+    advantages are constants); see policy_loss_forward. Differentiable once; for a
+    backward captured into a graph see rms_norm."""
     return PolicyLoss.apply(logp, advantage, old_logp, ref_logp, targets, cu_seqlens,
                             (clip_low, clip_high, dual_clip, kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence))
 
@@ -509,7 +511,8 @@ class PreferenceLoss(torch.autograd.Function):
 def preference_loss(logp, cu_seqlens, ref_logp=None, targets=None, kind: str = "sigmoid", beta: float = 0.1,
                     margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False, num_pairs: int = -1):
     """(loss, rewards) with the gradient of logp alone; see
-    preference_loss_forward. Differentiable once."""
+    preference_loss_forward. Differentiable once; for a backward captured into a
+    graph see rms_norm."""
     return PreferenceLoss.apply(logp, cu_seqlens, ref_logp, targets,
                                 (kind, beta, margin, label_smoothing, average, num_pairs))
 
@@ -565,7 +568,8 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     """A plan for adamw_step: parameters bf16 or fp32, gradients bf16 or fp32 of
     the same shapes (kept in place from step to step, as accumulators are),
     states from adamw_state, copies None or bf16 tensors that take the rounded
-    parameters. All contiguous, on one GPU, and none sharing memory with another."""
+    parameters. All contiguous, on one GPU, and none sharing memory with another.
+    Not while a graph is captured (the steps may be)."""
     copies = [None] * len(params) if copies is None else list(copies)
     if not len(params) == len(grads) == len(states) == len(copies):
         raise ValueError("params, grads, states and copies must be of one length")
@@ -611,7 +615,8 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
 def adamw_step(plan: AdamWPlan, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                weight_decay: float = 0.0, grad_scale: Optional[torch.Tensor] = None,
                seed: Optional[int] = None) -> None:
-    """One AdamW step of the plan's tensors, in place; see lmhead_adamw_step.
+    """One AdamW step of the plan's tensors, in place (autograd is not told: step
+    after the backward passes that read them); see lmhead_adamw_step.
     step: 1 for the first, or an int32 device tensor of one element (read at
     each replay of a captured step); lr: a number or an fp32 device tensor of one;
     grad_scale: an fp32 device tensor of one that multiplies the gradients. seed:

@@ -165,6 +165,70 @@ def test_policy_border_in_64_bits():
     assert abs(float(f.loss) - want[0]) < 6 * 4 * U
 
 
+@pytest.mark.parametrize("n", [0, 3, 700])
+def test_more_sequences_than_a_workgroup_takes(n):
+    """20,000 sequences over a few tokens, most of them empty."""
+    rng = np.random.default_rng(n)
+    sequences = 20000
+    cu = np.sort(rng.integers(0, n + 1, sequences + 1))
+    logp, old, adv = f32(-rng.random(n)), f32(-rng.random(n)), f32(rng.standard_normal(n))
+    args = (dev(logp), dev(adv), dev(old), None, None, dev(cu, torch.int32))
+    for reduction in ("mean", "sequence_mean"):
+        want = ref.policy(logp, adv, old, None, None, cu, reduction=reduction)
+        f = lm.policy_loss_forward(*args, reduction=reduction)
+        got = lm.policy_loss_backward(torch.ones(1, device="cuda"), f.weights, *args, reduction=reduction)
+        assert abs(float(f.loss) - want[0]) <= U * (want[3].sum() + 2 * abs(want[0])) * 1.01 + 1e-300
+        assert (np.abs(got.double().cpu().numpy() - want[2]) <= U * (want[3] + 4 * np.abs(want[2])) * 1.01).all()
+    want = ref.preference(logp, cu, None, None, average=True)
+    f = lm.preference_loss_forward(args[0], args[5], average=True)
+    got = lm.preference_loss_backward(torch.ones(1, device="cuda"), f.coef, n, args[5])
+    assert abs(float(f.loss) - want[0]) <= 2 * U * want[0]
+    # the slope's change with h: at most 1/4 of beta U (|s| + |s|), each |s| <= 1
+    assert (np.abs(got.double().cpu().numpy() - want[2]) <= 2 * U * np.abs(want[2]) + 0.1 * 0.25 * 0.2 * U).all()
+
+
+def test_policy_without_a_lower_border():
+    """clip_low 1: a ratio is never below 0."""
+    x, o, a = torch.tensor([-60.0, -1.0], device="cuda"), torch.zeros(2, device="cuda"), -torch.ones(2, device="cuda")
+    f = lm.policy_loss_forward(x, a, o, clip_low=1.0, reduction="sum")
+    got = lm.policy_loss_backward(torch.ones(1, device="cuda"), f.weights, x, a, o, clip_low=1.0, reduction="sum")
+    assert float(f.stats[1]) == 0 and torch.allclose(got, x.exp(), rtol=1e-6, atol=0)
+
+
+def test_autograd_captured():
+    """Gradients through autograd in a graph, both losses behind a lookup and the log-probs."""
+    n, hidden, vocab = 130, 128, 500
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    W = (torch.randn(vocab, hidden, generator=g, device="cuda") * 0.1).to(torch.bfloat16).requires_grad_()
+    ids = torch.randint(0, vocab, (n,), generator=g, device="cuda", dtype=torch.int32)
+    targets = torch.randint(-50, vocab, (n,), generator=g, device="cuda", dtype=torch.int32)
+    cu = torch.tensor([0, 40, 70, 70, 130], dtype=torch.int32, device="cuda")
+    adv, old = torch.randn(4, generator=g, device="cuda"), -torch.rand(n, generator=g, device="cuda")
+
+    def step():
+        logp = lm.logprob(lm.embedding(ids, W), W, targets, chunk=256)
+        a, _ = lm.policy_loss(logp, adv, logp.detach() + 0.1, old, targets, cu, kl_weight=0.1)
+        b, _ = lm.preference_loss(logp, cu, old, targets)
+        return torch.autograd.grad(a + b, W)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (out,) = step()
+    for rep in range(3):
+        with torch.no_grad():
+            W.normal_(0, 0.1)
+        ids.copy_(torch.randint(0, vocab, (n,), generator=g, device="cuda", dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, step()[0]), rep
+
+
 @pytest.mark.parametrize("x", [0.0, 1e-6, 1e-3, 0.1, 0.4999, 0.5001, 2.0, 30.0])
 def test_k3_small_and_large(x):
     """Relative accuracy of the estimate, where the plain difference cancels."""

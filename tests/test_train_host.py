@@ -125,6 +125,7 @@ def test_policy_refusals():
     # one launch needs none; above 8192 tokens six sums a tile of 1024, and with sequence means their parts
     assert size(pol(n=8192)) == 256 and size(pol(n=8193)) == 512
     assert size(pol(n=8193, reduction=2)) == 512 + 2 * 256
+    assert size(pol(n=0, sequences=8193, reduction=2)) == 256 + 131328 + 65792   # 8194 parts of 16 bytes, 8193 means
 
 
 def pref(**kw):

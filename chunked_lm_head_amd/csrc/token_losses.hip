@@ -189,6 +189,16 @@ __device__ __forceinline__ void look_up(Tile& o, const Tokens& t) {
     o.at = sequences_at(t, o.t0, o.t1 > o.t0 ? o.t1 - 1 : o.t0);
 }
 
+// Nothing differs between the sequences: then the tile's span is that of the
+// tokens which lie in one, and none is looked up (1 M tokens in 256 sequences:
+// backward 6.4 us, with the search 8.2; tiles of the forward 12.4 and 13.0).
+__device__ __forceinline__ bool all_alike(const PolicyArgs& a) { return !a.per_sequence && a.reduction != 2; }
+
+__device__ __forceinline__ void look_up(Tile& o, const PolicyArgs& a) {
+    if (all_alike(a)) o.at = Span{border(a.t, 0), border(a.t, a.t.sequences)};
+    else look_up(o, a.t);
+}
+
 // A thread's tokens t0 + thread, + THREADS, ...: loaded at once; then their terms.
 template <int THREADS, int EACH>
 struct PolicyTokens {
@@ -209,10 +219,11 @@ struct PolicyTokens {
             target[k] = a.t.targets != nullptr ? a.t.targets[i] : 0;
         }
     }
-    // the token's sequence where it counts, else -1
+    // the token's sequence where it counts, else -1; any sequence where all are one
     __device__ __forceinline__ int64_t place(const PolicyArgs& a, const Tile& tile, int k) const {
         const int64_t i = tile.t0 + k * THREADS + threadIdx.x;
         if (i >= tile.t1 || target[k] < 0) return -1;
+        if (all_alike(a)) return i >= tile.at.first && i < tile.at.last ? 0 : -1;
         const int64_t q = sequence_between(a.t, tile.at.first, tile.at.last, i);
         return q < a.t.sequences ? q : -1;
     }
@@ -228,7 +239,7 @@ template <int THREADS, int EACH, bool SEQ>
 __device__ __forceinline__ void policy_tile(const PolicyArgs& a, Tile& tile, double (&s)[6], float* kept, uint8_t* counts) {
     PolicyTokens<THREADS, EACH> tokens;
     tokens.load(a, tile);
-    look_up(tile, a.t);
+    look_up(tile, a);
 #pragma unroll
     for (int k = 0; k < 6; ++k) s[k] = 0.0;
 #pragma unroll
@@ -387,7 +398,7 @@ __global__ __launch_bounds__(kTileThreads) void policy_bwd_kernel(PolicyArgs a, 
     PolicyTokens<kTileThreads, kTileEach> tokens;
     tokens.load(a, tile);
     const float g = grad[0];
-    look_up(tile, a.t);
+    look_up(tile, a);
 #pragma unroll
     for (int k = 0; k < kTileEach; ++k) {
         const int64_t i = tile.t0 + k * kTileThreads + threadIdx.x;

@@ -1,8 +1,8 @@
 // embedding.hip — rows of the vocabulary matrix by token, and their gradient.
 //
 // Mathematics. out[i] = scale W[id_i]. dW[v] (+)= scale sum_{i: id_i = v}
-// dout[i]: a sum over the tokens of each id, in fp32, in an order that depends
-// on the ids alone.
+// dout[i]: a sum over the tokens of each id, in fp32, in the order of their places,
+// by pieces whose length depends on n alone.
 //
 // Both are bound by memory. The gradient runs in three launches:
 //   1. group: tokens in the order (bucket, id, place). A workgroup owns the ids

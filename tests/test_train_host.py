@@ -122,9 +122,9 @@ def test_policy_refusals():
     for name in ("grad", "weights", "dlogp"):
         assert backward(pol(), **{name: None}) == A, name
     assert forward(pol(), ws=F + 64) == AL and forward(pol(), bytes=0) == W
-    # one launch needs none; above 8192 tokens six sums a tile of 1024, and with sequence means their parts
-    assert size(pol(n=8192)) == 256 and size(pol(n=8193)) == 512
-    assert size(pol(n=8193, reduction=2)) == 512 + 2 * 256
+    # one launch needs none; above 4096 tokens six sums a tile of 1024, and with sequence means their parts
+    assert size(pol(n=4096)) == 256 and size(pol(n=6 * 1024)) == 512
+    assert size(pol(n=6 * 1024, reduction=2)) == 512 + 2 * 256
     assert size(pol(n=0, sequences=8193, reduction=2)) == 256 + 131328 + 65792   # 8194 parts of 16 bytes, 8193 means
 
 

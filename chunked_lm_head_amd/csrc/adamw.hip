@@ -73,6 +73,28 @@ __device__ __forceinline__ void put_codes(void* p, int64_t e, int64_t numel, boo
         if (e + c < numel) reinterpret_cast<uint8_t*>(p)[e + c] = (uint8_t)(w[c >> 2] >> (8 * (c & 3)));
 }
 
+// a x + b y with every product rounded
+__device__ __forceinline__ float each_rounded(float a, float x, float b, float y) {
+#pragma clang fp contract(off)
+    const float p = a * x, q = b * y;
+    return p + q;
+}
+
+// The root rounded to nearest (but for ties of the last step, within 2^-20 of one):
+// one Newton step with its remainder from the instruction's reciprocal root.
+// Below 2^-126: 0.
+__device__ __forceinline__ float rounded_root(float x) {
+    const float y = __builtin_amdgcn_rsqf(x), s = x * y;
+    const float r = __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * y, s);
+    const bool normal = x >= 0x1p-126f && x <= 3.402823466e38f;
+    return normal ? r : x < 0x1p-126f ? 0.0f : x;   // infinity and NaN are their own
+}
+
+// Scale of a block of 8-bit states: its largest magnitude by 448.
+__device__ __forceinline__ float state_scale(float amax) {
+    return amax > 0.0f ? fmaxf(amax * (1.0f / kE4m3Max), 0x1p-126f) : 1.0f;
+}
+
 // over the 16 lanes that hold a block of 128 (NaN left out)
 __device__ __forceinline__ float max16(float v) {
 #pragma unroll
@@ -99,7 +121,8 @@ __device__ __forceinline__ float cut_at_random(float y, uint32_t random20) {
     return __builtin_copysignf(__builtin_bit_cast(float, bits) - base, y);
 }
 
-// e4m3 of eight quotients by the block's scale. ROOT: a value above zero gets at
+// e4m3 of eight quotients by the block's scale, the quotients as a division
+// rounds them. ROOT: a value above zero gets at
 // least the least code. RANDOM: noise of the eight, in bits 4 .. 19.
 template <bool ROOT, bool RANDOM>
 __device__ __forceinline__ uint2 codes(const V8& f, float scale, const uint32_t* noise) {
@@ -132,8 +155,8 @@ struct Step {
 template <bool P32, bool G32, bool S8, bool RANDOM>
 __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int64_t chunk) {
     // 8-bit states leave few bytes per element: two trips in flight, past the
-    // caches (622 M bf16 parameters: 1050 us; one trip 1139, two through the
-    // caches 1093). fp32 states: one trip through them (525 M: 2296 us; two 2323,
+    // caches (622 M bf16 parameters, before the rounded root: 1050 us; one trip
+    // 1139, two through the caches 1093). fp32 states: one trip through them (525 M: 2296 us; two 2323,
     // past the caches 2390).
     constexpr int kTrips = (S8 ? kAdamWChunk8 : kAdamWChunk) / 2048;
     const bool wide = (t.kind & kAdamWWide) != 0;
@@ -175,11 +198,19 @@ __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int6
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const float gc = g[j].v[c] * k.grad_scale;
-            const float mc = __builtin_fmaf(k.rest1, gc, k.beta1 * m[j].v[c]);
-            const float vc = __builtin_fmaf(k.rest2 * gc, gc, k.beta2 * v[j].v[c]);
+            // What becomes 8 bits is rounded operation by operation, as elementwise
+            // programs do: a last bit that differs between two ways of computing
+            // m' is a code's step where it lies at a border, and the next step's
+            // scale where that code is its block's largest.
+            const float mc = S8 ? each_rounded(k.beta1, m[j].v[c], k.rest1, gc)
+                                : __builtin_fmaf(k.rest1, gc, k.beta1 * m[j].v[c]);
+            const float vc = S8 ? each_rounded(k.beta2, v[j].v[c], k.rest2, gc * gc)
+                                : __builtin_fmaf(k.rest2 * gc, gc, k.beta2 * v[j].v[c]);
             // the instructions' own root and reciprocal, each within 2^-23: the
-            // library's correctly rounded ones would double the arithmetic
-            const float rc = __builtin_amdgcn_sqrtf(vc);
+            // library's correctly rounded ones would double the arithmetic. A root
+            // that becomes 8 bits is rounded_root's: 1079 us for 622 M parameters, with the
+            // instruction's 1038, with the library's 1196.
+            const float rc = S8 ? rounded_root(vc) : __builtin_amdgcn_sqrtf(vc);
             const float step = mc * __builtin_amdgcn_rcpf(__builtin_fmaf(rc, k.root_scale, k.eps));
             p[j].v[c] = __builtin_fmaf(-k.step_size, step, p[j].v[c] * k.keep);
             m[j].v[c] = mc;
@@ -198,7 +229,7 @@ __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int6
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     noise[RANDOM ? c : 0] = scramble((uint32_t)(e + c) ^ k.mix ^ (uint32_t)(e >> 32) * 0x9e3779b9u);
-            const float sm = block_scale(max16(m_max)), sv = block_scale(max16(v_max));
+            const float sm = state_scale(max16(m_max)), sv = state_scale(max16(v_max));
             put_codes(t.m, e, t.numel, wide, codes<false, RANDOM>(m[j], sm, noise));
             put_codes(t.v, e, t.numel, wide, codes<true, RANDOM>(root, sv, noise));
             if ((threadIdx.x & 15) == 0 && e < t.numel) {

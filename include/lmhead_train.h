@@ -315,8 +315,10 @@ typedef struct lmhead_adamw {
  *            - lr / (1 - beta1^t) * m' / (sqrt(v') / sqrt(1 - beta2^t) + eps).
  * The parameter is updated from the fp32 m' and v'; states in 8 bits are
  * rounded after that, over blocks of 128 consecutive elements of a tensor as
- * lmhead_quantize_fp8 rounds, except that a sqrt(v') > 0 becomes no zero
- * (at least 2^-9 of its scale): a vanishing denominator would let m' loose.
+ * lmhead_quantize_fp8 rounds (the scale is the largest magnitude times 1 / 448 in
+ * fp32, and every operation on the way to a code is rounded by itself, so that
+ * elementwise fp32 programs get the same codes), except that a sqrt(v') > 0 becomes
+ * no zero (at least 2^-9 of its scale): a vanishing denominator would let m' loose.
  * The root of a v' below 2^-126 is zero.
  * States of zeros start (any finite scales).
  * Stochastic: with y = value / scale and u the upper 16 of 20 random bits, as a

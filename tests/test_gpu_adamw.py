@@ -302,6 +302,35 @@ def test_repeats_bit_for_bit_and_on_another_stream():
         assert all(torch.equal(a, b) for a, b in zip(outs[0], o))
 
 
+@pytest.mark.parametrize("step,beta2", [(1, 0.95), (3, 0.999), (1000, 0.95)])
+def test_8_bit_states_are_those_of_an_elementwise_program(step, beta2):
+    """Codes and scales bit for bit over three steps: a code's step more or less
+    would be the next step's scale where it is its block's largest."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(step)
+    n = 1 << 22
+    p, d, s, _ = make(g, (n,), BF, BF, E8, False)
+    m, v, ms, vs = (t.clone() if t.dtype != E8 else t.view(torch.uint8).clone().view(E8) for t in s)
+    plan = lm.adamw_plan([p], [d], [s])
+    for t in range(step, step + 3):
+        lm.adamw_step(plan, t, 0.01, 0.9, beta2)
+        m1 = (m.float() * ms.repeat_interleave(128)) * 0.9 + d.float() * (1.0 - 0.9)
+        v1 = (v.float() * vs.repeat_interleave(128)).square() * beta2 + d.float().square() * (1.0 - beta2)
+        out = []
+        for x, root in ((m1, False), (v1.sqrt(), True)):
+            b = x.view(-1, 128)
+            scale = b.abs().amax(1) * torch.tensor(1.0 / 448.0, device="cuda")
+            y = b / scale[:, None]
+            if root:
+                y = torch.where(b > 0, y.clamp(min=2.0 ** -9), 0.0)
+            out += [y.to(E8).view(-1), scale]
+        m, ms, v, vs = out
+        assert torch.equal(s.exp_avg_scale, ms) and torch.equal(s.exp_avg_sq_scale, vs)
+        assert torch.equal(s.exp_avg.view(torch.uint8), m.view(torch.uint8))
+        assert torch.equal(s.exp_avg_sq.view(torch.uint8), v.view(torch.uint8))
+        d.normal_(generator=g)
+
+
 def scramble(x):
     x = x & 0xffffffff
     x = (x ^ (x >> 16)) * 0x9e3779b9 & 0xffffffff

@@ -541,7 +541,8 @@ def adamw_state(param, dtype=torch.float32) -> AdamWState:
 class AdamWPlan:
     """The tensors of a step, checked and laid out once (adamw_plan). It keeps
     the storages that the tensors had then: a parameter or gradient that is given
-    another storage needs another plan."""
+    another storage needs another plan. A graph that holds a step reads the plan's
+    memory: keep the plan as long as the graph."""
 
     def __init__(self, device, tensors, keep):
         self.device, self.tensors, self.count, self.keep = device, tensors, len(tensors), keep

@@ -15,6 +15,9 @@
 //      8192 tokens); 16 .. 64 lanes add a piece over up to 1024 columns. A run
 //      of one piece is finished there, longer ones leave fp32 partial sums.
 //   3. join: the pieces of the longer runs, in order.
+// 16,384 tokens of Zipf ids, 152 k x 4096 bf16 written whole: 190 us (1.25 GB, 6.5
+// TB/s), 68 (while the zeros drain to memory) and 6.5. 4096 tokens added to fp32: 9.5,
+// 16 (78 MB, 4.8 TB/s) and 6.5.
 #include "host_util.h"
 #include "train_kernels.h"
 #include "vec8.h"

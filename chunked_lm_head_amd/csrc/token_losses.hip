@@ -424,6 +424,10 @@ __global__ __launch_bounds__(kTileThreads) void policy_bwd_kernel(PolicyArgs a, 
 }
 
 // --------------------------------------------------------------- preference
+//
+// The same tiles and slots; what a thread keeps is a difference. 512 pairs over 1 M
+// tokens: tiles 7.6 us (12 MB), pairs 6.2, backward 7 (8 MB); 4 pairs over 2500 tokens
+// in one launch 5.5, backward 4.5. Latency decides all of them.
 
 template <int THREADS, int EACH>
 __device__ __forceinline__ void preference_tile(const PreferenceArgs& a, const Tile& tile, float* kept, uint8_t* counts) {

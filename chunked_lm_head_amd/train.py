@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -286,7 +287,7 @@ def embedding(ids, weight, scale: float = 1.0, weight_scale=None, out_dtype=None
     see rms_norm."""
     if weight_scale is not None or not isinstance(weight, torch.Tensor) or weight.dtype not in _DTYPES:
         return embedding_forward(ids, weight, scale, weight_scale, out_dtype)
-    return Embedding.apply(ids, weight, scale, out_dtype)
+    return Embedding.apply(ids, weight, float(scale), out_dtype)
 
 
 # ------------------------------------------------- losses on log-probabilities
@@ -330,7 +331,13 @@ def _outputs(entry, p, nbytes, pointers, ws, floats, like):
     return ws, torch.empty(floats, dtype=torch.float32, device=like.device)
 
 
-# a problem and its workspace's size, by its numbers alone
+def _real(x) -> float:
+    """x as the C call reads it. A tensor's hash is its identity: under that a value
+    changed in place would be found by its old one."""
+    return x if type(x) is float else ctypes.c_double(x).value
+
+
+# a problem and its workspace's size, by its numbers alone: Python's own floats and ints
 @functools.lru_cache(maxsize=64)
 def _policy_sizes(*numbers):
     p = lmhead_policy_problem(*numbers, 0)
@@ -362,8 +369,8 @@ def _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, cl
         raise ValueError("kl_kind must be 'k1', 'k2' or 'k3'")
     if reduction not in _REDUCE:
         raise ValueError("reduction must be 'mean', 'sum' or 'sequence_mean'")
-    return _policy_sizes(n, sequences, num_valid, clip_low, clip_high, dual_clip, kl_weight, _KL[kl_kind],
-                         _REDUCE[reduction], int(per_sequence))
+    return _policy_sizes(n, sequences, operator.index(num_valid), _real(clip_low), _real(clip_high), _real(dual_clip),
+                         _real(kl_weight), _KL[kl_kind], _REDUCE[reduction], int(per_sequence))
 
 
 @_on_device_of(0)
@@ -435,7 +442,9 @@ def policy_loss(logp, advantage, old_logp=None, ref_logp=None, targets=None, cu_
     advantages are constants); see policy_loss_forward. Differentiable once; for a
     backward captured into a graph see rms_norm."""
     return PolicyLoss.apply(logp, advantage, old_logp, ref_logp, targets, cu_seqlens,
-                            (clip_low, clip_high, dual_clip, kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence))
+                            # numbers now: the backward's are the forward's
+                            (_real(clip_low), _real(clip_high), _real(dual_clip), _real(kl_weight), kl_kind, reduction,
+                             operator.index(num_valid), advantage_per_sequence))
 
 
 class PreferenceOutputs(NamedTuple):
@@ -456,8 +465,8 @@ def preference_loss_forward(logp, cu_seqlens, ref_logp=None, targets=None, kind:
     pairs = _pairs(cu_seqlens)
     if kind not in _PREFERENCE:
         raise ValueError("kind must be 'sigmoid', 'hinge' or 'squared'")
-    p, nbytes = _preference_sizes(n, pairs, num_pairs, beta, margin, label_smoothing, _PREFERENCE[kind],
-                                  int(bool(average)))
+    p, nbytes = _preference_sizes(n, pairs, operator.index(num_pairs), _real(beta), _real(margin),
+                                  _real(label_smoothing), _PREFERENCE[kind], int(bool(average)))
     ws, out = _outputs(lmhead_preference_loss_fwd, p, nbytes, 8, ws, 1 + 4 * pairs, logp)
     loss, rewards, coef = out[0], out[1:1 + 2 * pairs], out[1 + 2 * pairs:]
     _ok(lmhead_preference_loss_fwd(p, logp, ref_logp, targets, cu_seqlens, loss, rewards, coef, ws,
@@ -481,7 +490,7 @@ def preference_loss_backward(grad, coef, n: int, cu_seqlens, targets=None):
     _check_vector("coef", coef, _F32, 2 * pairs, grad)
     if targets is not None:
         _check_vector("targets", targets, _I32, n, grad)
-    p, _ = _preference_sizes(n, pairs, -1, 1.0, 0.0, 0.0, PREFERENCE_SIGMOID, 0)
+    p, _ = _preference_sizes(operator.index(n), pairs, -1, 1.0, 0.0, 0.0, PREFERENCE_SIGMOID, 0)
     dlogp = torch.empty(n, dtype=torch.float32, device=grad.device)
     _ok(lmhead_preference_loss_bwd(p, grad, coef, targets, cu_seqlens, dlogp), "lmhead_preference_loss_bwd")
     return dlogp

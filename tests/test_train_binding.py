@@ -1,0 +1,104 @@
+"""The binding of include/lmhead_train.h on the host: what it hands to the entries,
+with the entries and the checks for a GPU replaced."""
+import numpy as np
+import pytest
+import torch
+
+import chunked_lm_head_amd as lm
+from chunked_lm_head_amd import train
+
+CU = torch.tensor([0, 2, 4], dtype=torch.int32)
+
+
+@pytest.fixture
+def problems(monkeypatch):
+    """Problems that the helpers hand to the losses' entries, as dicts."""
+    seen = []
+
+    def entry(p, *args):
+        seen.append({name: getattr(p, name) for name, _ in p._fields_})
+        return lm.LMHEAD_OK
+    for name in ("lmhead_policy_loss_fwd", "lmhead_policy_loss_bwd", "lmhead_preference_loss_fwd",
+                 "lmhead_preference_loss_bwd"):
+        monkeypatch.setattr(train, name, entry)
+    for name in ("_check_gpu", "_check_vector", "_check_scalar"):
+        monkeypatch.setattr(train, name, lambda *a, **k: None)
+    return seen
+
+
+def numbers(value):
+    """The same number in every form that an entry's struct takes."""
+    return [torch.tensor(value, dtype=torch.float64), np.array(value), np.float64(value)]
+
+
+@pytest.mark.parametrize("name", ["clip_low", "clip_high", "dual_clip", "kl_weight"])
+@pytest.mark.parametrize("backward", [False, True])
+def test_policy_numbers_are_read_at_each_call(problems, name, backward):
+    x = torch.zeros(4)
+    call = (lambda **kw: lm.policy_loss_backward(x[:1], x[:1], x, x, ref_logp=x, **kw)) if backward else \
+        (lambda **kw: lm.policy_loss_forward(x, x, ref_logp=x, **kw))
+    start = 2.0 if name == "dual_clip" else 0.25
+    for v in numbers(start)[:2]:
+        for factor in (1.0, 2.0, 2.0):
+            v *= factor   # in place: the same object
+            call(**{name: v})
+        assert [p[name] for p in problems[-3:]] == [start, 2 * start, 4 * start]
+    for v in numbers(start)[2:]:
+        call(**{name: v})
+        assert problems[-1][name] == start
+
+
+@pytest.mark.parametrize("name", ["beta", "margin", "label_smoothing"])
+def test_preference_numbers_are_read_at_each_call(problems, name):
+    x = torch.zeros(4)
+    for v in numbers(0.125)[:2]:
+        for factor in (1.0, 2.0, 2.0):
+            v *= factor
+            lm.preference_loss_forward(x, CU, **{name: v})
+        assert [p[name] for p in problems[-3:]] == [0.125, 0.25, 0.5]
+
+
+@pytest.mark.parametrize("count", [torch.tensor(3), np.int64(3), np.array(3), 3])
+def test_given_counts_are_read_at_each_call(problems, count):
+    x = torch.zeros(4)
+    for want in (3, 5):
+        lm.policy_loss_forward(x, x, num_valid=count)
+        assert problems[-1]["num_valid"] == want
+        lm.preference_loss_forward(x, CU, num_pairs=count)
+        assert problems[-1]["num_pairs"] == want
+        count += 2
+
+
+def test_a_backward_takes_the_forwards_numbers(problems, monkeypatch):
+    x, k = torch.zeros(4, requires_grad=True), torch.tensor(0.25)
+    loss, _ = lm.policy_loss(x, x.detach(), ref_logp=x.detach(), kl_weight=k)
+    k.mul_(2)
+    loss.backward()
+    assert [p["kl_weight"] for p in problems] == [0.25, 0.25]
+    scales = []
+
+    def entry(p, *args):
+        scales.append(p.scale)
+        return lm.LMHEAD_OK
+    monkeypatch.setattr(train, "lmhead_embedding_fwd", entry)
+    monkeypatch.setattr(train, "lmhead_embedding_bwd", entry)
+    w, k = torch.zeros(5, 64, requires_grad=True), torch.tensor(0.25)
+    y = lm.embedding(torch.zeros(3, dtype=torch.int32), w, k)
+    k.mul_(2)
+    y.backward(torch.zeros_like(y))
+    assert scales == [0.25, 0.25]
+
+
+def test_what_is_no_number_is_refused(problems):
+    x = torch.zeros(4)
+    for bad in ("0.1", None, torch.zeros(2), [0.1]):
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            lm.policy_loss_forward(x, x, clip_low=bad)
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            lm.preference_loss_forward(x, CU, beta=bad)
+    for bad in ("3", 1.5, torch.tensor(1.5)):
+        with pytest.raises(TypeError):
+            lm.policy_loss_forward(x, x, num_valid=bad)
+        with pytest.raises(TypeError):
+            lm.preference_loss_forward(x, CU, num_pairs=bad)
+    assert not problems

@@ -550,11 +550,13 @@ def adamw_state(param, dtype=torch.float32) -> AdamWState:
 class AdamWPlan:
     """The tensors of a step, checked and laid out once (adamw_plan). It keeps
     the storages that the tensors had then: a parameter or gradient that is given
-    another storage needs another plan. A graph that holds a step reads the plan's
+    another storage needs another plan. It may be dropped while steps are still
+    running, on any streams; but a graph that holds a step reads the plan's
     memory: keep the plan as long as the graph."""
 
     def __init__(self, device, tensors, keep):
         self.device, self.tensors, self.count, self.keep = device, tensors, len(tensors), keep
+        self.streams = set()   # that its memory is marked as in use on
         self.table = None
         if self.count > 48:   # more than a launch takes as an argument
             table = torch.empty(lmhead_adamw_table_size(self.count), dtype=torch.uint8)
@@ -564,6 +566,23 @@ class AdamWPlan:
             _ok(st, "lmhead_adamw_table")
             self.table = table.to(device)
             torch.cuda.synchronize(device)   # steps may run on any stream
+
+    def step(self, p):
+        """One launch of the plan's tensors on the current stream of its device,
+        which is the current one."""
+        stream = _stream(None)
+        if stream not in self.streams and not torch.cuda.is_current_stream_capturing():
+            # The allocator hands a freed block at once to the stream that it was
+            # allocated on. Marked, it waits for this one first: else a plan dropped
+            # here would leave the kernel another tensor's bytes for addresses. Once
+            # per stream: a mark holds until the block is freed.
+            current = torch.cuda.current_stream()
+            for t in self.keep:
+                t.record_stream(current)
+            if self.table is not None:
+                self.table.record_stream(current)
+            self.streams.add(stream)
+        _ok(lmhead_adamw_step(p, self.tensors, self.count, self.table, stream), "lmhead_adamw_step")
 
 
 def _check_of(i, name, t, dtypes, shape, device):
@@ -648,7 +667,7 @@ def adamw_step(plan: AdamWPlan, step, lr, beta1: float = 0.9, beta2: float = 0.9
         _check_scalar("grad_scale", grad_scale, torch.float32, plan.device)
         p.grad_scale = grad_scale.data_ptr()
     if plan.device.index == torch.cuda.current_device():
-        _ok(lmhead_adamw_step(p, plan.tensors, plan.count, plan.table), "lmhead_adamw_step")
+        plan.step(p)
         return
     with torch.cuda.device(plan.device):
-        _ok(lmhead_adamw_step(p, plan.tensors, plan.count, plan.table), "lmhead_adamw_step")
+        plan.step(p)

@@ -102,3 +102,44 @@ def test_what_is_no_number_is_refused(problems):
         with pytest.raises(TypeError):
             lm.preference_loss_forward(x, CU, num_pairs=bad)
     assert not problems
+
+
+class Marked:
+    """Stands for a tensor of a plan."""
+
+    def __init__(self):
+        self.on = []
+
+    def record_stream(self, stream):
+        self.on.append(stream)
+
+
+def test_a_plans_memory_is_marked_on_every_stream_that_steps(monkeypatch):
+    """Read by a kernel on another stream than its own, a block must not go back to
+    its own before: the plan may be dropped while the step is pending."""
+    now = dict(stream=0, capturing=False)
+    launched = []
+
+    def entry(p, tensors, count, table, stream=None):
+        launched.append(train._stream(stream))
+        return lm.LMHEAD_OK
+    monkeypatch.setattr(train, "lmhead_adamw_step", entry)
+    monkeypatch.setattr(train, "_stream", lambda s: now["stream"] if s is None else s)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now["stream"])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now["capturing"])
+    keep = [Marked(), Marked()]
+    plan = lm.AdamWPlan(torch.device("cuda", 0), (lm.lmhead_adamw_tensor * 2)(), keep)
+    plan.table = Marked()
+    all_ = keep + [plan.table]
+    for stream, marks in ((0, [0]), (0, [0]), (7, [0, 7]), (0, [0, 7]), (7, [0, 7])):
+        now["stream"] = stream
+        lm.adamw_step(plan, 1, 0.1)
+        assert [m.on for m in all_] == [marks] * 3 and launched[-1] == stream
+    # a capture only records its launch; the graph's owner keeps the plan. The stream's first eager step marks
+    now.update(stream=9, capturing=True)
+    lm.adamw_step(plan, 1, 0.1)
+    assert [m.on for m in all_] == [[0, 7]] * 3 and launched[-1] == 9
+    now["capturing"] = False
+    lm.adamw_step(plan, 1, 0.1)
+    assert [m.on for m in all_] == [[0, 7, 9]] * 3

@@ -321,14 +321,15 @@ def _check_tokens(logp, targets, cu_seqlens):
     return n, cu_seqlens.shape[0] - 1
 
 
-def _outputs(entry, p, nbytes, pointers, ws, floats, like):
-    """(workspace, fp32 [floats] of outputs). A workspace of no more than a tile's
-    size stands in the outputs' own allocation."""
-    if ws is None and 0 < nbytes <= 4096:
-        both = torch.empty(nbytes // 4 + floats, dtype=torch.float32, device=like.device)
-        return both, both[nbytes // 4:]
-    ws = _workspace(ws, nbytes, like.device, entry, p, pointers)
-    return ws, torch.empty(floats, dtype=torch.float32, device=like.device)
+# An output has memory of its own: views of one buffer would share its version, so
+# that work in place on one (a loss divided, statistics reduced over ranks) would
+# spoil the others for the backward, and one kept would keep all. new_empty of an fp32
+# input is the quickest way to one.
+
+def _scratch(ws, nbytes, like, entry, p, pointers):
+    if ws is None and nbytes > 0:
+        return like.new_empty(nbytes >> 2)
+    return _workspace(ws, nbytes, like.device, entry, p, pointers)
 
 
 def _real(x) -> float:
@@ -384,8 +385,8 @@ def policy_loss_forward(logp, advantage, old_logp=None, ref_logp=None, targets=N
     which; targets int32 [n], negative: the token does not count."""
     p, nbytes = _policy_problem(logp, advantage, old_logp, ref_logp, targets, cu_seqlens, clip_low, clip_high, dual_clip,
                                 kl_weight, kl_kind, reduction, num_valid, advantage_per_sequence)
-    ws, out = _outputs(lmhead_policy_loss_fwd, p, nbytes, 10, ws, 5 + max(p.sequences, 1), logp)
-    loss, stats, weights = out[0], out[1:5], out[5:]
+    ws = _scratch(ws, nbytes, logp, lmhead_policy_loss_fwd, p, 10)
+    loss, stats, weights = logp.new_empty(()), logp.new_empty(4), logp.new_empty(max(p.sequences, 1))
     _ok(lmhead_policy_loss_fwd(p, logp, old_logp, ref_logp, advantage, targets, cu_seqlens, loss, stats, weights, ws,
                                ws.numel() * ws.element_size()), "lmhead_policy_loss_fwd")
     return PolicyOutputs(loss, stats, weights)
@@ -467,8 +468,8 @@ def preference_loss_forward(logp, cu_seqlens, ref_logp=None, targets=None, kind:
         raise ValueError("kind must be 'sigmoid', 'hinge' or 'squared'")
     p, nbytes = _preference_sizes(n, pairs, operator.index(num_pairs), _real(beta), _real(margin),
                                   _real(label_smoothing), _PREFERENCE[kind], int(bool(average)))
-    ws, out = _outputs(lmhead_preference_loss_fwd, p, nbytes, 8, ws, 1 + 4 * pairs, logp)
-    loss, rewards, coef = out[0], out[1:1 + 2 * pairs], out[1 + 2 * pairs:]
+    ws = _scratch(ws, nbytes, logp, lmhead_preference_loss_fwd, p, 8)
+    loss, rewards, coef = logp.new_empty(()), logp.new_empty(2 * pairs), logp.new_empty(2 * pairs)
     _ok(lmhead_preference_loss_fwd(p, logp, ref_logp, targets, cu_seqlens, loss, rewards, coef, ws,
                                    ws.numel() * ws.element_size()), "lmhead_preference_loss_fwd")
     return PreferenceOutputs(loss, rewards, coef)

@@ -104,6 +104,44 @@ def test_what_is_no_number_is_refused(problems):
     assert not problems
 
 
+def divided(loss, other):
+    loss /= 4
+
+
+def added(loss, other):
+    loss += 1.0
+
+
+def reduced(loss, other):
+    other.mul_(2)
+
+
+def detached(loss, other):
+    loss.detach().mul_(0)
+
+
+@pytest.mark.parametrize("how,factor", [(divided, 0.25), (added, 1.0), (reduced, 1.0), (detached, 1.0)])
+@pytest.mark.parametrize("kind", ["policy", "preference"])
+def test_outputs_may_be_worked_on_in_place(problems, monkeypatch, kind, how, factor):
+    """Before the backward, as programs do for logs and for accumulated batches."""
+    grads = []
+    for name in ("lmhead_policy_loss_bwd", "lmhead_preference_loss_bwd"):
+        monkeypatch.setattr(train, name, lambda p, grad, *args: grads.append(float(grad)) or lm.LMHEAD_OK)
+    x = torch.zeros(4, requires_grad=True)
+    loss, other = lm.policy_loss(x, x.detach(), cu_seqlens=CU, advantage_per_sequence=False) if kind == "policy" else \
+        lm.preference_loss(x, CU)
+    how(loss, other)
+    loss.backward()
+    assert grads == [factor] and x.grad.shape == (4,)
+
+
+def test_outputs_keep_no_others_memory(problems):
+    x = torch.zeros(4)
+    for f in (lm.policy_loss_forward(x, x), lm.preference_loss_forward(x, CU)):
+        for t in f:
+            assert t._base is None and t.untyped_storage().nbytes() == 4 * t.numel()
+
+
 class Marked:
     """Stands for a tensor of a plan."""
 

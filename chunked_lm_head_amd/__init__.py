@@ -368,10 +368,10 @@ def ce_loss_forward(H, W, targets, chunk: int, reduction: str = "mean", num_vali
                 temperature=temperature, row_temperature=row_temperature)
     if ws is None:
         ws = workspace(p, entry, False, H.device)
-    loss = torch.empty(1, dtype=torch.float32, device=H.device)
+    loss = torch.empty((), dtype=torch.float32, device=H.device)   # no view: work in place on it is allowed
     lse = torch.empty(H.shape[0], dtype=torch.float32, device=H.device)
     _ok(lmhead_loss_fwd(p, entry, H, W, targets, loss, lse, ws, ws.numel()), "lmhead_loss_fwd")
-    return loss[0], lse, ws
+    return loss, lse, ws
 
 
 @_on_device_of(0)

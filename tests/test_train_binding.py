@@ -142,6 +142,21 @@ def test_outputs_keep_no_others_memory(problems):
             assert t._base is None and t.untyped_storage().nbytes() == 4 * t.numel()
 
 
+def test_the_cross_entropys_loss_may_be_worked_on_in_place(monkeypatch):
+    grads = []
+    monkeypatch.setattr(lm, "_check_inputs", lambda *a, **k: None)
+    monkeypatch.setattr(lm, "workspace", lambda *a: torch.empty(256, dtype=torch.uint8))
+    monkeypatch.setattr(lm, "lmhead_loss_fwd", lambda *a: lm.LMHEAD_OK)
+    monkeypatch.setattr(lm, "backward", lambda entry, H, W, targets, lse, grad, *a, **k:
+                        grads.append(grad.tolist()) or (torch.zeros_like(H), torch.zeros_like(W)))
+    H, W = torch.zeros(4, 64, requires_grad=True), torch.zeros(9, 64, requires_grad=True)
+    loss = lm.ChunkedLMHeadCE.apply(H, W, torch.zeros(4, dtype=torch.int32), 256)
+    assert loss.shape == ()
+    loss /= 4
+    loss.backward()
+    assert grads == [[0.25]]
+
+
 class Marked:
     """Stands for a tensor of a plan."""
 

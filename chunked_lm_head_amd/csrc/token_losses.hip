@@ -171,8 +171,10 @@ __device__ __forceinline__ Term policy_term(const PolicyArgs& a, float logp, flo
             o.kl = e.k;
             dk = -e.m;
         }
-        o.loss = __builtin_fmaf(a.kl_weight, o.kl, o.loss);
-        o.slope = __builtin_fmaf(a.kl_weight, dk, o.slope);
+        if (a.kl_weight != 0.0f) {   // without: a statistic alone, and an infinite one spoils nothing
+            o.loss = __builtin_fmaf(a.kl_weight, o.kl, o.loss);
+            o.slope = __builtin_fmaf(a.kl_weight, dk, o.slope);
+        }
     }
     return o;
 }

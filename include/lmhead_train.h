@@ -132,7 +132,8 @@ enum lmhead_reduction {
  *                    micro-batches of one mean); 0 gives loss and gradient 0.
  *   clip_low         in [0, 1]; clip_high >= 0; both finite.
  *   dual_clip        0 = off, else > 1 and finite.
- *   kl_weight        finite; needs ref_logp unless 0.
+ *   kl_weight        finite; needs ref_logp unless 0. With 0 ref_logp goes into
+ *                    the statistics alone.
  *   kl_kind          enum lmhead_kl_kind; reduction: enum lmhead_reduction.
  *   advantage_per_sequence  0: advantage [n]; 1: advantage [sequences] (needs
  *                    sequences).

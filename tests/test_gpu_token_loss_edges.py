@@ -33,3 +33,31 @@ def test_work_in_place_on_the_outputs(kind, n):
             loss.detach().zero_()
         grads.append(torch.autograd.grad(loss, x)[0])
     assert torch.equal(grads[1] * 4, grads[0]) and torch.equal(grads[2], grads[0]) and (grads[0] != 0).any()
+
+
+@pytest.mark.parametrize("n", [300, 3000, 20000])
+@pytest.mark.parametrize("reduction", ["mean", "sum", "sequence_mean"])
+def test_a_reference_without_weight_takes_no_part(n, reduction):
+    """A reference for the statistics alone, however far away: exp(ref - logp) passes
+    fp32's range from 89 on."""
+    rng, cu, targets, logp, old, ref_ = inputs(n, 6, "even", 2)
+    _, ok = ref.counted(n, targets, cu)
+    at = np.flatnonzero(ok)
+    args = [dev(v) for v in (logp, rng.standard_normal(n), old)]
+    t, cu_, one = dev(targets, torch.int32), dev(cu, torch.int32), torch.ones(1, **ONE)
+    f = lm.policy_loss_forward(*args, None, t, cu_, reduction=reduction)
+    want = lm.policy_loss_backward(one, f.weights, *args, None, t, cu_, reduction=reduction)
+    assert f.loss.isfinite()
+    for far in (logp + 100.0, np.full(n, np.inf), np.full(n, -np.inf), np.full(n, np.nan)):
+        r = ref_.copy()
+        r[at[::7]] = far[at[::7]]
+        for kind in ("k1", "k2", "k3"):
+            g = lm.policy_loss_forward(*args, dev(r), t, cu_, reduction=reduction, kl_kind=kind)
+            d = lm.policy_loss_backward(one, g.weights, *args, dev(r), t, cu_, reduction=reduction, kl_kind=kind)
+            assert torch.equal(g.loss, f.loss) and torch.equal(d, want) and torch.equal(g.stats[1:], f.stats[1:])
+    # a reference at hand still gives its statistic
+    g = lm.policy_loss_forward(*args, dev(ref_), t, cu_, reduction=reduction)
+    x = (logp - ref_)[ok]
+    k = np.expm1(-x) + x
+    # as in check_policy: a token's estimate is off by its terms' roundings
+    assert abs(float(g.stats[0]) - k.mean()) <= U * ((4 + 4 * np.abs(x) + 4 * np.exp(-x)).mean() + k.mean())

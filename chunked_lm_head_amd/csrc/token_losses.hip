@@ -138,7 +138,8 @@ __device__ __forceinline__ K3 k3_of(float x, float power) {
 
 __device__ __forceinline__ Term policy_term(const PolicyArgs& a, float logp, float old, float ref, float adv) {
     Term o;
-    const double gap = (double)logp - (double)old;
+    // without old log-probs r is 1, of an infinite logp too; NaN stays
+    const double gap = a.old_logp != nullptr || logp != logp ? (double)logp - (double)old : 0.0;
     const float d = (float)gap;
     o.ratio = expf(d);
     float rho;
@@ -240,8 +241,7 @@ struct PolicyTokens {
         return q < a.t.sequences ? q : -1;
     }
     __device__ __forceinline__ Term term(const PolicyArgs& a, int k, int64_t q) const {
-        return policy_term(a, logp[k], a.old_logp != nullptr ? old[k] : logp[k], ref[k],
-                           a.per_sequence ? a.advantage[q >= 0 ? q : 0] : adv[k]);
+        return policy_term(a, logp[k], old[k], ref[k], a.per_sequence ? a.advantage[q >= 0 ? q : 0] : adv[k]);
     }
 };
 

@@ -165,7 +165,8 @@ size_t lmhead_policy_loss_workspace_size(const lmhead_policy_problem* p);
  * gradient; the border is decided in 64 bits on d. loss = sum of w L, with w = 1
  * / count, 1, or 1 / (sequences * the sequence's count).
  *   logp      device, fp32 [n] (lmhead_logprob's).
- *   old_logp  device, fp32 [n], or NULL: logp itself (r = 1).
+ *   old_logp  device, fp32 [n], or NULL: logp itself (r = 1, of an infinite logp
+ *             too; NaN of NaN).
  *   ref_logp  device, fp32 [n], or NULL.
  *   loss      device, fp32 [1].
  *   stats     device, fp32 [4] or NULL: means over the counted tokens of the

@@ -61,3 +61,25 @@ def test_a_reference_without_weight_takes_no_part(n, reduction):
     k = np.expm1(-x) + x
     # as in check_policy: a token's estimate is off by its terms' roundings
     assert abs(float(g.stats[0]) - k.mean()) <= U * ((4 + 4 * np.abs(x) + 4 * np.exp(-x)).mean() + k.mean())
+
+
+@pytest.mark.parametrize("n", [5, 3000, 20000])
+def test_without_old_log_probs_a_ratio_is_one(n):
+    """Whatever the log-prob: an infinite one too, as a masked token's. NaN stays NaN."""
+    rng = np.random.default_rng(n)
+    logp, adv = f32(-rng.random(n)), f32(rng.standard_normal(n))
+    one = torch.ones(1, **ONE)
+    clean = lm.policy_loss_forward(dev(logp), dev(adv))
+    want = lm.policy_loss_backward(one, clean.weights, dev(logp), dev(adv))
+    assert clean.stats.tolist() == [0, 0, 1, 0]
+    for bad in (-np.inf, np.inf):
+        x = logp.copy()
+        x[::3] = bad
+        f = lm.policy_loss_forward(dev(x), dev(adv))
+        d = lm.policy_loss_backward(one, f.weights, dev(x), dev(adv))
+        assert all(torch.equal(a, b) for a, b in zip(f, clean)) and torch.equal(d, want)
+    x = logp.copy()
+    x[3] = np.nan
+    f = lm.policy_loss_forward(dev(x), dev(adv))
+    d = lm.policy_loss_backward(one, f.weights, dev(x), dev(adv))
+    assert f.loss.isnan() and d[3].isnan() and int(d.isnan().sum()) == 1

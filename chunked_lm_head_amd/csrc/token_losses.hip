@@ -421,7 +421,8 @@ __global__ __launch_bounds__(kTileThreads) void policy_bwd_kernel(PolicyArgs a, 
         if (i >= tile.t1) continue;
         const int64_t q = tokens.place(a, tile, k);
         const Term o = tokens.term(a, k, q);
-        dlogp[i] = q >= 0 ? g * (a.weights[q] * o.slope) : 0.0f;
+        const float w = q >= 0 ? a.weights[q] : 0.0f;   // 0 (a given count of 0) of an infinite slope too
+        dlogp[i] = w != 0.0f ? g * (w * o.slope) : 0.0f;
     }
 }
 

@@ -83,3 +83,19 @@ def test_without_old_log_probs_a_ratio_is_one(n):
     f = lm.policy_loss_forward(dev(x), dev(adv))
     d = lm.policy_loss_backward(one, f.weights, dev(x), dev(adv))
     assert f.loss.isnan() and d[3].isnan() and int(d.isnan().sum()) == 1
+
+
+@pytest.mark.parametrize("n", [5, 3000, 20000])
+@pytest.mark.parametrize("reduction", ["mean", "sequence_mean"])
+def test_a_given_count_of_zero_gives_zeros(n, reduction):
+    """Also where a token's own term is infinite: a ratio past fp32's range, an
+    estimate past it, a log-prob of -infinity or NaN."""
+    rng = np.random.default_rng(n)
+    logp, old, ref_ = f32(-rng.random(n)), f32(-rng.random(n)), f32(-rng.random(n))
+    adv = -np.abs(f32(rng.standard_normal(n))) - 0.1
+    old[0], ref_[1], logp[2], logp[3] = -200.0, 200.0, -np.inf, np.nan
+    args = [dev(v) for v in (logp, adv, old, ref_)]
+    kw = dict(kl_weight=0.1, reduction=reduction, num_valid=0)
+    f = lm.policy_loss_forward(*args, **kw)
+    d = lm.policy_loss_backward(torch.ones(1, **ONE), f.weights, *args, **kw)
+    assert float(f.loss) == 0 and (f.weights == 0).all() and (d == 0).all()

@@ -278,7 +278,8 @@ __device__ __forceinline__ void policy_tile(const PolicyArgs& a, Tile& tile, dou
 }
 
 // One sequence's part of a tile, from LDS, by one wave.
-__device__ __forceinline__ Part part_of(const Tokens& t, const Tile& tile, int64_t q, const float* kept,
+template <typename T>
+__device__ __forceinline__ Part part_of(const Tokens& t, const Tile& tile, int64_t q, const T* kept,
                                         const uint8_t* counts) {
     int64_t from = border(t, q), to = border(t, q + 1);
     from = from > tile.t0 ? from : tile.t0;
@@ -428,19 +429,20 @@ __global__ __launch_bounds__(kTileThreads) void policy_bwd_kernel(PolicyArgs a, 
 
 // --------------------------------------------------------------- preference
 //
-// The same tiles and slots; what a thread keeps is a difference. 512 pairs over 1 M
+// The same tiles and slots; what a thread keeps is a difference, in 64 bits as the
+// sums: in fp32 what is left of them between two answers could be its roundings. 512 pairs over 1 M
 // tokens: tiles 7.6 us (12 MB), pairs 6.2, backward 7 (8 MB); 4 pairs over 2500 tokens
 // in one launch 5.5, backward 4.5. Latency decides all of them.
 
 template <int THREADS, int EACH>
-__device__ __forceinline__ void preference_tile(const PreferenceArgs& a, const Tile& tile, float* kept, uint8_t* counts) {
+__device__ __forceinline__ void preference_tile(const PreferenceArgs& a, const Tile& tile, double* kept, uint8_t* counts) {
 #pragma unroll
     for (int k = 0; k < EACH; ++k) {
         const int64_t i = tile.t0 + k * THREADS + threadIdx.x;
-        float gain = 0.0f;
+        double gain = 0.0;
         bool valid = false;
         if (i < tile.t1) {
-            gain = a.logp[i] - (a.ref_logp != nullptr ? a.ref_logp[i] : 0.0f);
+            gain = (double)a.logp[i] - (a.ref_logp != nullptr ? (double)a.ref_logp[i] : 0.0);
             valid = a.t.targets == nullptr || a.t.targets[i] >= 0;
         }
         kept[k * THREADS + threadIdx.x] = gain;
@@ -487,7 +489,7 @@ __device__ __forceinline__ double pair_loss(const PreferenceArgs& a, int64_t pai
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void preference_whole_kernel(PreferenceArgs a) {
     __shared__ double red[THREADS / 64];
-    __shared__ float kept[THREADS * kWholeEach];
+    __shared__ double kept[THREADS * kWholeEach];
     __shared__ uint8_t counts[THREADS * kWholeEach];
     const Tile tile = tile_of<THREADS * kWholeEach>(a.t);
     preference_tile<THREADS, kWholeEach>(a, tile, kept, counts);
@@ -503,7 +505,7 @@ __global__ __launch_bounds__(THREADS) void preference_whole_kernel(PreferenceArg
 }
 
 __global__ __launch_bounds__(kTileThreads) void preference_tiles_kernel(PreferenceArgs a, Part* slots) {
-    __shared__ float kept[kTileTokens];
+    __shared__ double kept[kTileTokens];
     __shared__ uint8_t counts[kTileTokens];
     Tile tile = tile_of<kTileTokens>(a.t);
     preference_tile<kTileThreads, kTileEach>(a, tile, kept, counts);

@@ -99,3 +99,28 @@ def test_a_given_count_of_zero_gives_zeros(n, reduction):
     f = lm.policy_loss_forward(*args, **kw)
     d = lm.policy_loss_backward(torch.ones(1, **ONE), f.weights, *args, **kw)
     assert float(f.loss) == 0 and (f.weights == 0).all() and (d == 0).all()
+
+
+@pytest.mark.parametrize("length,pairs", [(100, 1), (1000, 1), (700, 3), (20000, 1), (1500, 40), (10, 1100)])
+def test_preference_differences_are_of_64_bits(length, pairs):
+    """Tokens whose logp - ref an fp32 difference would round to 1, on the chosen side
+    alone: what is lost there is all of h. Sums of `length` terms near 1 in 64 bits are
+    within length^2 2^-53 of the true ones, and so is h by beta; then one rounding."""
+    step = 2.0 ** -24
+    logp = np.concatenate([np.full(pairs * length, -1.1 * step), np.zeros(pairs * length)])
+    ref_ = np.concatenate([np.full(pairs * length, -1.0 - 2 * step), np.full(pairs * length, -1.0)])
+    logp, ref_ = f32(logp), f32(ref_)
+    cu = np.arange(2 * pairs + 1) * length
+    beta = 0.5 / (length * 0.9 * step)   # h near 1/2
+    assert (np.float32(logp) - np.float32(ref_) == 1).all()
+    want = ref.preference(logp, cu, ref_, kind="hinge", beta=beta)
+    args = (dev(logp), dev(cu, torch.int32), dev(ref_))
+    f = lm.preference_loss_forward(*args, kind="hinge", beta=beta)
+    assert 0.4 < want[0] < 0.6
+    assert abs(float(f.loss) - want[0]) <= 2 * beta * length ** 2 * 2.0 ** -53 + U
+    want = ref.preference(logp, cu, ref_, beta=beta)
+    f = lm.preference_loss_forward(*args, beta=beta)
+    got = lm.preference_loss_backward(torch.ones(1, **ONE), f.coef, len(logp), args[1]).double().cpu().numpy()
+    # the slope moves by at most h's error / 4, then two roundings
+    off = beta / pairs * (0.25 * 2 * beta * length ** 2 * 2.0 ** -53) + 2 * U * np.abs(want[2])
+    assert (np.abs(got - want[2]) <= off).all()

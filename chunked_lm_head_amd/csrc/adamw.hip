@@ -117,11 +117,12 @@ __device__ __forceinline__ uint32_t scramble(uint32_t x) {
 
 // |y| plus a random part of its code's step (20 bits of the fp32 value), cut to
 // the code below. Below 2^-6 the codes' step is that of 2^-6 .. 2^-5, so the
-// value is moved there and back.
+// value is moved there and back. NaN stays: bits added to a fraction of ones would
+// carry over into its sign and leave a zero.
 __device__ __forceinline__ float cut_at_random(float y, uint32_t random20) {
     const float mag = fabsf(y), base = mag < 0x1p-6f ? 0x1p-6f : 0.0f;
     const uint32_t bits = (__builtin_bit_cast(uint32_t, mag + base) + random20) & 0xfff00000u;
-    return __builtin_copysignf(__builtin_bit_cast(float, bits) - base, y);
+    return y == y ? __builtin_copysignf(__builtin_bit_cast(float, bits) - base, y) : y;
 }
 
 // e4m3 of eight quotients by the block's scale, the quotients as a division

@@ -83,14 +83,24 @@ __device__ __forceinline__ float each_rounded(float a, float x, float b, float y
     return p + q;
 }
 
-// The root rounded to nearest (but for ties of the last step, within 2^-20 of one):
-// one Newton step with its remainder from the instruction's reciprocal root.
-// Below 2^-126: 0.
-__device__ __forceinline__ float rounded_root(float x) {
-    const float y = __builtin_amdgcn_rsqf(x), s = x * y;
-    const float r = __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * y, s);
-    const bool normal = x >= 0x1p-126f && x <= 3.402823466e38f;
-    return normal ? r : x < 0x1p-126f ? 0.0f : x;   // infinity and NaN are their own
+// The root instructions take a value below 2^-126 for 0, which with a small eps
+// makes a vanishing gradient's step large, and below 2^-100 the remainder of a
+// rounded root loses bits: so small values a power of two larger, and back.
+template <bool ROUNDED>
+__device__ __forceinline__ float root_of(float x) {
+    const bool small = x < 0x1p-64f;
+    const float z = small ? x * 0x1p64f : x;
+    float r;
+    if (ROUNDED) {
+        // to nearest (but for ties of the last step, within 2^-20 of one): one Newton
+        // step with its remainder from the instruction's reciprocal root
+        const float y = __builtin_amdgcn_rsqf(z), s = z * y;
+        r = __builtin_fmaf(__builtin_fmaf(-s, s, z), 0.5f * y, s);
+        r = z > 0.0f && z <= 3.402823466e38f ? r : z;   // zero, infinity and NaN are their own
+    } else {
+        r = __builtin_amdgcn_sqrtf(z);
+    }
+    return small ? r * 0x1p-32f : r;
 }
 
 // Scale of a block of 8-bit states: its largest magnitude by 448.
@@ -212,9 +222,9 @@ __device__ __forceinline__ void update(const AdamWTensor& t, const Step& k, int6
                                 : __builtin_fmaf(k.rest2 * gc, gc, k.beta2 * v[j].v[c]);
             // the instructions' own root and reciprocal, each within 2^-23: the
             // library's correctly rounded ones would double the arithmetic. A root
-            // that becomes 8 bits is rounded_root's: 1079 us for 622 M parameters, with the
-            // instruction's 1038, with the library's 1196.
-            const float rc = S8 ? rounded_root(vc) : __builtin_amdgcn_sqrtf(vc);
+            // that becomes 8 bits is rounded, 41 of the 1097 us of 622 M parameters; the
+            // library's would take 158.
+            const float rc = root_of<S8>(vc);
             const float step = mc * __builtin_amdgcn_rcpf(__builtin_fmaf(rc, k.root_scale, k.eps));
             p[j].v[c] = __builtin_fmaf(-k.step_size, step, p[j].v[c] * k.keep);
             m[j].v[c] = mc;

@@ -321,7 +321,6 @@ typedef struct lmhead_adamw {
  * fp32, and every operation on the way to a code is rounded by itself, so that
  * elementwise fp32 programs get the same codes), except that a sqrt(v') > 0 becomes
  * no zero (at least 2^-9 of its scale): a vanishing denominator would let m' loose.
- * The root of a v' below 2^-126 is zero.
  * States of zeros start (any finite scales).
  * Stochastic: with y = value / scale and u the upper 16 of 20 random bits, as a
  * fraction, |y| + u step(y) is cut to the code below, step(y) being the distance

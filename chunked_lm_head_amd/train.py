@@ -551,12 +551,15 @@ def adamw_state(param, dtype=torch.float32) -> AdamWState:
 class AdamWPlan:
     """The tensors of a step, checked and laid out once (adamw_plan). It keeps
     the storages that the tensors had then: a parameter or gradient that is given
-    another storage needs another plan. It may be dropped while steps are still
+    another storage needs another plan. Where a gradient was its parameter's own
+    .grad then, a step is refused once it no longer is (after zero_grad() without
+    set_to_none=False, for instance): the plan still holds the old one. It may be dropped while steps are still
     running, on any streams; but a graph that holds a step reads the plan's
     memory: keep the plan as long as the graph."""
 
-    def __init__(self, device, tensors, keep):
+    def __init__(self, device, tensors, keep, own=()):
         self.device, self.tensors, self.count, self.keep = device, tensors, len(tensors), keep
+        self.own = list(own)           # (parameter, its own .grad)
         self.streams = set()   # that its memory is marked as in use on
         self.table = None
         if self.count > 48:   # more than a launch takes as an argument
@@ -571,6 +574,11 @@ class AdamWPlan:
     def step(self, p):
         """One launch of the plan's tensors on the current stream of its device,
         which is the current one."""
+        for param, grad in self.own:
+            if param.grad is not grad:
+                at = [a is param for a, _ in self.own].index(True)
+                raise ValueError(f"the .grad of parameter {at} of those planned with theirs is another tensor now: "
+                                 "keep gradients in place (zero_grad(set_to_none=False)) or make another plan")
         stream = _stream(None)
         if stream not in self.streams and not torch.cuda.is_current_stream_capturing():
             # The allocator hands a freed block at once to the stream that it was
@@ -606,7 +614,7 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     if len(params) == 0:
         raise ValueError("a plan needs a parameter")
     table = (lmhead_adamw_tensor * len(params))()
-    dev, keep, spans = None, [], []
+    dev, keep, spans, own = None, [], [], []
     for i, (p, g, s, c) in enumerate(zip(params, grads, states, copies)):
         m, v, ms, vs = s
         shape = p.shape if isinstance(p, torch.Tensor) else ()
@@ -635,11 +643,13 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
             keep.append(t.detach())
             if t.numel() > 0:
                 spans.append((start, start + t.numel() * t.element_size()))
+        if p.is_leaf and p.grad is g:
+            own.append((p, g))
         table[i] = (*at, numel, _DTYPES[p.dtype], _DTYPES[g.dtype], _WEIGHT_DTYPES[m.dtype], 0)
     spans.sort()
     if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
         raise ValueError("two tensors of the plan share memory")
-    return AdamWPlan(dev, table, keep)
+    return AdamWPlan(dev, table, keep, own)
 
 
 def adamw_step(plan: AdamWPlan, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,

@@ -196,3 +196,48 @@ def test_a_plans_memory_is_marked_on_every_stream_that_steps(monkeypatch):
     now["capturing"] = False
     lm.adamw_step(plan, 1, 0.1)
     assert [m.on for m in all_] == [[0, 7, 9]] * 3
+
+
+@pytest.fixture
+def host_plan(monkeypatch):
+    """adamw_plan of CPU tensors, its steps counted instead of launched."""
+    steps = []
+    monkeypatch.setattr(train, "_check_of", lambda *a: None)
+    monkeypatch.setattr(train, "lmhead_adamw_step", lambda *a: steps.append(1) or lm.LMHEAD_OK)
+    monkeypatch.setattr(train, "_stream", lambda s: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+
+    def make(*args):
+        plan = lm.adamw_plan(*args)
+        plan.device = torch.device("cuda", 0)
+        return plan
+    make.steps = steps
+    return make
+
+
+def leaf(n=4):
+    return torch.ones(n, requires_grad=True)
+
+
+def test_a_replaced_gradient_is_refused(host_plan):
+    a, b = leaf(), leaf()
+    acc = torch.zeros(4)
+    (a.sum() + b.sum()).backward()
+    plan = host_plan([a, b], [acc, b.grad], [lm.adamw_state(a), lm.adamw_state(b)])   # a's is an accumulator elsewhere
+    opt = torch.optim.SGD([a, b], lr=0.1)
+    lm.adamw_step(plan, 1, 0.1)
+    opt.zero_grad(set_to_none=False)
+    (2 * b).sum().backward()
+    a.grad = None
+    lm.adamw_step(plan, 2, 0.1)
+    assert len(host_plan.steps) == 2
+    opt.zero_grad()
+    with pytest.raises(ValueError, match="set_to_none"):
+        lm.adamw_step(plan, 3, 0.1)
+    b.sum().backward()
+    with pytest.raises(ValueError, match="set_to_none"):
+        lm.adamw_step(plan, 3, 0.1)
+    assert len(host_plan.steps) == 2
+    lm.adamw_step(host_plan([b], [b.grad], [lm.adamw_state(b)]), 3, 0.1)
+    assert len(host_plan.steps) == 3

@@ -557,9 +557,10 @@ class AdamWPlan:
     running, on any streams; but a graph that holds a step reads the plan's
     memory: keep the plan as long as the graph."""
 
-    def __init__(self, device, tensors, keep, own=()):
+    def __init__(self, device, tensors, keep, own=(), watched=()):
         self.device, self.tensors, self.count, self.keep = device, tensors, len(tensors), keep
         self.own = list(own)           # (parameter, its own .grad)
+        self.watched = list(watched)   # written tensors that autograd may have saved
         self.streams = set()   # that its memory is marked as in use on
         self.table = None
         if self.count > 48:   # more than a launch takes as an argument
@@ -592,6 +593,8 @@ class AdamWPlan:
                 self.table.record_stream(current)
             self.streams.add(stream)
         _ok(lmhead_adamw_step(p, self.tensors, self.count, self.table, stream), "lmhead_adamw_step")
+        if self.watched:
+            torch.autograd.graph.increment_version(self.watched)
 
 
 def _check_of(i, name, t, dtypes, shape, device):
@@ -614,7 +617,7 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     if len(params) == 0:
         raise ValueError("a plan needs a parameter")
     table = (lmhead_adamw_tensor * len(params))()
-    dev, keep, spans, own = None, [], [], []
+    dev, keep, spans, own, watched = None, [], [], [], []
     for i, (p, g, s, c) in enumerate(zip(params, grads, states, copies)):
         m, v, ms, vs = s
         shape = p.shape if isinstance(p, torch.Tensor) else ()
@@ -645,18 +648,21 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
                 spans.append((start, start + t.numel() * t.element_size()))
         if p.is_leaf and p.grad is g:
             own.append((p, g))
+        watched += [t for t in (p, c) if t is not None and t.requires_grad]
         table[i] = (*at, numel, _DTYPES[p.dtype], _DTYPES[g.dtype], _WEIGHT_DTYPES[m.dtype], 0)
     spans.sort()
     if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
         raise ValueError("two tensors of the plan share memory")
-    return AdamWPlan(dev, table, keep, own)
+    return AdamWPlan(dev, table, keep, own, watched)
 
 
 def adamw_step(plan: AdamWPlan, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                weight_decay: float = 0.0, grad_scale: Optional[torch.Tensor] = None,
                seed: Optional[int] = None) -> None:
-    """One AdamW step of the plan's tensors, in place (autograd is not told: step
-    after the backward passes that read them); see lmhead_adamw_step.
+    """One AdamW step of the plan's tensors, in place; see lmhead_adamw_step. A
+    backward pass that saved a parameter (or copy) given to the plan as a tensor that
+    requires gradients raises after the step, as after any work in place; of others
+    (W.data, or at a graph's replays) autograd learns nothing: step after it.
     step: 1 for the first, or an int32 device tensor of one element (read at
     each replay of a captured step); lr: a number or an fp32 device tensor of one;
     grad_scale: an fp32 device tensor of one that multiplies the gradients. seed:

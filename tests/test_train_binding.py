@@ -241,3 +241,20 @@ def test_a_replaced_gradient_is_refused(host_plan):
     assert len(host_plan.steps) == 2
     lm.adamw_step(host_plan([b], [b.grad], [lm.adamw_state(b)]), 3, 0.1)
     assert len(host_plan.steps) == 3
+
+
+def test_a_backward_that_saved_a_parameter_raises_after_the_step(host_plan):
+    w, master, frozen = leaf(), torch.ones(4), torch.ones(4)
+    copy = torch.ones(4, dtype=torch.bfloat16, requires_grad=True)
+    plan = host_plan([w, master, frozen], [torch.zeros(4) for _ in range(3)],
+                     [lm.adamw_state(t) for t in (w, master, frozen)], [None, copy, None])
+    for t in (w, copy):
+        y = (t * t).sum()
+        lm.adamw_step(plan, 1, 0.1)
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            y.backward()
+        y = (t * t).sum()
+        y.backward()
+    before = frozen._version
+    lm.adamw_step(plan, 2, 0.1)
+    assert frozen._version == before

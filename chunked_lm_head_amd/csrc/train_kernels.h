@@ -90,8 +90,8 @@ constexpr uint32_t kAdamWParamF32 = 1, kAdamWGradF32 = 2, kAdamWState8 = 4, kAda
 constexpr int kAdamWPlace = 4;
 constexpr int kAdamWTensors = 48;   // per launch where the table travels as a kernel argument
 struct AdamWScalars {
-    float beta1, rest1, beta2, rest2, eps, decay;   // decay: weight_decay (lr is applied on the device)
-    float lr, step_size, root_scale, keep;          // of the host's step and lr
+    float beta1, rest1, beta2, rest2, eps;
+    float step_size, root_scale, keep;   // of the host's step and lr
     double log_beta1, log_beta2, weight_decay;
     const int32_t* step;
     const float* device_lr;

@@ -30,12 +30,16 @@ namespace {
 
 // A row is taken by 8 .. 64 lanes of a wave (all that its vectors of 8 can
 // use), four vectors per lane in flight; wider rows in segments (grid y). 16,384
-// rows of 4096 bf16: 37.7 us, eight vectors 41.5, two 45.2. STREAM: the output
-// past the caches, for outputs that they would not hold until the next
-// operator: 28.5 us there, the same 82 us with the norm behind it; 12,288 rows
-// with the norm 63 us, through the caches 60; 4096 rows 25.4 and 24.4.
+// rows of 4096 bf16, through the caches: 37.7 us, eight vectors 41.5, two 45.2.
+// STREAM: the output past the caches, from twice the eight L2s' 32 MB on. Rows of
+// 4096 and 2048 bf16, common and uniform ids, with the norm behind them, through the
+// caches / past them: 32 MB of output 25.1 / 26.6 and 26.3 / 28.1 us, 64 MB 42.0 /
+// 42.5, 50.3 / 49.1, 40.2 / 41.5 and 49.1 / 47.4, 128 MB 86 / 89, 105 / 104, 86 / 91 and
+// 105 / 99, 192 MB 131 / 130, 153 / 148, 140 / 137 and 149 / 147, 512 MB 353 / 340 and 383 / 375.
+// The lookup alone gains at every size: 64 MB 18.5 / 15.8, 128 MB 35.3 / 30.7, 512 MB
+// 168 / 107.
 constexpr int kVectors = 4;
-constexpr int64_t kStreamBytes = int64_t(128) << 20;
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 template <int TYPE, bool OUT32, bool STREAM>
 __global__ __launch_bounds__(256) void embedding_kernel(EmbedArgs a, int log_lanes) {

@@ -30,8 +30,11 @@ constexpr int kTileThreads = 256, kTileEach = 4;     // tokens per thread
 constexpr int64_t kTileTokens = kTileThreads * kTileEach;
 // Forward and backward of the policy loss with sequence means, in a graph. Up to
 // 512 tokens by 256 threads: 11.3 us, by 1024 12.9 (1024 tokens 18.8 and 17.5).
-// One launch for up to 4096 tokens in up to 64 sequences: 22.0 us, as tiles 23.4
-// (8192 tokens 27.5 and 22.9; 128 sequences 35.2 and 32.9).
+// One launch for up to 4096 tokens in up to 64 sequences: 30.2 us, as tiles 31.8 (128
+// sequences 36.3 and 33.9; 4096 tokens in 8 sequences 21.1 and 23.4). The preference
+// loss: 512 tokens 8.1 us by 256 threads and by 1024 (1024 tokens in 64 sequences 25.1
+// and 17.5); 4096 tokens in 64 sequences 18.0 us in one launch, as tiles 21.4 (128
+// sequences 26.6 and 23.3).
 constexpr int kFewThreads = 256, kWholeThreads = 1024, kWholeEach = 4;
 constexpr int64_t kFewTokens = 512, kWholeTokens = kWholeThreads * kWholeEach, kWholeSequences = 64;
 

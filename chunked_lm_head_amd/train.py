@@ -553,9 +553,9 @@ class AdamWPlan:
     the storages that the tensors had then: a parameter or gradient that is given
     another storage needs another plan. Where a gradient was its parameter's own
     .grad then, a step is refused once it no longer is (after zero_grad() without
-    set_to_none=False, for instance): the plan still holds the old one. It may be dropped while steps are still
-    running, on any streams; but a graph that holds a step reads the plan's
-    memory: keep the plan as long as the graph."""
+    set_to_none=False, for instance): the plan still holds the old one. It may be
+    dropped while steps are still running, on any streams; but a graph that holds a
+    step reads the plan's memory: keep the plan as long as the graph."""
 
     def __init__(self, device, tensors, keep, own=(), watched=()):
         self.device, self.tensors, self.count, self.keep = device, tensors, len(tensors), keep
@@ -572,6 +572,25 @@ class AdamWPlan:
             self.table = table.to(device)
             torch.cuda.synchronize(device)   # steps may run on any stream
 
+    def mark(self):
+        """Mark the plan's memory as in use on the current stream of its device, which
+        is the current one; its handle.
+
+        The allocator hands a freed block at once to the stream that it was allocated
+        on. Marked, it waits for this one first: else a plan dropped while a step
+        is pending would leave the kernel another tensor's bytes for addresses. Once per
+        stream: a mark holds until the block is freed. Not in a capture, whose owner
+        keeps the plan."""
+        stream = _stream(None)
+        if stream not in self.streams and not torch.cuda.is_current_stream_capturing():
+            current = torch.cuda.current_stream()
+            for t in self.keep:
+                t.record_stream(current)
+            if self.table is not None:
+                self.table.record_stream(current)
+            self.streams.add(stream)
+        return stream
+
     def step(self, p):
         """One launch of the plan's tensors on the current stream of its device,
         which is the current one."""
@@ -580,26 +599,14 @@ class AdamWPlan:
                 at = [a is param for a, _ in self.own].index(True)
                 raise ValueError(f"the .grad of parameter {at} of those planned with theirs is another tensor now: "
                                  "keep gradients in place (zero_grad(set_to_none=False)) or make another plan")
-        stream = _stream(None)
-        if stream not in self.streams and not torch.cuda.is_current_stream_capturing():
-            # The allocator hands a freed block at once to the stream that it was
-            # allocated on. Marked, it waits for this one first: else a plan dropped
-            # here would leave the kernel another tensor's bytes for addresses. Once
-            # per stream: a mark holds until the block is freed.
-            current = torch.cuda.current_stream()
-            for t in self.keep:
-                t.record_stream(current)
-            if self.table is not None:
-                self.table.record_stream(current)
-            self.streams.add(stream)
-        _ok(lmhead_adamw_step(p, self.tensors, self.count, self.table, stream), "lmhead_adamw_step")
+        _ok(lmhead_adamw_step(p, self.tensors, self.count, self.table, self.mark()), "lmhead_adamw_step")
         if self.watched:
             torch.autograd.graph.increment_version(self.watched)
 
 
 def _check_of(i, name, t, dtypes, shape, device):
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous() and \
-            (device is None or t.device == device):
+            (device is None or t.get_device() == device.index):
         return
     _check_gpu(f"{name} of tensor {i}", t, dtypes, shape, device)
 
@@ -643,9 +650,10 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
                 continue
             start = t.data_ptr()
             at.append(start)
-            keep.append(t.detach())
-            if t.numel() > 0:
-                spans.append((start, start + t.numel() * t.element_size()))
+            keep.append(t.data)   # its storage now, whatever t is given later
+            size = t.nbytes
+            if size > 0:
+                spans.append((start, start + size))
         if p.is_leaf and p.grad is g:
             own.append((p, g))
         watched += [t for t in (p, c) if t is not None and t.requires_grad]
@@ -653,7 +661,10 @@ def adamw_plan(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     spans.sort()
     if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
         raise ValueError("two tensors of the plan share memory")
-    return AdamWPlan(dev, table, keep, own, watched)
+    plan = AdamWPlan(dev, table, keep, own, watched)
+    if dev.index == torch.cuda.current_device():
+        plan.mark()   # here rather than in the first step: this stream's most likely
+    return plan
 
 
 def adamw_step(plan: AdamWPlan, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,

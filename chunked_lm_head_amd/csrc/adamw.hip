@@ -13,9 +13,10 @@
 // lanes hold a block of 128 and its maximum is four shuffles. Tensors share a
 // launch; a workgroup finds its tensor by its chunk's number, in a table of up to
 // 48 that travels as a kernel argument, or in the caller's table on the device.
-// bf16 parameters: 525 M with fp32 gradients and states 2300 us (5.5 TB/s), 622 M
-// with bf16 gradients and 8-bit states 1079 us (5.8 TB/s; a large copy reaches
-// 4.7); 129 tensors of 4096 4.8 us, with the kernel argument's three launches 14.3.
+// bf16 parameters: 525 M with fp32 gradients and states 2303 us (5.5 TB/s), 622 M
+// with bf16 gradients and 8-bit states 1097 us (5.7 TB/s; a large copy reaches
+// 4.7), at random rounding 1310 (a hash per element); 129 tensors of 4096 in one
+// kernel of 4.8 us, by kernel arguments in three of 5.3, 5.3 and 4.7.
 #include "host_util.h"
 #include "train_kernels.h"
 #include "vec8.h"

@@ -17,7 +17,8 @@
 //   3. join: the pieces of the longer runs, in order.
 // 16,384 tokens of Zipf ids, 152 k x 4096 bf16 written whole: 190 us (1.25 GB, 6.5
 // TB/s), 68 (while the zeros drain to memory) and 6.5. 4096 tokens added to fp32: 9.5,
-// 16 (78 MB, 4.8 TB/s) and 6.5.
+// 16 (78 MB, 4.8 TB/s) and 6.5; to bf16 9.4, 13 and 6.5. 64 tokens: written whole 190,
+// 8 and 4.5, added 6.6, 7 and 4.4 (latency; 16 in a graph).
 #include "host_util.h"
 #include "train_kernels.h"
 #include "vec8.h"

@@ -14,7 +14,8 @@
 // order (over more sequences or tiles than a workgroup can take at once, a
 // third). A tile's tokens are loaded before its sequences are looked up, and all
 // its sums cross the workgroup behind one barrier. 1 M tokens: tiles 12.4 us, their
-// sums 7, backward 6.4; the bytes alone would take 10 us of the 26.
+// sums 7, backward 7; the bytes alone would take 10 us of the 26. With sequence means
+// 16, 8.5 and 8.5 (30 in a graph).
 //
 // Sequences and tiles. A tile's partial of sequence s stands at slot tile + s:
 // along the packed tokens either the tile or the sequence moves on, so no two
@@ -140,6 +141,9 @@ __device__ __forceinline__ K3 k3_of(float x, float power) {
 }
 
 __device__ __forceinline__ Term policy_term(const PolicyArgs& a, float logp, float old, float ref, float adv) {
+    // The terms are fp32, as the outputs; their sums are of 64 bits. Rounding the gap
+    // to fp32 moves r by |d| 2^-24 of it, and the estimates outside their series are
+    // off by a few 2^-24 of their largest term.
     Term o;
     // without old log-probs r is 1, of an infinite logp too; NaN stays
     const double gap = a.old_logp != nullptr || logp != logp ? (double)logp - (double)old : 0.0;
@@ -433,9 +437,9 @@ __global__ __launch_bounds__(kTileThreads) void policy_bwd_kernel(PolicyArgs a, 
 // --------------------------------------------------------------- preference
 //
 // The same tiles and slots; what a thread keeps is a difference, in 64 bits as the
-// sums: in fp32 what is left of them between two answers could be its roundings. 512 pairs over 1 M
-// tokens: tiles 7.6 us (12 MB), pairs 6.2, backward 7 (8 MB); 4 pairs over 2500 tokens
-// in one launch 5.5, backward 4.5. Latency decides all of them.
+// sums: in fp32 what is left of them between two answers could be its roundings. 512
+// pairs over 1 M tokens: tiles 9 us (12 MB; 7.6 with fp32 differences), pairs 6.0, backward 7
+// (8 MB); 4 pairs over 2500 tokens in one launch 5.7, backward 4.5. Latency decides all of them.
 
 template <int THREADS, int EACH>
 __device__ __forceinline__ void preference_tile(const PreferenceArgs& a, const Tile& tile, double* kept, uint8_t* counts) {

@@ -130,6 +130,7 @@ enum lmhead_reduction {
  *   num_valid        -1: the tokens that count (sequence mean: the sequences);
  *                    >= 0: this number in its place ("given counts", for
  *                    micro-batches of one mean); 0 gives loss and gradient 0.
+ *                    A sum does not use it.
  *   clip_low         in [0, 1]; clip_high >= 0; both finite.
  *   dual_clip        0 = off, else > 1 and finite.
  *   kl_weight        finite; needs ref_logp unless 0. With 0 ref_logp goes into

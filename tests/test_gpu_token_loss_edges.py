@@ -6,7 +6,7 @@ import torch
 
 import chunked_lm_head_amd as lm
 import train_ref as ref
-from test_gpu_token_losses import check_policy, dev, f32, inputs
+from test_gpu_token_losses import dev, f32, inputs
 
 pytestmark = pytest.mark.gpu
 

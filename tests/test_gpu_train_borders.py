@@ -126,3 +126,23 @@ def test_the_longest_chain_of_additions():
         tol = (64 + 33 + 8) * U * part.abs().sum(0)
         assert ((got[v].double() - part.sum(0)).abs() <= tol).all()
     assert (got.abs().sum(1) != 0).sum() == 2
+
+
+@pytest.mark.parametrize("weight", [BF, F32, torch.float8_e4m3fn])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("less", [0, 1])
+def test_rows_on_both_sides_of_the_caches(weight, out, less):
+    """64 MB of output: past the caches from there on. Rows times a power of two: the very bits."""
+    hidden, vocab = 2048, 3000
+    n = (64 << 20) // (hidden * (2 if out == BF else 4)) - less
+    g = te.gen(n)
+    w, scale = te.randn(g, vocab, hidden, dtype=F32 if weight == F32 else BF), None
+    ids = torch.randint(-200, vocab, (n,), generator=g, device="cuda", dtype=torch.int32)
+    at = ids.clamp(min=0).long()
+    if weight == torch.float8_e4m3fn:
+        w, scale = lm.quantize_fp8(w, 128)
+        rows = w.float()[at] * scale[at // 128].repeat_interleave(128, 1)
+    else:
+        rows = w[at].float()
+    want = torch.where((ids >= 0)[:, None], rows * 4.0, 0.0).to(out)
+    assert torch.equal(lm.embedding_forward(ids, w, 4.0, scale, out), want)
